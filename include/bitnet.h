@@ -352,6 +352,190 @@ bitnet_status bitnet_linear_b3(const uint16_t* x, int64_t M, int64_t K, const ui
                                bitnet_out_dtype out_dtype, void* stream);
 
 /*
+ * Linear layers with 4-bit weights and group scales, for the layers of a model that are kept
+ * wider than ternary ("BitNet 深度实战" on mixed precision keeps the output table and the down
+ * projection at more bits). x is used as it is (bf16, no activation quantiser):
+ *   y[m, n] = sum_g scale[n, g] * sum_{k in group g} x[m, k] * t[n, k],  t in [-8, 7].
+ *
+ * Format. A row is cut into blocks of 128 weights of 64 bytes each, 16 little-endian 32-bit
+ * words; word 4c + j (c, j = 0..3) holds the block's weights 32j + 8c + i, i = 0..7, as code
+ * t + 8: weight i in bits 2i .. 2i + 3 for even i and in bits 2i + 14 .. 2i + 17 for odd i (the
+ * even weights in the low half-word's nibbles, the odd ones in the high half-word's, so one mask
+ * yields a pair of neighbours). Weights past K have code 8 (t = 0). A row takes
+ * bitnet_w4_row_bytes(K) = 64 * ceil(K / 128) bytes. Scales are bf16, (N, ceil(K / group)),
+ * group = 32, 64 or 128 (BITNET_ERR_UNSUPPORTED otherwise); the last group may be cut by K.
+ *
+ * bitnet_pack_w4 — W (N, K) fp32 -> packed (N, bitnet_w4_row_bytes(K)) uint8 and scales. Per
+ *   group: s = bf16(max(max |W|, 1e-5) / 7), t = clamp(rint(W / s), -8, 7) (binary32 divides,
+ *   ties to even; the clamp to -8 never acts).
+ * bitnet_linear_w4 — the forward for any M >= 1 in tiles of up to 32 tokens per pass over the
+ *   weights: made for decode, where the time is that of reading the weights once; a prompt of M
+ *   tokens reads them ceil(M / 32) times. Codes are exact in bf16; products and sums run in
+ *   binary32 (sums within a group, times the scale, added over the groups in a fixed order, so
+ *   results are the same on every run), and y is rounded once at the end.
+ *   A row of x that holds an Inf or NaN gives unspecified values in that row of y only.
+ * x, packed, W and y 16-byte aligned, scales 2-byte aligned. No workspace. Asynchronous on
+ * `stream`; argument errors as for the other calls.
+ */
+int64_t bitnet_w4_row_bytes(int64_t K);
+bitnet_status bitnet_pack_w4(const float* W, int64_t N, int64_t K, int32_t group,
+                             uint8_t* packed, uint16_t* scales, void* stream);
+bitnet_status bitnet_linear_w4(const uint16_t* x, int64_t M, int64_t K, const uint8_t* packed,
+                               const uint16_t* scales, int32_t group, int64_t N, void* y,
+                               bitnet_out_dtype out_dtype, void* stream);
+
+/*
+ * Paged key/value cache of a decode step: what stands between bitnet_linear_batch of q/k/v and
+ * bitnet_linear of the output projection ("BitNet 深度实战" section 3.2, BitLlamaAttention).
+ * All memory is the caller's; the calls below are asynchronous on `stream`, keep their
+ * bookkeeping on the device, and so can be captured into a CUDA graph.
+ *
+ * bitnet_cache describes the page tables shared by all layers of a model, bitnet_cache_layer the
+ * pools of one layer: K and V pages of shape (num_pages, kv_heads, page_size, head_dim), bf16
+ * bits or int8 with one fp32 scale per token and head, (num_pages, kv_heads, page_size), that
+ * stands for value = q / scale (the activation quantiser's convention). Sequence slot s holds
+ * lens[s] tokens, token j of it in page table[s * max_pages + j / page_size] at offset
+ * j % page_size; entries past its ceil(lens[s] / page_size) pages are not read. refs[p] counts
+ * the slots that hold page p; the page is free while it is 0. A new cache has lens and refs 0.
+ *
+ * Device lists of slots (`seqs`, `src`, `dst`, int32) may be padded: an entry with a negative
+ * slot is skipped. Every list must name a slot at most once where the call changes that slot.
+ *
+ * What the host cannot check is checked on the device and reported in the caller's word
+ * cache->error, into which the calls OR BITNET_CACHE_ERR_* bits (they never clear it):
+ * bitnet_cache_fork, _extend and _free then change nothing; bitnet_cache_append and
+ * bitnet_paged_attention skip the tokens concerned and handle the others; bitnet_cache_copy skips
+ * the pairs concerned.
+ */
+typedef enum {
+    BITNET_CACHE_BF16 = 0, /* pools hold bf16 bits                                         */
+    BITNET_CACHE_I8 = 1    /* pools hold int8 with a scale per token and head              */
+} bitnet_cache_dtype;
+
+#define BITNET_CACHE_ERR_SEQ (1 << 0)  /* a slot out of range, named twice, or (fork) not empty */
+#define BITNET_CACHE_ERR_LEN (1 << 1)  /* a length or position outside the table               */
+#define BITNET_CACHE_ERR_PAGE (1 << 2) /* a page number outside the pool                       */
+#define BITNET_CACHE_ERR_FULL (1 << 3) /* fewer free pages than bitnet_cache_extend needs      */
+
+typedef struct {
+    int32_t* table;    /* (max_seqs, max_pages) page numbers, device        */
+    int32_t* lens;     /* (max_seqs) tokens held, device                    */
+    int32_t* refs;     /* (num_pages) holders of each page, device          */
+    int32_t* error;    /* one word of BITNET_CACHE_ERR_* bits, device       */
+    int64_t num_pages; /* 1 .. 2^30                                         */
+    int64_t max_seqs;  /* 1 .. 2^24                                         */
+    int64_t max_pages; /* pages a slot can hold; times page_size below 2^31 */
+    int32_t page_size; /* tokens per page: 8, 16, 32, 64, 128 or 256        */
+    int32_t kv_heads;  /* 1 .. 1024                                         */
+    int32_t head_dim;  /* 64 or 128                                         */
+    int32_t dtype;     /* bitnet_cache_dtype                                */
+} bitnet_cache;
+
+typedef struct {
+    void* k;        /* K pages, device, 16-byte aligned                      */
+    void* v;        /* V pages, device, 16-byte aligned                      */
+    float* k_scale; /* BITNET_CACHE_I8: scales of K, 16-byte aligned; else NULL */
+    float* v_scale; /* BITNET_CACHE_I8: scales of V, 16-byte aligned; else NULL */
+} bitnet_cache_layer;
+
+/* Scratch bytes (256-byte aligned device memory) that bitnet_cache_fork, _extend, _free (with
+ * lists of n slots) and _compact need; its contents on entry are ignored, and it must not be
+ * shared by calls that may overlap. 0 for a descriptor that the calls would refuse. */
+size_t bitnet_cache_workspace_size(const bitnet_cache* cache, int64_t n);
+
+/*
+ * bitnet_cache_fork — slot dst[i] becomes a copy of slot src[i] that shares all its pages:
+ *   lens and the table row are copied and refs of each page goes up by one. dst[i] must be empty
+ *   (lens 0); a src may appear many times. No page is copied (see bitnet_cache_extend).
+ * bitnet_cache_extend — slot seqs[i] grows by add[i] >= 0 tokens: lens[seqs[i]] += add[i], and
+ *   the pages that it then needs are taken from the free ones, lowest number first, for i in
+ *   order. If its last page is partly filled and other slots hold it too, the slot gets a new
+ *   page in its place and the pair (old, new) goes into `copies`, so that the tokens can be
+ *   written without touching the other holders; where all holders of a page grow in this call,
+ *   the last of them in the list keeps it. The slots' new tokens are then written by
+ *   bitnet_cache_append, after bitnet_cache_copy has run on `copies` for the layer.
+ *   If too few pages are free nothing is changed (BITNET_CACHE_ERR_FULL).
+ * bitnet_cache_free — slots seqs[i] become empty: refs of each of their pages goes down by one
+ *   and lens becomes 0.
+ * bitnet_cache_compact — moves the pages in use to the front of the pool: with L of them, the
+ *   ones numbered L and up go, in ascending order, to the free numbers below L, ascending. The
+ *   tables of all slots and refs are rewritten, and the moves go into `copies`; the pages'
+ *   contents move when bitnet_cache_copy runs on `copies`, which has to be before any other call
+ *   that reads or writes them.
+ * copies [out] int32, 8-byte aligned: [0] the number of pairs, [1] 0, then pairs (from, to).
+ *   It has room for `max_copies` pairs: at least n (extend) or num_pages / 2 (compact), or the
+ *   call returns BITNET_ERR_WORKSPACE. Entries past the pairs are left as they were.
+ */
+bitnet_status bitnet_cache_fork(const bitnet_cache* cache, const int32_t* src,
+                                const int32_t* dst, int64_t n, void* workspace,
+                                size_t workspace_bytes, void* stream);
+bitnet_status bitnet_cache_extend(const bitnet_cache* cache, const int32_t* seqs,
+                                  const int32_t* add, int64_t n, int32_t* copies,
+                                  int64_t max_copies, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+bitnet_status bitnet_cache_free(const bitnet_cache* cache, const int32_t* seqs, int64_t n,
+                                void* workspace, size_t workspace_bytes, void* stream);
+bitnet_status bitnet_cache_compact(const bitnet_cache* cache, int32_t* copies,
+                                   int64_t max_copies, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
+/*
+ * bitnet_cache_copy — copies pages from -> to, K and V with their scales, in `nlayers` layers
+ *   (HOST array, 1 .. BITNET_CACHE_MAX_LAYERS) for the pairs of a `copies` list. The number of
+ *   pairs is read on the device and cut at max_copies. No page may be the target of one pair and
+ *   part of another; the lists that the calls above write are such.
+ */
+#define BITNET_CACHE_MAX_LAYERS 64
+bitnet_status bitnet_cache_copy(const bitnet_cache* cache, const bitnet_cache_layer* layers,
+                                int32_t nlayers, const int32_t* copies, int64_t max_copies,
+                                void* stream);
+
+/*
+ * bitnet_cache_append — writes T tokens into one layer's pages.
+ *   k, v  [in] (T, kv_heads, head_dim) bf16 bits, 16-byte aligned.
+ *   seqs  [in] (T) slots, or NULL: token t goes to slot t.
+ *   pos   [in] (T) positions, or NULL: the last one, lens - 1 (one new token per slot, after
+ *         bitnet_cache_extend has counted it). A position outside [0, lens) is reported
+ *         (BITNET_CACHE_ERR_LEN) and the token skipped.
+ *   BITNET_CACHE_I8: per token and head scale = 127 / max(max |x|, 1e-5), q = rint(x * scale), the
+ *   arithmetic of bitnet_quant_act. No two tokens may have one slot and position.
+ */
+bitnet_status bitnet_cache_append(const bitnet_cache* cache, const bitnet_cache_layer* layer,
+                                  const uint16_t* k, const uint16_t* v, int64_t T,
+                                  const int32_t* seqs, const int32_t* pos, void* stream);
+
+/*
+ * bitnet_paged_attention — attention of one new token per sequence over the cache. For query b
+ * of slot s = seqs[b] (NULL: slot b) with n = lens[s], and head h of `heads`, which reads the
+ * key/value head h / (heads / kv_heads):
+ *   z_j = scale * sum_d q[b, h, d] * k_j[d] over the visible positions j of [0, n);
+ *   out[b, h] = sum_j exp(z_j) v_j / sum_j exp(z_j),   lse[b, h] = log sum_j exp(z_j).
+ * All positions are visible with window = 0; otherwise those with j < sinks or j >= n - window
+ * (a sliding window, and the first tokens that stay visible). A sequence of no visible token
+ * gives out = 0 and lse = -inf.
+ *   q    [in]  (B, heads, head_dim) bf16 bits, 16-byte aligned; heads a multiple of kv_heads.
+ *   out  [out] (B, heads, head_dim) bf16 bits, 16-byte aligned.
+ *   lse  [out] (B, heads) fp32, 4-byte aligned, or NULL.
+ *   Rows of skipped queries (slot negative or out of range) are left as they were.
+ *   workspace: bitnet_paged_attention_workspace_size(cache, B, heads) bytes, 256-byte aligned;
+ *   contents on entry are ignored; not to be shared by calls that may overlap. The size does not
+ *   depend on the lengths.
+ * Scores, the softmax's maximum and sum, and the weighted sum are held in binary32; weights enter
+ * the second product as two bf16 terms (relative error 2^-16), out is rounded once. The work is
+ * cut over (sequence, key/value head, tokens) by the lengths that the kernel finds on the device,
+ * and joined in a fixed order: the same inputs give the same bits on the same GPU model. Tokens
+ * of a page outside the pool count as not visible (BITNET_CACHE_ERR_PAGE); a length outside the
+ * table is cut at its end (BITNET_CACHE_ERR_LEN). Inf or NaN in a hidden token has no effect.
+ */
+size_t bitnet_paged_attention_workspace_size(const bitnet_cache* cache, int64_t B,
+                                             int64_t heads);
+bitnet_status bitnet_paged_attention(const bitnet_cache* cache, const bitnet_cache_layer* layer,
+                                     const uint16_t* q, int64_t B, int64_t heads,
+                                     const int32_t* seqs, float scale, int64_t window,
+                                     int64_t sinks, uint16_t* out, float* lse, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
+/*
  * Tensor-parallel steps ("BitNet：1-bit LLM推理框架技术实战指南", section on the distributed
  * engine: a model split by layer or by tensor across devices). When a projection's K range is
  * split over ranks (rank r holds x[:, k0:k1] and packed[:, k0/4 : k1/4], k0 and k1 multiples

@@ -16,6 +16,10 @@ Functions keep the C names:
     bitnet_linear_i32(q, packed, ...)          -> acc (int32)
     bitnet_interleave_gate_up(pg, sg, pu, su, per_row) -> (packed_gu, s_w_gu)
     bitnet_linear_swiglu(x, packed_gu, s_w_gu, per_row, ...) -> h (bf16)
+    bitnet_pack_w4(W, group)                   -> (packed, scales)
+    bitnet_linear_w4(x, packed, scales, group, ...) -> y
+    bitnet_cache_fork / _extend / _free / _compact / _copy / _append(cache, ...)
+    bitnet_paged_attention(q, cache, layer, ...) -> out or (out, lse)
     bitnet_check_device_errors()               -> watchdog word (0 = clean)
 """
 from __future__ import annotations
@@ -50,6 +54,9 @@ WATCHDOG_TMA_FULL, WATCHDOG_UNPACK, WATCHDOG_EMPTY, WATCHDOG_ACCUM, WATCHDOG_DRA
     1 << 0, 1 << 1, 1 << 2, 1 << 3, 1 << 4)
 WATCHDOG_SELFTEST = 1 << 6
 MAX_PROJ = 8
+CACHE_BF16, CACHE_I8 = 0, 1
+CACHE_ERR_SEQ, CACHE_ERR_LEN, CACHE_ERR_PAGE, CACHE_ERR_FULL = 1 << 0, 1 << 1, 1 << 2, 1 << 3
+CACHE_MAX_LAYERS = 64
 SWIGLU_BLOCK = 16  # interleaved gate/up rows come in blocks of this many
 
 _P, _I64, _I32, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
@@ -63,6 +70,16 @@ class bitnet_proj(ctypes.Structure):
 class bitnet_plan(ctypes.Structure):
     _fields_ = [("kernel", _I32), ("grid", _I32), ("tile_tokens", _I32), ("splits", _I32),
                 ("tile_rows", _I32), ("reserved", _I32 * 3)]
+
+
+class bitnet_cache(ctypes.Structure):
+    _fields_ = [("table", _P), ("lens", _P), ("refs", _P), ("error", _P), ("num_pages", _I64),
+                ("max_seqs", _I64), ("max_pages", _I64), ("page_size", _I32), ("kv_heads", _I32),
+                ("head_dim", _I32), ("dtype", _I32)]
+
+
+class bitnet_cache_layer(ctypes.Structure):
+    _fields_ = [("k", _P), ("v", _P), ("k_scale", _P), ("v_scale", _P)]
 
 
 KERNEL_GEMV, KERNEL_MMA_GEMV, KERNEL_STREAM, KERNEL_TC, KERNEL_GS = 1, 2, 3, 4, 5
@@ -104,6 +121,23 @@ _SIGS = {
     "bitnet_dequant": ([_P, _I64, _I64, _P, _P, ctypes.c_int, _P, ctypes.c_int, _P], ctypes.c_int),
     "bitnet_linear_plan": ([_I64, _I64, ctypes.POINTER(_I64), _I32, _I32, _SZ, ctypes.c_int,
                             ctypes.POINTER(bitnet_plan)], ctypes.c_int),
+    "bitnet_w4_row_bytes": ([_I64], _I64),
+    "bitnet_pack_w4": ([_P, _I64, _I64, _I32, _P, _P, _P], ctypes.c_int),
+    "bitnet_linear_w4": ([_P, _I64, _I64, _P, _P, _I32, _I64, _P, ctypes.c_int, _P], ctypes.c_int),
+    "bitnet_cache_workspace_size": ([ctypes.POINTER(bitnet_cache), _I64], _SZ),
+    "bitnet_cache_fork": ([ctypes.POINTER(bitnet_cache), _P, _P, _I64, _P, _SZ, _P], ctypes.c_int),
+    "bitnet_cache_extend": ([ctypes.POINTER(bitnet_cache), _P, _P, _I64, _P, _I64, _P, _SZ, _P],
+                            ctypes.c_int),
+    "bitnet_cache_free": ([ctypes.POINTER(bitnet_cache), _P, _I64, _P, _SZ, _P], ctypes.c_int),
+    "bitnet_cache_compact": ([ctypes.POINTER(bitnet_cache), _P, _I64, _P, _SZ, _P], ctypes.c_int),
+    "bitnet_cache_copy": ([ctypes.POINTER(bitnet_cache), ctypes.POINTER(bitnet_cache_layer), _I32,
+                           _P, _I64, _P], ctypes.c_int),
+    "bitnet_cache_append": ([ctypes.POINTER(bitnet_cache), ctypes.POINTER(bitnet_cache_layer), _P,
+                             _P, _I64, _P, _P, _P], ctypes.c_int),
+    "bitnet_paged_attention_workspace_size": ([ctypes.POINTER(bitnet_cache), _I64, _I64], _SZ),
+    "bitnet_paged_attention": ([ctypes.POINTER(bitnet_cache), ctypes.POINTER(bitnet_cache_layer),
+                                _P, _I64, _I64, _P, ctypes.c_float, _I64, _I64, _P, _P, _P, _SZ,
+                                _P], ctypes.c_int),
     "bitnet_check_device_errors": ([ctypes.POINTER(_I32)], ctypes.c_int),
     "bitnet_selftest_wait_timeout": ([_I64, _P], ctypes.c_int),
     "bitnet_probe_int_rate": ([_I32, _I32, _I64, _P, _P], ctypes.c_int),
@@ -507,6 +541,353 @@ def bitnet_linear_b3(x: torch.Tensor, packed_b3: torch.Tensor, s_w: torch.Tensor
                                 _dev(s_w, torch.float32, "s_w"), int(bool(per_row)), N,
                                 _dev(y, y.dtype, "y"), od, _stream(stream)), "bitnet_linear_b3")
     return y
+
+
+# ----------------------------------------------------------------------------- decode step
+# The operators of a decode step beside the ternary projections. Their device work runs on the
+# device of their tensors, whichever is current, and scratch that a call allocates is kept from
+# reuse until `stream` is done with it.
+class _Launch:
+    """The device of a call's tensors made current, and the stream that the call runs on."""
+
+    __slots__ = ("handle", "_guard", "_stream")
+
+    def __init__(self, device: torch.device, stream: Optional[torch.cuda.Stream]):
+        if device.type != "cuda":
+            raise ValueError(f"tensors must be on a CUDA device, got {device}")
+        self._guard = None
+        self._stream = stream
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+        if device.index != torch.cuda.current_device():
+            self._guard = torch.cuda.device(device)
+        if stream is None:
+            self.handle = torch.cuda.current_stream(device).cuda_stream
+        else:
+            self.handle = stream.cuda_stream
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+
+    def scratch(self, n: int, dtype: torch.dtype, device: torch.device) -> torch.Tensor:
+        t = torch.empty(n, dtype=dtype, device=device)
+        return self.keep(t)
+
+    def keep(self, t: torch.Tensor) -> torch.Tensor:
+        """t was allocated on the current stream; it may not be reused before `stream` is done."""
+        if self._stream is not None:
+            t.record_stream(self._stream)
+        return t
+
+
+def _on(t: torch.Tensor, dtype: torch.dtype, device: torch.device, name: str) -> int:
+    if t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on {device}, got {t.dtype} on "
+                         f"{t.device}" + ("" if t.is_contiguous() else ", not contiguous"))
+    return t.data_ptr()
+
+
+def bitnet_pack_w4(W: torch.Tensor, group: int = 128, stream=None):
+    """Latent weights (N, K) fp32 -> 4-bit weights (N, 64 ceil(K / 128)) uint8 and their scales
+    (N, ceil(K / group)) bf16, group = 32, 64 or 128."""
+    if W.dim() != 2:
+        raise ValueError(f"W must be (N, K), got {tuple(W.shape)}")
+    if group not in (32, 64, 128):
+        raise ValueError(f"group must be 32, 64 or 128, got {group}")
+    N, K = W.shape
+    dev = W.device
+    with _Launch(dev, stream) as on:
+        packed = on.keep(torch.empty((N, int(lib.bitnet_w4_row_bytes(K))), dtype=torch.uint8,
+                                     device=dev))
+        scales = on.keep(torch.empty((N, -(-K // group)), dtype=torch.bfloat16, device=dev))
+        _check(lib.bitnet_pack_w4(_on(W, torch.float32, dev, "W"), N, K, group, packed.data_ptr(),
+                                  scales.data_ptr(), on.handle), "bitnet_pack_w4")
+    return packed, scales
+
+
+def bitnet_linear_w4(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, group: int,
+                     out_dtype: torch.dtype = torch.bfloat16, y: Optional[torch.Tensor] = None,
+                     stream=None) -> torch.Tensor:
+    """y (M, N) = x (M, K) bf16 times 4-bit weights with group scales (bitnet_pack_w4)."""
+    M, K = x.shape
+    N = packed.shape[0]
+    if packed.dim() != 2 or packed.shape[1] != -(-K // 128) * 64:
+        raise ValueError(f"packed must be (N, {-(-K // 128) * 64}), got {tuple(packed.shape)}")
+    if group not in (32, 64, 128):
+        raise ValueError(f"group must be 32, 64 or 128, got {group}")
+    if tuple(scales.shape) != (N, -(-K // group)):
+        raise ValueError(f"scales must be ({N}, {-(-K // group)}), got {tuple(scales.shape)}")
+    dev = x.device
+    with _Launch(dev, stream) as on:
+        if y is None:
+            y = on.keep(torch.empty((M, N), dtype=out_dtype, device=dev))
+        _check_out(y, M, N)
+        od = OUT_BF16 if y.dtype == torch.bfloat16 else OUT_F32
+        _check(lib.bitnet_linear_w4(_on(x, torch.bfloat16, dev, "x"), M, K,
+                                    _on(packed, torch.uint8, dev, "packed"),
+                                    _on(scales, torch.bfloat16, dev, "scales"), group, N,
+                                    _on(y, y.dtype, dev, "y"), od, on.handle),
+               "bitnet_linear_w4")
+    return y
+
+
+class PagedCache:
+    """A paged key/value cache over the caller's tensors (see bitnet.h for the layout).
+
+    table  (max_seqs, max_pages) int32, lens (max_seqs) int32, refs (num_pages) int32.
+    layers one (k, v) or (k, v, k_scale, v_scale) per layer: pools (num_pages, kv_heads,
+           page_size, head_dim), bf16, or int8 with scales (num_pages, kv_heads, page_size) fp32.
+    error  one int32 word of CACHE_ERR_* bits (allocated and cleared here if not given);
+           errors() reads and clears it.
+    make_cache allocates a new, empty one.
+    """
+
+    def __init__(self, table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor,
+                 layers: Sequence, error: Optional[torch.Tensor] = None):
+        dev = table.device
+        if dev.type != "cuda":
+            raise ValueError(f"table must be a CUDA tensor, got {dev}")
+        if table.dim() != 2 or lens.shape != table.shape[:1] or refs.dim() != 1:
+            raise ValueError("table must be (max_seqs, max_pages), lens (max_seqs), refs (num_pages)")
+        if not 1 <= len(layers) <= CACHE_MAX_LAYERS:
+            raise ValueError(f"1..{CACHE_MAX_LAYERS} layers")
+        k0 = layers[0][0]
+        if k0.dim() != 4 or k0.shape[0] != refs.shape[0]:
+            raise ValueError(f"pools must be ({refs.shape[0]}, kv_heads, page_size, head_dim), got "
+                             f"{tuple(k0.shape)}")
+        if k0.dtype not in (torch.bfloat16, torch.int8):
+            raise ValueError(f"pools must be bfloat16 or int8, got {k0.dtype}")
+        i8 = k0.dtype == torch.int8
+        self.table, self.lens, self.refs = table, lens, refs
+        self.layers = [tuple(layer) for layer in layers]
+        self.device, self.dtype = dev, k0.dtype
+        self.num_pages, self.kv_heads, self.page_size, self.head_dim = k0.shape
+        self.max_seqs, self.max_pages = table.shape
+        if error is None:
+            error = torch.zeros(1, dtype=torch.int32, device=dev)
+        if error.numel() != 1:
+            raise ValueError("error must have 1 element")
+        self.error = error
+        self._layers = (bitnet_cache_layer * len(layers))()
+        for c_layer, layer in zip(self._layers, self.layers):
+            pools, scales = layer[:2], [t for t in layer[2:] if t is not None]
+            if len(pools) != 2 or len(scales) != (2 if i8 else 0):
+                raise ValueError("a layer is (k, v) in bfloat16, or (k, v, k_scale, v_scale) in int8")
+            if any(t.shape != k0.shape for t in pools) or \
+                    any(t.shape != k0.shape[:3] for t in scales):
+                raise ValueError("all pools must have one shape, scales (num_pages, kv_heads, "
+                                 "page_size)")
+            c_layer.k, c_layer.v = (_on(t, k0.dtype, dev, "pool") for t in pools)
+            if i8:
+                c_layer.k_scale, c_layer.v_scale = (_on(t, torch.float32, dev, "scale")
+                                                    for t in scales)
+        self._c = bitnet_cache(_on(table, torch.int32, dev, "table"),
+                               _on(lens, torch.int32, dev, "lens"),
+                               _on(refs, torch.int32, dev, "refs"),
+                               _on(error, torch.int32, dev, "error"), self.num_pages,
+                               self.max_seqs, self.max_pages, self.page_size, self.kv_heads,
+                               self.head_dim, CACHE_I8 if i8 else CACHE_BF16)
+        self._ref = ctypes.byref(self._c)
+
+    def layer(self, i: int):
+        if not 0 <= i < len(self.layers):
+            raise IndexError(f"layer {i} of {len(self.layers)}")
+        return ctypes.byref(self._layers[i])
+
+    def workspace_size(self, n: int) -> int:
+        return int(lib.bitnet_cache_workspace_size(self._ref, n))
+
+    def errors(self) -> int:
+        """Reads and clears the error word (synchronises)."""
+        e = int(self.error.item())
+        if e:
+            self.error.zero_()
+        return e
+
+
+def make_cache(num_pages: int, max_seqs: int, max_pages: int, kv_heads: int, head_dim: int,
+               page_size: int = 64, layers: int = 1, dtype: torch.dtype = torch.bfloat16,
+               device=None) -> PagedCache:
+    """A new, empty cache."""
+    dev = torch.device(device or "cuda")
+    if dev.index is None:
+        dev = torch.device(dev.type, torch.cuda.current_device())
+    shape = (num_pages, kv_heads, page_size, head_dim)
+    made = []
+    for _ in range(layers):
+        pools = [torch.zeros(shape, dtype=dtype, device=dev) for _ in range(2)]
+        if dtype == torch.int8:
+            pools += [torch.ones(shape[:3], dtype=torch.float32, device=dev) for _ in range(2)]
+        made.append(tuple(pools))
+    return PagedCache(torch.full((max_seqs, max_pages), -1, dtype=torch.int32, device=dev),
+                      torch.zeros(max_seqs, dtype=torch.int32, device=dev),
+                      torch.zeros(num_pages, dtype=torch.int32, device=dev), made)
+
+
+def _slots(cache: PagedCache, t: torch.Tensor, name: str, n: Optional[int] = None) -> int:
+    if t.dim() != 1 or (n is not None and t.shape[0] != n):
+        raise ValueError(f"{name} must be one list" + ("" if n is None else f" of {n}")
+                         + f", got {tuple(t.shape)}")
+    return _on(t, torch.int32, cache.device, name)
+
+
+def _cache_ws(cache: PagedCache, on: _Launch, n: int, workspace: Optional[torch.Tensor]):
+    if workspace is None:
+        workspace = on.scratch(cache.workspace_size(n), torch.uint8, cache.device)
+    elif workspace.device != cache.device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {cache.device}")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def bitnet_cache_fork(cache: PagedCache, src: torch.Tensor, dst: torch.Tensor,
+                      workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Slots dst[i] (empty ones) become copies of slots src[i] that share their pages."""
+    n = src.shape[0]
+    if n == 0:
+        return
+    with _Launch(cache.device, stream) as on:
+        ws, wb = _cache_ws(cache, on, n, workspace)
+        _check(lib.bitnet_cache_fork(cache._ref, _slots(cache, src, "src"),
+                                     _slots(cache, dst, "dst", n), n, ws.data_ptr(), wb, on.handle),
+               "bitnet_cache_fork")
+
+
+def _copies(cache: PagedCache, on: _Launch, room: int, copies: Optional[torch.Tensor]):
+    """A list of page copies with room for `room` pairs: int32 [count, 0, from, to, from, ...]."""
+    if copies is None:
+        return on.scratch(2 + 2 * room, torch.int32, cache.device)
+    if copies.dim() != 1 or copies.shape[0] < 2 + 2 * room:
+        raise ValueError(f"copies must be one list of at least {2 + 2 * room}")
+    _on(copies, torch.int32, cache.device, "copies")
+    return copies
+
+
+def bitnet_cache_extend(cache: PagedCache, seqs: torch.Tensor, add: torch.Tensor,
+                        copies: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Slots seqs[i] grow by add[i] tokens. Returns the page copies that bitnet_cache_copy has
+    to make before the tokens are written: int32 [count, 0, from, to, from, to, ...]."""
+    n = seqs.shape[0]
+    with _Launch(cache.device, stream) as on:
+        copies = _copies(cache, on, n, copies)
+        if n == 0:
+            raise ValueError("seqs is empty")
+        ws, wb = _cache_ws(cache, on, n, workspace)
+        _check(lib.bitnet_cache_extend(cache._ref, _slots(cache, seqs, "seqs"),
+                                       _slots(cache, add, "add", n), n, copies.data_ptr(),
+                                       (copies.shape[0] - 2) // 2, ws.data_ptr(), wb, on.handle),
+               "bitnet_cache_extend")
+    return copies
+
+
+def bitnet_cache_free(cache: PagedCache, seqs: torch.Tensor,
+                      workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Slots seqs[i] become empty."""
+    n = seqs.shape[0]
+    if n == 0:
+        return
+    with _Launch(cache.device, stream) as on:
+        ws, wb = _cache_ws(cache, on, n, workspace)
+        _check(lib.bitnet_cache_free(cache._ref, _slots(cache, seqs, "seqs"), n, ws.data_ptr(), wb,
+                                     on.handle), "bitnet_cache_free")
+
+
+def bitnet_cache_compact(cache: PagedCache, copies: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Moves the pages in use to the front of the pool. Returns the moves for bitnet_cache_copy,
+    which must run before the cache is read or written again."""
+    with _Launch(cache.device, stream) as on:
+        copies = _copies(cache, on, cache.num_pages // 2, copies)
+        ws, wb = _cache_ws(cache, on, 0, workspace)
+        _check(lib.bitnet_cache_compact(cache._ref, copies.data_ptr(), (copies.shape[0] - 2) // 2,
+                                        ws.data_ptr(), wb, on.handle), "bitnet_cache_compact")
+    return copies
+
+
+def bitnet_cache_copy(cache: PagedCache, copies: torch.Tensor, stream=None) -> None:
+    """Copies pages from -> to in every layer of the cache, for a list that bitnet_cache_extend or
+    bitnet_cache_compact returned."""
+    room = (copies.shape[0] - 2) // 2
+    if copies.dim() != 1 or room < 0:
+        raise ValueError("copies must be [count, 0, from, to, ...]")
+    with _Launch(cache.device, stream) as on:
+        _check(lib.bitnet_cache_copy(cache._ref, cache._layers, len(cache.layers),
+                                     _on(copies, torch.int32, cache.device, "copies"), room,
+                                     on.handle), "bitnet_cache_copy")
+
+
+def bitnet_cache_append(cache: PagedCache, layer: int, k: torch.Tensor, v: torch.Tensor,
+                        seqs: Optional[torch.Tensor] = None, pos: Optional[torch.Tensor] = None,
+                        stream=None) -> None:
+    """Writes T tokens, k and v (T, kv_heads, head_dim) or (T, kv_heads * head_dim) bf16, into a
+    layer's pages: token t at position pos[t] (default: the last) of slot seqs[t] (default: t)."""
+    T = k.shape[0]
+    flat, heads = (T, cache.kv_heads * cache.head_dim), (T, cache.kv_heads, cache.head_dim)
+    if tuple(k.shape) not in (flat, heads) or tuple(v.shape) not in (flat, heads):
+        raise ValueError(f"k and v must be (T, {cache.kv_heads}, {cache.head_dim}), got "
+                         f"{tuple(k.shape)} and {tuple(v.shape)}")
+    if T == 0:
+        return
+    if seqs is None and T > cache.max_seqs:
+        raise ValueError(f"{T} tokens for {cache.max_seqs} slots: give seqs")
+    with _Launch(cache.device, stream) as on:
+        _check(lib.bitnet_cache_append(
+            cache._ref, cache.layer(layer), _on(k, torch.bfloat16, cache.device, "k"),
+            _on(v, torch.bfloat16, cache.device, "v"), T,
+            None if seqs is None else _slots(cache, seqs, "seqs", T),
+            None if pos is None else _slots(cache, pos, "pos", T), on.handle),
+            "bitnet_cache_append")
+
+
+@functools.lru_cache(maxsize=4096)
+def _attention_ws(kv_heads: int, head_dim: int, B: int, heads: int) -> int:
+    c = bitnet_cache(1 << 8, 1 << 8, 1 << 8, 1 << 8, 1, 1, 1, 16, kv_heads, head_dim, CACHE_BF16)
+    return int(lib.bitnet_paged_attention_workspace_size(ctypes.byref(c), B, heads))
+
+
+def bitnet_paged_attention(q: torch.Tensor, cache: PagedCache, layer: int = 0,
+                           seqs: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                           window: int = 0, sinks: int = 0, out: Optional[torch.Tensor] = None,
+                           return_lse: bool = False, lse: Optional[torch.Tensor] = None,
+                           workspace: Optional[torch.Tensor] = None, stream=None):
+    """Attention of one new token per sequence: q (B, heads, head_dim) or (B, heads * head_dim)
+    bf16 over slot seqs[b] (default: b) of the cache. scale defaults to head_dim ** -0.5; window
+    and sinks hide all but the first `sinks` and the last `window` tokens. Returns out (shaped as
+    q), or (out, lse) with lse (B, heads) fp32 if return_lse or a tensor for it is given."""
+    D, B = cache.head_dim, q.shape[0]
+    heads = (q.shape[1] if q.dim() == 3 else q.numel() // max(B * D, 1))
+    if q.numel() != B * heads * D or (q.dim() == 3 and q.shape[2] != D) or q.dim() not in (2, 3):
+        raise ValueError(f"q must be (B, heads, {D}), got {tuple(q.shape)}")
+    if seqs is None and B > cache.max_seqs:
+        raise ValueError(f"{B} queries for {cache.max_seqs} slots: give seqs")
+    dev = cache.device
+    with _Launch(dev, stream) as on:
+        if out is None:
+            out = on.keep(torch.empty_like(q))
+        elif out.shape != q.shape:
+            raise ValueError(f"out must be {tuple(q.shape)}, got {tuple(out.shape)}")
+        if lse is None and return_lse:
+            lse = on.scratch(B * heads, torch.float32, dev).view(B, heads)
+        elif lse is not None and tuple(lse.shape) != (B, heads):
+            raise ValueError(f"lse must be ({B}, {heads}), got {tuple(lse.shape)}")
+        if workspace is None:
+            workspace = on.scratch(_attention_ws(cache.kv_heads, D, B, heads), torch.uint8, dev)
+        elif workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous on {dev}")
+        _check(lib.bitnet_paged_attention(
+            cache._ref, cache.layer(layer), _on(q, torch.bfloat16, dev, "q"), B, heads,
+            None if seqs is None else _slots(cache, seqs, "seqs", B),
+            D ** -0.5 if scale is None else scale, window, sinks,
+            _on(out, torch.bfloat16, dev, "out"),
+            None if lse is None else _on(lse, torch.float32, dev, "lse"), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), on.handle), "bitnet_paged_attention")
+    return out if lse is None else (out, lse)
 
 
 def bitnet_act_amax(x: torch.Tensor, stream=None) -> torch.Tensor:

@@ -23,22 +23,6 @@ std::mutex g_err_mu;
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_encode_once;
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-bitnet_status from_cuda(cudaError_t e) { return e == cudaSuccess ? BITNET_OK : BITNET_ERR_CUDA; }
-
-// K, M, N shared checks.
-bitnet_status check_mk(int64_t M, int64_t K) {
-    if (M < 1 || K < 1 || M >= (int64_t(1) << 31) || K >= (int64_t(1) << 31)) return BITNET_ERR_SHAPE;
-    if (K % 4 != 0) return BITNET_ERR_SHAPE;
-    if (K % 64 != 0) return BITNET_ERR_UNSUPPORTED;
-    return BITNET_OK;
-}
-
-bitnet_status check_n(int64_t N) {
-    return (N < 1 || N >= (int64_t(1) << 31)) ? BITNET_ERR_SHAPE : BITNET_OK;
-}
-
 // Validated batch description shared by bitnet_linear and bitnet_linear_batch.
 struct Batch {
     int nproj;

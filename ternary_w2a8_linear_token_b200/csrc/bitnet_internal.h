@@ -12,6 +12,25 @@ namespace bitnet {
 
 constexpr int kMaxProj = BITNET_MAX_PROJ;
 
+// ----------------------------------------------------------------------------- host checks
+inline bool aligned(const void* p, uintptr_t a) {
+    return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
+}
+
+inline bitnet_status from_cuda(cudaError_t e) { return e == cudaSuccess ? BITNET_OK : BITNET_ERR_CUDA; }
+
+// K, M, N shared checks.
+inline bitnet_status check_mk(int64_t M, int64_t K) {
+    if (M < 1 || K < 1 || M >= (int64_t(1) << 31) || K >= (int64_t(1) << 31)) return BITNET_ERR_SHAPE;
+    if (K % 4 != 0) return BITNET_ERR_SHAPE;
+    if (K % 64 != 0) return BITNET_ERR_UNSUPPORTED;
+    return BITNET_OK;
+}
+
+inline bitnet_status check_n(int64_t N) {
+    return (N < 1 || N >= (int64_t(1) << 31)) ? BITNET_ERR_SHAPE : BITNET_OK;
+}
+
 // ----------------------------------------------------------------------------- workspace
 // Tensor-core path scratch: q (M, K) int8 in the in-group permuted K order, s_x (M),
 // r_x = 1/s_x (M) and qsum (M, int32: the sum of each token's q), each region 256-byte

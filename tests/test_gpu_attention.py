@@ -1,0 +1,281 @@
+"""bitnet_paged_attention against 64-bit attention over the same tokens. The tolerances are those
+that decode_ref.attention derives from binary32 arithmetic, plus one rounding to bf16."""
+import numpy as np
+import pytest
+import torch
+
+import decode_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def bn():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import ternary_w2a8_linear_token_b200 as bn
+    return bn
+
+
+def _dev(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def _fill(bn, lens, kv, D, page, dtype, seed=0, layers=1, spare=3):
+    """A cache of sequences of these lengths over scattered pages, random tokens everywhere (so a
+    token that should not be seen would show)."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    need = [-(-n // page) for n in lens]
+    P = sum(need) + spare
+    cache = bn.make_cache(P, len(lens), max(max(need), 1) + 1, kv, D, page, layers, dtype)
+    perm = torch.randperm(P, generator=g, device="cuda").to(torch.int32)
+    at = 0
+    for s, n in enumerate(need):
+        cache.table[s, :n] = perm[at:at + n]
+        cache.refs[perm[at:at + n].long()] = 1
+        at += n
+    cache.lens.copy_(_dev(lens))
+    for layer in cache.layers:
+        for w in range(2):
+            x = torch.randn(layer[w].shape, generator=g, device="cuda")
+            if dtype == torch.int8:
+                layer[w].copy_((x * 40).clamp(-127, 127).round().to(torch.int8))
+                layer[2 + w].copy_(torch.rand(layer[2 + w].shape, generator=g, device="cuda") * 60
+                                   + 20)
+            else:
+                layer[w].copy_(x)
+    return cache
+
+
+def _tokens(cache, layer, slot, n):
+    """k, v of a slot's n tokens as 64-bit arrays (n, kv_heads, D)."""
+    j = torch.arange(n, device="cuda")
+    p, o = cache.table[slot].long()[j // cache.page_size], j % cache.page_size
+    got = []
+    for w in range(2):
+        x = cache.layers[layer][w][p, :, o].double()
+        if cache.dtype == torch.int8:
+            x = x / cache.layers[layer][2 + w][p, :, o].double()[..., None]
+        got.append(x.cpu().numpy())
+    return got
+
+
+def _check(cache, q, out, lse, slots=None, scale=None, window=0, sinks=0, layer=0, rows=None):
+    qd, got = q.double().cpu().numpy(), out.double().cpu().numpy()
+    got_lse = lse.double().cpu().numpy()
+    lens = cache.lens.tolist()
+    for b in range(q.shape[0]) if rows is None else rows:
+        s = b if slots is None else slots[b]
+        k, v = _tokens(cache, layer, s, lens[s])
+        if window:
+            j = np.arange(lens[s])
+            seen = (j < sinks) | (j >= lens[s] - window)
+            k, v = k[seen], v[seen]
+        o, l, to, tl = ref.attention(qd[b], k, v, cache.head_dim ** -0.5 if scale is None else scale)
+        tol = to + ref.BF16_HALF * (np.abs(o) + to)
+        err = np.abs(got[b] - o)
+        assert np.all(err <= tol), f"query {b} of {lens[s]}: {np.nanmax(err / tol):.2f}"
+        if len(k):
+            assert np.all(np.abs(got_lse[b] - l) <= tl), f"lse {b}: {np.max(np.abs(got_lse[b] - l) / tl)}"
+        else:
+            assert np.all(got_lse[b] == -np.inf) and not got[b].any()
+
+
+def _q(B, heads, D, seed=1):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(B, heads, D, generator=g, device="cuda").to(torch.bfloat16)
+
+
+RAGGED = [0, 1, 15, 16, 17, 300, 64, 2, 1025, 0]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.int8])
+@pytest.mark.parametrize("D,kv,group", [(128, 5, 4), (64, 2, 1), (128, 1, 8), (64, 1, 16),
+                                        (128, 2, 3), (64, 2, 17), (128, 1, 40)])
+def test_ragged_batch(bn, D, kv, group, dtype):
+    for page in (8, 64):
+        cache = _fill(bn, RAGGED, kv, D, page, dtype)
+        q = _q(len(RAGGED), kv * group, D)
+        out, lse = bn.bitnet_paged_attention(q, cache, return_lse=True)
+        _check(cache, q, out, lse)
+        again, lse2 = bn.bitnet_paged_attention(q, cache, return_lse=True)
+        assert torch.equal(out, again) and torch.equal(lse, lse2)
+        assert cache.errors() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.int8])
+@pytest.mark.parametrize("n", [1, 7, 4096, 33000])
+def test_one_sequence(bn, n, dtype):
+    """From one token to a length that is split over the whole GPU."""
+    cache = _fill(bn, [n], 2, 128, 16, dtype)
+    q = _q(1, 8, 128)
+    _check(cache, q, *bn.bitnet_paged_attention(q, cache, return_lse=True))
+
+
+def test_one_long_among_many_short(bn):
+    lens = [5] * 100 + [20001] + [40] * 60
+    cache = _fill(bn, lens, 2, 64, 32, torch.bfloat16)
+    q = _q(len(lens), 8, 64)
+    _check(cache, q, *bn.bitnet_paged_attention(q, cache, return_lse=True))
+
+
+@pytest.mark.parametrize("many", [300, 2500])
+def test_many_sequences(bn, many):
+    """More sequences than CTAs, and than one round of the search over lengths."""
+    lens = [(i * 37) % 50 for i in range(many)]
+    cache = _fill(bn, lens, 1, 64, 16, torch.bfloat16)
+    q = _q(many, 2, 64)
+    _check(cache, q, *bn.bitnet_paged_attention(q, cache, return_lse=True))
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (16, 4), (100, 0), (64, 70), (5000, 3),
+                                          (2 ** 40, 2 ** 40)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.int8])
+def test_window_and_sinks(bn, window, sinks, dtype):
+    lens = RAGGED + [2000, 135, 134, 133]
+    cache = _fill(bn, lens, 2, 128, 16, dtype)
+    q = _q(len(lens), 8, 128)
+    out, lse = bn.bitnet_paged_attention(q, cache, window=window, sinks=sinks, return_lse=True)
+    _check(cache, q, out, lse, window=window, sinks=sinks)
+
+
+def test_hidden_tokens_may_hold_anything(bn):
+    """Inf and NaN behind the end of a sequence, in pages of nobody and outside the window, and
+    page numbers that no visible token needs."""
+    for dtype in (torch.bfloat16, torch.int8):
+        lens = [21, 100, 300]
+        cache = _fill(bn, lens, 2, 64, 16, dtype)
+        q = _q(3, 8, 64)
+        want, want_lse = bn.bitnet_paged_attention(q, cache, window=40, sinks=2, return_lse=True)
+        k, v = cache.layers[0][:2]
+        seen = torch.zeros(k.shape[0], 16, dtype=torch.bool)
+        table = cache.table.cpu()
+        for s, n in enumerate(lens):
+            for j in range(n):
+                if j < 2 or j >= n - 40:
+                    seen[table[s, j // 16], j % 16] = True
+        hide = ~seen.cuda()
+        bad = [k, v] if dtype == torch.bfloat16 else list(cache.layers[0][2:])
+        for i, t in enumerate(bad):
+            t.transpose(1, 2)[hide] = (float("nan"), float("inf"))[i]
+        cache.table[2, 3:10] = 10 ** 9  # hidden pages of a long sequence
+        cache.table[0, 2:] = -5  # entries behind the end
+        out, lse = bn.bitnet_paged_attention(q, cache, window=40, sinks=2, return_lse=True)
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+        assert cache.errors() == 0
+
+
+def test_bad_pages_and_slots_are_skipped_and_reported(bn):
+    lens = [40, 70, 0]
+    cache = _fill(bn, lens, 2, 64, 16, torch.bfloat16)
+    q = _q(5, 8, 64)
+    keep = cache.table.clone()
+    cache.table[1, 1] = cache.num_pages
+    cache.table[1, 3] = -1
+    slots = [1, -1, 0, 3, 2]
+    out = torch.full_like(q, 9.0)
+    lse = torch.full((5, 8), 9.0, device="cuda")
+    bn.bitnet_paged_attention(q, cache, seqs=_dev(slots), out=out, lse=lse)
+    assert cache.errors() == bn.CACHE_ERR_PAGE | bn.CACHE_ERR_SEQ
+    for b in (1, 3):  # skipped queries leave their rows
+        assert torch.all(out[b] == 9.0) and torch.all(lse[b] == 9.0)
+    cache.table.copy_(keep)
+    _check(cache, q, out, lse, slots, rows=[2, 4])
+    k, v = _tokens(cache, 0, 1, 70)
+    there = np.array([j // 16 not in (1, 3) for j in range(70)])
+    o, l, to, tl = ref.attention(q[0].double().cpu().numpy(), k[there], v[there], 64 ** -0.5)
+    assert np.all(np.abs(out[0].double().cpu().numpy() - o)
+                  <= to + ref.BF16_HALF * (np.abs(o) + to))
+    # a length outside the table is cut at the table's end
+    full = cache.max_pages * 16
+    cache2 = _fill(bn, [full], 2, 64, 16, torch.bfloat16)
+    cache2.table[0, -1] = cache2.table[0, 0]
+    q2 = _q(1, 8, 64)
+    cap = cache2.max_pages * 16
+    cache2.lens.fill_(cap)
+    want = bn.bitnet_paged_attention(q2, cache2)
+    cache2.lens.fill_(cap + 1)
+    got = bn.bitnet_paged_attention(q2, cache2)
+    assert cache2.errors() == bn.CACHE_ERR_LEN and torch.equal(got, want)
+    cache2.lens.fill_(-1)
+    got, lse = bn.bitnet_paged_attention(q2, cache2, return_lse=True)
+    assert cache2.errors() == bn.CACHE_ERR_LEN and not got.any() and torch.all(lse == -np.inf)
+
+
+@pytest.mark.parametrize("scale", [1.0, 5.0, -0.3, 0.0])
+def test_scales_and_peaked_scores(bn, scale):
+    cache = _fill(bn, [500, 33, 1], 2, 128, 16, torch.bfloat16)
+    q = _q(3, 8, 128)
+    _check(cache, q, *bn.bitnet_paged_attention(q, cache, scale=scale, return_lse=True),
+           scale=scale)
+
+
+def test_scores_far_from_zero(bn):
+    """Scores of several thousand, rising along the sequence (every step changes the maximum)."""
+    cache = _fill(bn, [257], 1, 64, 16, torch.bfloat16)
+    q = torch.ones(1, 4, 64, dtype=torch.bfloat16, device="cuda")
+    for j in range(257):
+        cache.layers[0][0][cache.table[0, j // 16], 0, j % 16] = float(j - 128)
+    _check(cache, q, *bn.bitnet_paged_attention(q, cache, scale=0.5, return_lse=True), scale=0.5)
+
+
+def test_shapes_slots_and_layers(bn):
+    """Flat queries, the same slot twice, several layers, no lse."""
+    cache = _fill(bn, [90, 5, 31], 2, 64, 8, torch.bfloat16, layers=2)
+    q = _q(4, 6, 64)
+    slots = [2, 0, 2, 1]
+    out, lse = bn.bitnet_paged_attention(q.view(4, -1), cache, 1, seqs=_dev(slots), return_lse=True)
+    assert out.shape == (4, 6 * 64)
+    _check(cache, q, out.view(4, 6, 64), lse, slots, layer=1)
+    alone = bn.bitnet_paged_attention(q, cache, 1, seqs=_dev(slots))
+    assert torch.equal(alone.view(4, -1), out)
+
+
+def test_offsets_past_32_bits(bn):
+    """A pool of more than 2^31 values: its last pages are read and written at the right place."""
+    page, kv, D = 256, 8, 128
+    P = (1 << 31) // (page * kv * D) + 3
+    cache = bn.make_cache(P, 2, 3, kv, D, page)
+    cache.table[0, :3] = _dev([P - 1, 0, P - 2])
+    cache.refs[torch.tensor([P - 1, 0, P - 2], device="cuda")] = 1
+    cache.lens[0] = 700
+    g = torch.Generator(device="cuda").manual_seed(3)
+    kv_new = [torch.randn(700, kv, D, generator=g, device="cuda").to(torch.bfloat16)
+              for _ in range(2)]
+    bn.bitnet_cache_append(cache, 0, *kv_new, _dev([0] * 700), _dev(list(range(700))))
+    assert torch.equal(cache.layers[0][0][P - 1].transpose(0, 1), kv_new[0][:256])
+    q = _q(1, 16, D)
+    _check(cache, q, *bn.bitnet_paged_attention(q, cache, seqs=_dev([0]), return_lse=True))
+    bn.bitnet_cache_copy(cache, _dev([1, 0, P - 1, P - 3]))
+    assert torch.equal(cache.layers[0][1][P - 3], cache.layers[0][1][P - 1])
+
+
+def test_two_captured_graphs_with_their_own_workspaces(bn):
+    """Captured once, replayed after the sequences have grown, two graphs in turn."""
+    lens = [60, 1, 200]
+    cache = _fill(bn, lens, 2, 128, 16, torch.bfloat16, spare=40)
+    cache.table.copy_(torch.arange(cache.table.numel(), device="cuda").view_as(cache.table) % cache.num_pages)
+    qs = [_q(3, 8, 128, s) for s in (1, 2)]
+    graphs = []
+    for q in qs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            r = bn.bitnet_paged_attention(q, cache, return_lse=True)
+        graphs.append((g, r))
+    for step in range(3):
+        cache.lens.copy_(_dev([60 + 5 * step, 1 + step, 200 + 8 * step]))
+        for (g, _) in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for q, (_, r) in zip(qs, graphs):
+            _check(cache, q, *r)
+
+
+def test_side_stream(bn):
+    cache = _fill(bn, [900, 30], 2, 128, 16, torch.int8)
+    q = _q(2, 8, 128)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    out, lse = bn.bitnet_paged_attention(q, cache, return_lse=True, stream=side)
+    side.synchronize()
+    _check(cache, q, out, lse)
