@@ -426,7 +426,7 @@ typedef struct {
     int64_t max_seqs;  /* 1 .. 2^24                                         */
     int64_t max_pages; /* pages a slot can hold; times page_size below 2^31 */
     int32_t page_size; /* tokens per page: 8, 16, 32, 64, 128 or 256        */
-    int32_t kv_heads;  /* 1 .. 1024                                         */
+    int32_t kv_heads;  /* 1 .. 1024; num_pages * kv_heads * page_size < 2^31 */
     int32_t head_dim;  /* 64 or 128                                         */
     int32_t dtype;     /* bitnet_cache_dtype                                */
 } bitnet_cache;

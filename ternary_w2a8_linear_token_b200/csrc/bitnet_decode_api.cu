@@ -18,6 +18,8 @@ bitnet_status check_cache(const bitnet_cache* c, CacheView* v) {
     while (shift <= 8 && (1 << shift) != c->page_size) ++shift;
     if (shift > 8) return BITNET_ERR_UNSUPPORTED;
     if (c->max_pages < 1 || c->max_pages >= (int64_t(1) << (31 - shift))) return BITNET_ERR_SHAPE;
+    // Rows of a pool are numbered in 32 bits (2^31 of the smallest would be 137 GB of K alone).
+    if ((c->num_pages * c->kv_heads) << shift >= (int64_t(1) << 31)) return BITNET_ERR_UNSUPPORTED;
     if (c->head_dim != 64 && c->head_dim != 128) return BITNET_ERR_UNSUPPORTED;
     if (c->dtype != BITNET_CACHE_BF16 && c->dtype != BITNET_CACHE_I8) return BITNET_ERR_UNSUPPORTED;
     if (!aligned(c->table, 4) || !aligned(c->lens, 4) || !aligned(c->refs, 4) ||

@@ -1,109 +1,703 @@
 // Attention of one new token per sequence over the paged cache. Contract: include/bitnet.h.
+//
+// Mathematics. For the query heads of one key/value head, with a running maximum m, sum l and
+// weighted sum o per head (all binary32, base 2): for each tile of tokens
+//   z = scale log2(e) q.k,  m' = max(m, max z),  p = 2^(z - m'),
+//   l = l 2^(m - m') + sum p,  o = o 2^(m - m') + p v,  m = m',
+// and two such states join by the same formula. out = o / l, lse = (m + log2 l) ln 2.
+//
+// Bound by HBM: every K and V byte is read once, for 2 to 32 multiply-adds. The products still run
+// on the tensor cores (mma.sync m16n8k16, up to 16 heads of a group as its rows), which leaves
+// the issue slots to the loads; tcgen05 would need 64 rows and more to pay. p enters the second
+// product as two bf16 terms (value and remainder), so its error of 2^-16 vanishes beside the
+// output's rounding of 2^-8; one term would add as much again as that rounding.
+//
+// Split. The tokens of all (sequence, key/value head, block of 16 heads) items are cut into units
+// of 64, and every CTA takes an equal, contiguous share of all units, so that one long sequence
+// among short ones keeps the whole GPU busy. The lengths are on the device, so each CTA finds its
+// share there. A CTA's four warps take 16 tokens of each unit and load them through a ring of
+// their own (cp.async, 16 bytes a lane, no barrier between warps); at the end of an item, or of
+// the CTA's share, the four states are joined in shared memory, and the result goes out, or into
+// the workspace if other CTAs hold parts of the item. A second kernel joins those, in order.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include "act_quant_device.cuh"
+#include "bitnet_device.cuh"
+#include "bitnet_internal.h"
 #include "cache_internal.h"
 
 namespace bitnet {
 namespace {
 
-constexpr int kAttnThreads = 128;
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kTile = 16;              // tokens per warp and unit
+constexpr int kUnit = kTile * kWarps;  // tokens per CTA step
+constexpr int kRows = 16;              // heads per item
+constexpr int kJoinBytes = 8192;       // shared memory in which the warps' states are joined
+constexpr int kMinUnits = 2;           // fewest units that are worth a CTA of their own
+constexpr int kJoinThreads = 512;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// The operator, plainly: one CTA per (query, head), its warps take every fourth token, the lanes
-// the dimensions; a running maximum and sum per warp, joined at the end.
-template <int D>
-__global__ void __launch_bounds__(kAttnThreads) attn_kernel(AttnParams p) {
-    constexpr int E = D / 32;
+template <int D, bool I8>
+struct Shape {
+    static constexpr int kRowBytes = D * (I8 ? 1 : 2);
+    static constexpr int kPool = kTile * kRowBytes;  // K or V of one tile
+    static constexpr int kStageBytes = 2 * kPool + (I8 ? 2 * kTile * 4 : 0);
+    // CTAs per SM and ring stages: 3 x 8 KB per warp and two CTAs for 256-byte rows; smaller rows
+    // leave room for three CTAs, whose warps hide the longer unpacking (8 bits) or the shorter
+    // loads (D = 64).
+    static constexpr int kCtas = kRowBytes == 256 ? 2 : 3;
+    static constexpr int kStages = kRowBytes == 256 ? 3 : kRowBytes == 128 ? 3 : 5;
+    static constexpr int kSmem = kWarps * kStages * kStageBytes + kJoinBytes;
+};
+
+// The workspace: a header, the first unit of each sequence, then two partial states per CTA.
+struct AttnWs {
+    int64_t* head;   // [0] units, [1] CTAs that share them
+    int64_t* first;  // (B + 1) units before each sequence, per item of a sequence
+    float* part;     // [cta][2][kRows * D + 2 * kRows]: o, then m, then l
+};
+
+__host__ __device__ inline AttnWs attn_ws(void* ws, int64_t B) {
+    AttnWs w;
+    w.head = static_cast<int64_t*>(ws);
+    w.first = w.head + 32;
+    w.part = reinterpret_cast<float*>(w.first + ((B + 1 + 31) & ~int64_t(31)));
+    return w;
+}
+
+// Heads of a group in one item, and items of a sequence.
+__host__ __device__ inline int head_blocks(int heads, int kv_heads) {
+    return (heads / kv_heads + kRows - 1) / kRows;
+}
+
+// What a query sees: its slot (-1: none) and its visible tokens, of which those from the sinks on
+// are shifted by `skip` positions.
+struct Seen {
+    int32_t slot, n, skip;
+};
+
+__device__ __forceinline__ Seen seen_by(const AttnParams& p, int64_t b, bool report) {
     const CacheView& c = p.c;
-    const int b = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int kvh = h / (p.heads / c.kv_heads);
+    Seen r = {-1, 0, 0};
     const int64_t s = p.seqs ? p.seqs[b] : b;
-    if (s < 0) return;
+    if (s < 0) return r;
     if (s >= c.max_seqs) {
-        if (threadIdx.x == 0) atomicOr(c.error, BITNET_CACHE_ERR_SEQ);
-        return;
+        if (report) atomicOr(c.error, BITNET_CACHE_ERR_SEQ);
+        return r;
     }
     int64_t n = c.lens[s];
     const int64_t cap = c.max_pages << c.page_shift;
     if (n < 0 || n > cap) {
-        if (threadIdx.x == 0) atomicOr(c.error, BITNET_CACHE_ERR_LEN);
+        if (report) atomicOr(c.error, BITNET_CACHE_ERR_LEN);
         n = n < 0 ? 0 : cap;
     }
     const int64_t span = int64_t(p.window) + p.sinks;
-    const int64_t seen = p.window && n > span ? span : n;
-    float q[E], o[E] = {};
+    const int64_t vis = p.window && n > span ? span : n;
+    r.slot = static_cast<int32_t>(s);
+    r.n = static_cast<int32_t>(vis);
+    r.skip = static_cast<int32_t>(n - vis);
+    return r;
+}
+
+// Units of one item of a query; a query without tokens still has one, which writes its zeros.
+__device__ __forceinline__ int32_t units_of(const Seen& s) {
+    return s.slot < 0 ? 0 : s.n <= kUnit ? 1 : (s.n - 1) / kUnit + 1;
+}
+
+__device__ __forceinline__ int64_t share_begin(int64_t units, int64_t ctas, int64_t cta) {
+    return units * cta / ctas;
+}
+__device__ __forceinline__ int64_t share_owner(int64_t units, int64_t ctas, int64_t unit) {
+    return ((unit + 1) * ctas - 1) / units;
+}
+
+// A position in the list of units: sequence, item within it, unit within that.
+struct Walk {
+    int32_t b, item, t, units;
+    Seen s;
+};
+
+struct Shared {
+    Seen seen[kThreads];  // of the sequences from `base` on
+    int64_t sums[kWarps];
+    int64_t before;  // units before sequence `start`
+    int32_t base, start;
+    float m[kWarps][kRows], l[kWarps][kRows];
+    uint32_t mask[kWarps][8];  // visible tokens of each ring stage
+};
+
+__device__ __forceinline__ void walk_enter(const AttnParams& p, const Shared& sh, Walk& w) {
+    const uint32_t at = uint32_t(w.b - sh.base);
+    w.s = at < uint32_t(kThreads) ? sh.seen[at] : seen_by(p, w.b, false);
+    w.units = units_of(w.s);
+}
+
+// To the next unit; there must be one.
+__device__ __forceinline__ void walk_next(const AttnParams& p, const Shared& sh, int items,
+                                          Walk& w) {
+    if (++w.t < w.units) return;
+    w.t = 0;
+    if (++w.item < items) return;
+    w.item = 0;
+    do {
+        ++w.b;
+        walk_enter(p, sh, w);
+    } while (w.units == 0 && w.b < p.B - 1);
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(there ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool there) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+                 "r"(there ? 4 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a)
+                 : "memory");
+}
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Signed bytes 0 and 2 of w (odd: 1 and 3) as a bf16 pair, exactly: 128 + the low seven bits,
+// less 128, or 256 for a negative byte.
+__device__ __forceinline__ uint32_t bytes_to_bf16(uint32_t w, bool odd) {
+    if (odd) w >>= 8;
+    const uint32_t v = (w & 0x007F007Fu) | 0x43004300u, o = (w & 0x00800080u) | 0x43004300u;
+    __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v),
+                               *reinterpret_cast<const __nv_bfloat162*>(&o));
+    return *reinterpret_cast<uint32_t*>(&r);
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// a, b -> their bf16 pair (a low), and the pair of what the rounding lost.
+__device__ __forceinline__ uint32_t split_bf16(float a, float b, uint32_t& rest) {
+    uint32_t hi;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(b), "f"(a));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(rest) : "f"(b - bf16_hi(hi)), "f"(a - bf16_lo(hi)));
+    return hi;
+}
+
+// Byte offset of 16-byte chunk `chunk` of row `row` in a tile: chunks are permuted within 128
+// bytes so that eight rows' equal chunks (one ldmatrix phase) lie in different banks.
+template <int RB>
+__device__ __forceinline__ uint32_t tile_at(int row, int chunk) {
+    const int swz = RB == 64 ? (row >> 1) & 3 : row & 7;
+    return uint32_t(row * RB + ((chunk ^ swz) << 4));
+}
+
+template <int D, bool I8>
+__global__ void __launch_bounds__(kThreads, Shape<D, I8>::kCtas)
+    attn_kernel(const __grid_constant__ AttnParams p) {
+    using Sh = Shape<D, I8>;
+    constexpr int RB = Sh::kRowBytes, S = Sh::kStages;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ Shared sh;
+    const CacheView& c = p.c;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int group = p.heads / c.kv_heads, blocks = head_blocks(p.heads, c.kv_heads);
+    const int items = c.kv_heads * blocks;
+    const AttnWs ws = attn_ws(p.ws, p.B);
+
+    pdl_wait();
+    pdl_trigger();
+
+    // This CTA's share of the units: their number first, then where the share begins.
+    int64_t sum = 0;
+    for (int64_t b = threadIdx.x; b < p.B; b += kThreads)
+        sum += units_of(seen_by(p, b, blockIdx.x == 0));
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-        q[e] = bf16_lo(p.q[(int64_t(b) * p.heads + h) * D + lane * E + e]);
-    float top = -INFINITY, sum = 0.0f;
-    for (int64_t i = warp; i < seen; i += kAttnThreads / 32) {
-        const int64_t j = i < p.sinks ? i : i + (n - seen);
-        const int32_t page = c.table[s * c.max_pages + (j >> c.page_shift)];
-        if (uint32_t(page) >= uint32_t(c.num_pages)) {
-            if (lane == 0) atomicOr(c.error, BITNET_CACHE_ERR_PAGE);
-            continue;
+    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+    if (lane == 0) sh.sums[warp] = sum;
+    __syncthreads();
+    const int64_t units = (sh.sums[0] + sh.sums[1] + sh.sums[2] + sh.sums[3]) * items;
+    const int64_t want = (units + kMinUnits - 1) / kMinUnits;
+    const int64_t ctas = want < gridDim.x ? want : gridDim.x;
+    const bool last_cta = blockIdx.x == (ctas ? ctas - 1 : 0);
+    if (last_cta && threadIdx.x == 0) {
+        ws.head[0] = units;
+        ws.head[1] = ctas;
+    }
+    if (blockIdx.x >= ctas) return;
+    const int64_t u0 = share_begin(units, ctas, blockIdx.x);
+    const int64_t u1 = share_begin(units, ctas, int64_t(blockIdx.x) + 1);
+    int64_t before = 0;
+    bool placed = false;
+    for (int64_t b0 = 0; b0 < p.B && (!placed || last_cta); b0 += kThreads) {
+        const int64_t b = b0 + threadIdx.x;
+        const Seen s = b < p.B ? seen_by(p, b, false) : Seen{-1, 0, 0};
+        const int64_t mine = units_of(s);
+        int64_t upto = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t up = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+            if (lane >= d) upto += up;
         }
-        const int64_t row = ((int64_t(page) * c.kv_heads + kvh) << c.page_shift) +
-                            (j & ((1 << c.page_shift) - 1));
-        float k[E], v[E];
+        __syncthreads();  // sums and the last round's values have been read
+        if (lane == 31) sh.sums[warp] = upto;
+        if (!placed) sh.seen[threadIdx.x] = s;
+        __syncthreads();
+        int64_t all = 0;
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int64_t at = row * D + lane * E + e;
-            if (c.i8) {
-                k[e] = float(static_cast<const int8_t*>(p.layer.k)[at]) / p.layer.k_scale[row];
-                v[e] = float(static_cast<const int8_t*>(p.layer.v)[at]) / p.layer.v_scale[row];
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) upto += sh.sums[w];
+            all += sh.sums[w];
+        }
+        upto += before;
+        if (last_cta && b < p.B) ws.first[b] = upto - mine;
+        if (!placed && (upto - mine) * items <= u0 && u0 < upto * items) {
+            sh.before = (upto - mine) * items;
+            sh.base = static_cast<int32_t>(b0);
+            sh.start = static_cast<int32_t>(b);
+        }
+        before += all;
+        placed = placed || u0 < before * items;
+    }
+    if (last_cta && threadIdx.x == 0) ws.first[p.B] = before;
+    __syncthreads();
+
+    Walk ahead;  // the unit whose pages are looked up next
+    ahead.b = sh.start;
+    walk_enter(p, sh, ahead);
+    {
+        const int64_t r = u0 - sh.before;
+        ahead.item = static_cast<int32_t>(r / ahead.units);
+        ahead.t = static_cast<int32_t>(r - int64_t(ahead.item) * ahead.units);
+    }
+    Walk cur = ahead;
+    int64_t looked = u0, loaded = u0;  // units whose pages are looked up, whose loads are issued
+
+    uint8_t* ring = smem + warp * (S * Sh::kStageBytes);
+    const uint32_t ring_at = smem_addr(ring);
+
+    // Page lookup of one unit, a step ahead of its loads: lane i (and i + 16) has token i.
+    int32_t row = 0;
+    bool there = false;
+    auto look_up = [&]() {
+        if (looked >= u1) return;
+        const int32_t v = ahead.t * kUnit + warp * kTile + (lane & 15);
+        there = v < ahead.s.n;
+        row = 0;
+        if (there) {
+            const int32_t j = v < p.sinks ? v : v + ahead.s.skip;
+            const int32_t page =
+                c.table[int64_t(ahead.s.slot) * c.max_pages + (j >> c.page_shift)];
+            there = uint32_t(page) < uint32_t(c.num_pages);
+            if (there)
+                row = ((page * c.kv_heads + ahead.item / blocks) << c.page_shift) +
+                      (j & ((1 << c.page_shift) - 1));
+            else
+                atomicOr(c.error, BITNET_CACHE_ERR_PAGE);
+        }
+        if (++looked < u1) walk_next(p, sh, items, ahead);
+    };
+    // Loads of the unit that was looked up last, into ring stage loaded % S; one commit group per
+    // call, empty behind the end.
+    auto load = [&](int stage) {
+        if (loaded < u1) {
+            const uint32_t mask = __ballot_sync(0xFFFFFFFFu, there) & 0xFFFFu;
+            if (lane == 0) sh.mask[warp][stage] = mask;
+            const uint32_t at = ring_at + stage * Sh::kStageBytes;
+            constexpr int kLanes = RB / 16, kStep = 32 / kLanes;
+#pragma unroll
+            for (int i = 0; i < kTile / kStep; ++i) {
+                const int r = i * kStep + lane / kLanes, ch = lane % kLanes;
+                const int64_t from = __shfl_sync(0xFFFFFFFFu, row, r);
+                const bool ok = mask >> r & 1;
+                const uint32_t to = at + tile_at<RB>(r, ch);
+                cp_async16(to, static_cast<const uint8_t*>(p.layer.k) + from * RB + ch * 16, ok);
+                cp_async16(to + Sh::kPool,
+                           static_cast<const uint8_t*>(p.layer.v) + from * RB + ch * 16, ok);
+            }
+            if (I8)
+                cp_async4(at + 2 * Sh::kPool + lane * 4,
+                          (lane < 16 ? p.layer.k_scale : p.layer.v_scale) + row, there);
+            ++loaded;
+        }
+        cp_async_commit();
+    };
+
+    look_up();
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) {
+        load(i);
+        look_up();
+    }
+
+    const int g = lane >> 2, cq = lane & 3;
+    uint32_t q[D / 16][4];
+    float o[D / 8][4], m[2], l[2];
+    bool fresh = true;  // an item begins
+    int stage = 0;
+    const float sc = p.scale * kLog2e;
+
+    for (int64_t u = u0; u < u1; ++u) {
+        const int rows = min(kRows, group - cur.item % blocks * kRows);
+        const int head0 = cur.item / blocks * group + cur.item % blocks * kRows;
+        if (fresh) {
+            fresh = false;
+            const uint16_t* qb = p.q + (int64_t(cur.b) * p.heads + head0) * D;
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const int r = g + 8 * hf;
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    uint32_t x = 0, y = 0;
+                    if (r < rows) {
+                        if (I8) {  // the order in which the bytes of K are unpacked
+                            const uint2 w = *reinterpret_cast<const uint2*>(qb + r * D + 16 * ks +
+                                                                            4 * cq);
+                            x = __byte_perm(w.x, w.y, 0x5410);
+                            y = __byte_perm(w.x, w.y, 0x7632);
+                        } else {
+                            x = *reinterpret_cast<const uint32_t*>(qb + r * D + 16 * ks + 2 * cq);
+                            y = *reinterpret_cast<const uint32_t*>(qb + r * D + 16 * ks + 8 +
+                                                                   2 * cq);
+                        }
+                    }
+                    q[ks][hf] = x;
+                    q[ks][2 + hf] = y;
+                }
+                m[hf] = -INFINITY;
+                l[hf] = 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+        }
+
+        cp_async_wait<S - 2>();
+        __syncwarp();  // this unit's tile is in; all lanes are done with the last one
+        load(stage == 0 ? S - 1 : stage - 1);
+        look_up();
+
+        const uint32_t mask = sh.mask[warp][stage];
+        if (mask) {
+            const uint32_t kt = ring_at + stage * Sh::kStageBytes, vt = kt + Sh::kPool;
+            float z[2][4] = {};
+            const int krow = (lane & 7) + (lane >> 4 << 3), kch = lane >> 3 & 1;
+            if (I8) {
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    uint32_t r[4];
+                    ldmatrix4(r, kt + tile_at<RB>(krow, 2 * i + kch));
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        mma_bf16(z[0], q[2 * i + h], bytes_to_bf16(r[h], false),
+                                 bytes_to_bf16(r[h], true));
+                        mma_bf16(z[1], q[2 * i + h], bytes_to_bf16(r[2 + h], false),
+                                 bytes_to_bf16(r[2 + h], true));
+                    }
+                }
             } else {
-                k[e] = bf16_lo(static_cast<const uint16_t*>(p.layer.k)[at]);
-                v[e] = bf16_lo(static_cast<const uint16_t*>(p.layer.v)[at]);
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    uint32_t r[4];
+                    ldmatrix4(r, kt + tile_at<RB>(krow, 2 * ks + kch));
+                    mma_bf16(z[0], q[ks], r[0], r[1]);
+                    mma_bf16(z[1], q[ks], r[2], r[3]);
+                }
+            }
+            // z[n][2 hf + e]: head g + 8 hf, token 8 n + 2 cq + e.
+            float vs[2][2];
+            const float* scales = reinterpret_cast<const float*>(ring + stage * Sh::kStageBytes +
+                                                                 2 * Sh::kPool);
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int t = 8 * n + 2 * cq + e;
+                    const bool vis = mask >> t & 1;
+                    const float f = I8 ? sc / scales[t] : sc;
+                    if (I8) vs[n][e] = vis ? 1.0f / scales[16 + t] : 0.0f;
+                    z[n][e] = vis ? z[n][e] * f : -INFINITY;
+                    z[n][2 + e] = vis ? z[n][2 + e] * f : -INFINITY;
+                }
+            float keep[2];
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                float top = fmaxf(fmaxf(z[0][2 * hf], z[0][2 * hf + 1]),
+                                  fmaxf(z[1][2 * hf], z[1][2 * hf + 1]));
+                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+                top = fmaxf(top, m[hf]);
+                const float base = top == -INFINITY ? 0.0f : top;
+                keep[hf] = exp2_fast(m[hf] - base);
+                m[hf] = top;
+                float part = 0.0f;
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        z[n][2 * hf + e] = exp2_fast(z[n][2 * hf + e] - base);
+                        part += z[n][2 * hf + e];
+                    }
+                l[hf] = l[hf] * keep[hf] + part;
+            }
+            if (__any_sync(0xFFFFFFFFu, keep[0] != 1.0f || keep[1] != 1.0f)) {
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    o[i][0] *= keep[0];
+                    o[i][1] *= keep[0];
+                    o[i][2] *= keep[1];
+                    o[i][3] *= keep[1];
+                }
+            }
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    const float a = z[n][2 * hf], b = z[n][2 * hf + 1];
+                    // a token of weight 0 must not meet its scale, which may be anything
+                    hi[2 * n + hf] = split_bf16(I8 ? a * vs[n][0] : a, I8 ? b * vs[n][1] : b,
+                                                lo[2 * n + hf]);
+                }
+            const int vrow = lane & 15, vch = lane >> 4;
+            if (I8) {
+#pragma unroll
+                for (int i = 0; i < D / 16; i += 2) {
+                    uint32_t r[4];
+                    ldmatrix4_trans(r, vt + tile_at<RB>(vrow, i + vch));
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int odd = 0; odd < 2; ++odd) {
+                            const uint32_t b0 = bytes_to_bf16(r[2 * h], odd);
+                            const uint32_t b1 = bytes_to_bf16(r[2 * h + 1], odd);
+                            mma_bf16(o[2 * (i + h) + odd], hi, b0, b1);
+                            mma_bf16(o[2 * (i + h) + odd], lo, b0, b1);
+                        }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    uint32_t r[4];
+                    ldmatrix4_trans(r, vt + tile_at<RB>(vrow, 2 * i + vch));
+                    mma_bf16(o[2 * i], hi, r[0], r[1]);
+                    mma_bf16(o[2 * i + 1], hi, r[2], r[3]);
+                    mma_bf16(o[2 * i], lo, r[0], r[1]);
+                    mma_bf16(o[2 * i + 1], lo, r[2], r[3]);
+                }
             }
         }
-        float z = 0.0f;
+        stage = stage + 1 == S ? 0 : stage + 1;
+
+        if (cur.t + 1 == cur.units || u + 1 == u1) {
+            // Join the warps' states.
 #pragma unroll
-        for (int e = 0; e < E; ++e) z += q[e] * k[e];
+            for (int hf = 0; hf < 2; ++hf) {
+                l[hf] += __shfl_xor_sync(0xFFFFFFFFu, l[hf], 1);
+                l[hf] += __shfl_xor_sync(0xFFFFFFFFu, l[hf], 2);
+                if (cq == 0) {
+                    sh.m[warp][g + 8 * hf] = m[hf];
+                    sh.l[warp][g + 8 * hf] = l[hf];
+                }
+            }
+            __syncthreads();
+            float top[2], f[2], total[2];
 #pragma unroll
-        for (int d = 16; d; d >>= 1) z += __shfl_xor_sync(0xFFFFFFFFu, z, d);
-        z *= p.scale;
-        const float next = fmaxf(top, z), keep = expf(top - next), w = expf(z - next);
-        sum = sum * keep + w;
+            for (int hf = 0; hf < 2; ++hf) {
+                const int r = g + 8 * hf;
+                top[hf] = fmaxf(fmaxf(sh.m[0][r], sh.m[1][r]), fmaxf(sh.m[2][r], sh.m[3][r]));
+                const float base = top[hf] == -INFINITY ? 0.0f : top[hf];
+                f[hf] = exp2_fast(m[hf] - base);
+            }
+            const bool begun = int64_t(u) - cur.t >= u0, ended = cur.t + 1 == cur.units;
+            const bool whole = begun && ended;
+            float* part = ws.part + (int64_t(blockIdx.x) * 2 + begun) * (kRows * D + 2 * kRows);
+            // Columns go through shared memory in pieces that hold all warps' rows.
+            float* buf = reinterpret_cast<float*>(smem + kWarps * S * Sh::kStageBytes);
+            int piece = D;
+            while (piece * rows * 4 * kWarps > kJoinBytes) piece >>= 1;
+            for (int d0 = 0; d0 < D; d0 += piece) {
+                if (d0) __syncthreads();
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = o[e] * keep + w * v[e];
+                for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int r = g + (e >> 1) * 8;
+                        const int d = I8 ? 16 * (i >> 1) + 4 * cq + 2 * (e & 1) + (i & 1)
+                                         : 8 * i + 2 * cq + (e & 1);
+                        if (r < rows && d >= d0 && d < d0 + piece)
+                            buf[(warp * rows + r) * piece + d - d0] = o[i][e] * f[e >> 1];
+                    }
+                __syncthreads();
+                for (int x = threadIdx.x; x < rows * piece; x += kThreads) {
+                    const int r = x / piece, d = x - r * piece;
+                    float v = 0.0f;
+#pragma unroll
+                    for (int w = 0; w < kWarps; ++w) v += buf[(w * rows + r) * piece + d];
+                    if (whole) {
+                        float t = 0.0f, b = fmaxf(fmaxf(sh.m[0][r], sh.m[1][r]),
+                                                  fmaxf(sh.m[2][r], sh.m[3][r]));
+                        b = b == -INFINITY ? 0.0f : b;
+#pragma unroll
+                        for (int w = 0; w < kWarps; ++w) t += sh.l[w][r] * exp2_fast(sh.m[w][r] - b);
+                        p.out[(int64_t(cur.b) * p.heads + head0 + r) * D + d0 + d] =
+                            __bfloat16_as_ushort(__float2bfloat16_rn(t > 0.0f ? v / t : 0.0f));
+                    } else {
+                        part[r * D + d0 + d] = v;
+                    }
+                }
+            }
+            if (threadIdx.x < rows) {
+                const int r = threadIdx.x;
+                const float b = fmaxf(fmaxf(sh.m[0][r], sh.m[1][r]), fmaxf(sh.m[2][r], sh.m[3][r]));
+                const float base = b == -INFINITY ? 0.0f : b;
+                float t = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) t += sh.l[w][r] * exp2_fast(sh.m[w][r] - base);
+                if (!whole) {
+                    part[kRows * D + r] = b;
+                    part[kRows * D + kRows + r] = t;
+                } else if (p.lse) {
+                    p.lse[int64_t(cur.b) * p.heads + head0 + r] =
+                        t > 0.0f ? (b + log2f(t)) * kLn2 : -INFINITY;
+                }
+            }
+            __syncthreads();
+            fresh = true;
+        }
+        if (u + 1 < u1) walk_next(p, sh, items, cur);
+    }
+    cp_async_wait<0>();
+}
+
+// Joins the parts of the items that several CTAs worked on: one CTA per (query, head), its thread
+// groups take every n-th part, in a fixed order.
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttnParams p) {
+    constexpr int kGroups = kJoinThreads / D;
+    __shared__ float acc[kGroups][D], tops[kGroups], sums[kGroups];
+    pdl_wait();
+    const AttnWs ws = attn_ws(p.ws, p.B);
+    const int64_t b = blockIdx.x / p.heads;
+    const int h = static_cast<int>(blockIdx.x - b * p.heads);
+    const int64_t units = ws.head[0], ctas = ws.head[1];
+    if (units == 0) return;  // no query at all
+    const int64_t first = ws.first[b], mine = ws.first[b + 1] - first;
+    if (mine == 0) return;
+    const int group = p.heads / p.c.kv_heads, blocks = head_blocks(p.heads, p.c.kv_heads);
+    const int r = h % group % kRows;
+    const int64_t u0 = first * (p.c.kv_heads * blocks) +
+                       (int64_t(h / group) * blocks + h % group / kRows) * mine;
+    const int64_t c0 = share_owner(units, ctas, u0), c1 = share_owner(units, ctas, u0 + mine - 1);
+    if (c0 == c1) return;  // whole in one CTA, which has written it
+    const int d = threadIdx.x % D, grp = threadIdx.x / D;
+    float top = -INFINITY, sum = 0.0f, o = 0.0f;
+#pragma unroll 4
+    for (int64_t c = c0 + grp; c <= c1; c += kGroups) {
+        // the item begins in c0's share and goes on in the others'
+        const float* part = ws.part + (c * 2 + (c == c0)) * (kRows * D + 2 * kRows);
+        const float m = part[kRows * D + r], l = part[kRows * D + kRows + r], v = part[r * D + d];
+        const float next = fmaxf(top, m), base = next == -INFINITY ? 0.0f : next;
+        const float a = exp2_fast(top - base), f = exp2_fast(m - base);
+        sum = sum * a + l * f;
+        o = o * a + v * f;
         top = next;
     }
-    __shared__ float tops[4], sums[4], outs[4][D];
-    if (lane == 0) {
-        tops[warp] = top;
-        sums[warp] = sum;
+    acc[grp][d] = o;
+    if (d == 0) {
+        tops[grp] = top;
+        sums[grp] = sum;
     }
-#pragma unroll
-    for (int e = 0; e < E; ++e) outs[warp][lane * E + e] = o[e];
     __syncthreads();
-    const float all = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-    float total = 0.0f, f[4];
-    for (int i = 0; i < 4; ++i) {
-        f[i] = tops[i] == -INFINITY ? 0.0f : expf(tops[i] - all);
-        total += f[i] * sums[i];
+    if (grp) return;
+#pragma unroll
+    for (int i = 1; i < kGroups; ++i) top = fmaxf(top, tops[i]);
+    const float base = top == -INFINITY ? 0.0f : top;
+    float total = 0.0f, out = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+        const float f = exp2_fast(tops[i] - base);
+        total += sums[i] * f;
+        out += acc[i][d] * f;
     }
-    for (int d = threadIdx.x; d < D; d += kAttnThreads) {
-        const float r = f[0] * outs[0][d] + f[1] * outs[1][d] + f[2] * outs[2][d] + f[3] * outs[3][d];
-        p.out[(int64_t(b) * p.heads + h) * D + d] =
-            __bfloat16_as_ushort(__float2bfloat16_rn(total > 0.0f ? r / total : 0.0f));
-    }
-    if (p.lse && threadIdx.x == 0)
-        p.lse[int64_t(b) * p.heads + h] = total > 0.0f ? all + logf(total) : -INFINITY;
+    const int64_t at = b * p.heads + h;
+    p.out[at * D + d] = __bfloat16_as_ushort(__float2bfloat16_rn(total > 0.0f ? out / total : 0.0f));
+    if (p.lse && d == 0) p.lse[at] = total > 0.0f ? (top + log2f(total)) * kLn2 : -INFINITY;
+}
+
+template <typename... A>
+cudaError_t launch_pdl(void (*kernel)(A...), unsigned grid, unsigned threads, size_t smem,
+                       cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// CTAs of the split: as many as the GPU holds at once, whatever the lengths will be.
+int attn_ctas(int head_dim, bool i8) {
+    const int per = head_dim == 64 ? (i8 ? Shape<64, true>::kCtas : Shape<64, false>::kCtas)
+                                   : (i8 ? Shape<128, true>::kCtas : Shape<128, false>::kCtas);
+    return tc_num_sms() * per;
+}
+
+template <int D, bool I8>
+cudaError_t launch_one(const AttnParams& p, cudaStream_t stream) {
+    using Sh = Shape<D, I8>;
+    cudaError_t e = cudaFuncSetAttribute(attn_kernel<D, I8>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(attn_kernel<D, I8>, static_cast<unsigned>(attn_ctas(D, I8)), kThreads, Sh::kSmem,
+                   stream, p);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(join_kernel<D>, static_cast<unsigned>(int64_t(p.B) * p.heads), kJoinThreads, 0,
+                      stream, p);
 }
 
 }  // namespace
 
-size_t attn_ws_bytes(int32_t, int32_t, int64_t, int64_t) { return 256; }
+size_t attn_ws_bytes(int32_t, int32_t head_dim, int64_t B, int64_t) {
+    const AttnWs w = attn_ws(nullptr, B);
+    return reinterpret_cast<size_t>(w.part) +
+           size_t(attn_ctas(head_dim, true)) * 2 * (kRows * head_dim + 2 * kRows) * 4;
+}
 
 cudaError_t launch_paged_attention(const AttnParams& p, cudaStream_t stream) {
-    const dim3 grid(static_cast<unsigned>(p.B), static_cast<unsigned>(p.heads));
     if (p.c.head_dim == 64)
-        attn_kernel<64><<<grid, kAttnThreads, 0, stream>>>(p);
-    else
-        attn_kernel<128><<<grid, kAttnThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+        return p.c.i8 ? launch_one<64, true>(p, stream) : launch_one<64, false>(p, stream);
+    return p.c.i8 ? launch_one<128, true>(p, stream) : launch_one<128, false>(p, stream);
 }
 
 }  // namespace bitnet
