@@ -13,9 +13,9 @@
 // output's rounding of 2^-8; one term would add as much again as that rounding.
 //
 // Split. The tokens of all (sequence, key/value head, block of 16 heads) items are cut into units
-// of 64, and every CTA takes an equal, contiguous share of all units, so that one long sequence
+// of 64 or 128, and every CTA takes an equal, contiguous share of all units, so that one long sequence
 // among short ones keeps the whole GPU busy. The lengths are on the device, so each CTA finds its
-// share there. A CTA's four warps take 16 tokens of each unit and load them through a ring of
+// share there. A CTA's four warps take a quarter of each unit and load them through a ring of
 // their own (cp.async, 16 bytes a lane, no barrier between warps); at the end of an item, or of
 // the CTA's share, the four states are joined in shared memory, and the result goes out, or into
 // the workspace if other CTAs hold parts of the item. A second kernel joins those, in order.
@@ -32,24 +32,24 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kTile = 16;              // tokens per warp and unit
-constexpr int kUnit = kTile * kWarps;  // tokens per CTA step
-constexpr int kRows = 16;              // heads per item
-constexpr int kJoinBytes = 8192;       // shared memory in which the warps' states are joined
-constexpr int kMinUnits = 2;           // fewest units that are worth a CTA of their own
+constexpr int kRows = 16;         // heads per item
+constexpr int kJoinBytes = 8192;  // shared memory in which the warps' states are joined
+constexpr int kMinUnits = 2;      // fewest units that are worth a CTA of their own
 constexpr int kJoinThreads = 512;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
+// A unit is kTile tokens for each warp: 16 of 256 bytes (a row of K or V), 32 of 128 or 64, so
+// that a ring stage is 8 KB (4 KB for the smallest rows) and the work per tile that does not
+// depend on its bytes weighs less.
 template <int D, bool I8>
 struct Shape {
     static constexpr int kRowBytes = D * (I8 ? 1 : 2);
+    static constexpr int kTile = kRowBytes == 256 ? 16 : 32;
+    static constexpr int kUnit = kTile * kWarps;
     static constexpr int kPool = kTile * kRowBytes;  // K or V of one tile
     static constexpr int kStageBytes = 2 * kPool + (I8 ? 2 * kTile * 4 : 0);
-    // CTAs per SM and ring stages: 3 x 8 KB per warp and two CTAs for 256-byte rows; smaller rows
-    // leave room for three CTAs, whose warps hide the longer unpacking (8 bits) or the shorter
-    // loads (D = 64).
-    static constexpr int kCtas = kRowBytes == 256 ? 2 : 3;
-    static constexpr int kStages = kRowBytes == 256 ? 3 : kRowBytes == 128 ? 3 : 5;
+    static constexpr int kCtas = kRowBytes == 64 ? 3 : 2;  // per SM
+    static constexpr int kStages = 3;
     static constexpr int kSmem = kWarps * kStages * kStageBytes + kJoinBytes;
 };
 
@@ -103,8 +103,9 @@ __device__ __forceinline__ Seen seen_by(const AttnParams& p, int64_t b, bool rep
 }
 
 // Units of one item of a query; a query without tokens still has one, which writes its zeros.
+template <int UNIT>
 __device__ __forceinline__ int32_t units_of(const Seen& s) {
-    return s.slot < 0 ? 0 : s.n <= kUnit ? 1 : (s.n - 1) / kUnit + 1;
+    return s.slot < 0 ? 0 : s.n <= UNIT ? 1 : (s.n - 1) / UNIT + 1;
 }
 
 __device__ __forceinline__ int64_t share_begin(int64_t units, int64_t ctas, int64_t cta) {
@@ -114,37 +115,42 @@ __device__ __forceinline__ int64_t share_owner(int64_t units, int64_t ctas, int6
     return ((unit + 1) * ctas - 1) / units;
 }
 
-// A position in the list of units: sequence, item within it, unit within that.
-struct Walk {
-    int32_t b, item, t, units;
-    Seen s;
-};
-
 struct Shared {
     Seen seen[kThreads];  // of the sequences from `base` on
     int64_t sums[kWarps];
     int64_t before;  // units before sequence `start`
     int32_t base, start;
     float m[kWarps][kRows], l[kWarps][kRows];
-    uint32_t mask[kWarps][8];  // visible tokens of each ring stage
+    uint32_t mask[kWarps][4];  // visible tokens of each ring stage
 };
 
+// A position in the list of units: sequence, then key/value head and block of its heads, then
+// unit within that item.
+struct Walk {
+    int32_t b, head, block, t, units;
+    Seen s;
+};
+
+template <int UNIT>
 __device__ __forceinline__ void walk_enter(const AttnParams& p, const Shared& sh, Walk& w) {
     const uint32_t at = uint32_t(w.b - sh.base);
     w.s = at < uint32_t(kThreads) ? sh.seen[at] : seen_by(p, w.b, false);
-    w.units = units_of(w.s);
+    w.units = units_of<UNIT>(w.s);
 }
 
 // To the next unit; there must be one.
-__device__ __forceinline__ void walk_next(const AttnParams& p, const Shared& sh, int items,
+template <int UNIT>
+__device__ __forceinline__ void walk_next(const AttnParams& p, const Shared& sh, int blocks,
                                           Walk& w) {
     if (++w.t < w.units) return;
     w.t = 0;
-    if (++w.item < items) return;
-    w.item = 0;
+    if (++w.block < blocks) return;
+    w.block = 0;
+    if (++w.head < p.c.kv_heads) return;
+    w.head = 0;
     do {
         ++w.b;
-        walk_enter(p, sh, w);
+        walk_enter<UNIT>(p, sh, w);
     } while (w.units == 0 && w.b < p.B - 1);
 }
 
@@ -218,11 +224,15 @@ __device__ __forceinline__ uint32_t tile_at(int row, int chunk) {
     return uint32_t(row * RB + ((chunk ^ swz) << 4));
 }
 
-template <int D, bool I8>
+// WIDE: items of more than 8 heads; otherwise the lower half of the products' rows is unused, and
+// what belongs to it is left out where that saves instructions.
+template <int D, bool I8, bool WIDE>
 __global__ void __launch_bounds__(kThreads, Shape<D, I8>::kCtas)
     attn_kernel(const __grid_constant__ AttnParams p) {
     using Sh = Shape<D, I8>;
-    constexpr int RB = Sh::kRowBytes, S = Sh::kStages;
+    constexpr int RB = Sh::kRowBytes, S = Sh::kStages, T = Sh::kTile, UNIT = Sh::kUnit;
+    constexpr int NT = T / 8;            // token tiles of eight, the products' columns
+    constexpr int H = WIDE ? 2 : 1;      // halves of the rows that are used
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Shared sh;
     const CacheView& c = p.c;
@@ -237,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8>::kCtas)
     // This CTA's share of the units: their number first, then where the share begins.
     int64_t sum = 0;
     for (int64_t b = threadIdx.x; b < p.B; b += kThreads)
-        sum += units_of(seen_by(p, b, blockIdx.x == 0));
+        sum += units_of<UNIT>(seen_by(p, b, blockIdx.x == 0));
 #pragma unroll
     for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
     if (lane == 0) sh.sums[warp] = sum;
@@ -258,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8>::kCtas)
     for (int64_t b0 = 0; b0 < p.B && (!placed || last_cta); b0 += kThreads) {
         const int64_t b = b0 + threadIdx.x;
         const Seen s = b < p.B ? seen_by(p, b, false) : Seen{-1, 0, 0};
-        const int64_t mine = units_of(s);
+        const int64_t mine = units_of<UNIT>(s);
         int64_t upto = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -290,24 +300,28 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8>::kCtas)
 
     Walk ahead;  // the unit whose pages are looked up next
     ahead.b = sh.start;
-    walk_enter(p, sh, ahead);
+    walk_enter<UNIT>(p, sh, ahead);
     {
         const int64_t r = u0 - sh.before;
-        ahead.item = static_cast<int32_t>(r / ahead.units);
-        ahead.t = static_cast<int32_t>(r - int64_t(ahead.item) * ahead.units);
+        const int32_t item = static_cast<int32_t>(r / ahead.units);
+        ahead.t = static_cast<int32_t>(r - int64_t(item) * ahead.units);
+        ahead.head = item / blocks;
+        ahead.block = item - ahead.head * blocks;
     }
     Walk cur = ahead;
-    int64_t looked = u0, loaded = u0;  // units whose pages are looked up, whose loads are issued
+    // Units of this share: to do, to load, to look up (a share is below 2^31 units).
+    const int32_t n_units = static_cast<int32_t>(u1 - u0);
+    int32_t looked = 0, loaded = 0;
 
     uint8_t* ring = smem + warp * (S * Sh::kStageBytes);
     const uint32_t ring_at = smem_addr(ring);
 
-    // Page lookup of one unit, a step ahead of its loads: lane i (and i + 16) has token i.
+    // Page lookup of one unit, a step ahead of its loads: lane i has token i (modulo T).
     int32_t row = 0;
     bool there = false;
     auto look_up = [&]() {
-        if (looked >= u1) return;
-        const int32_t v = ahead.t * kUnit + warp * kTile + (lane & 15);
+        if (looked >= n_units) return;
+        const int32_t v = ahead.t * UNIT + warp * T + (lane & (T - 1));
         there = v < ahead.s.n;
         row = 0;
         if (there) {
@@ -316,34 +330,40 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8>::kCtas)
                 c.table[int64_t(ahead.s.slot) * c.max_pages + (j >> c.page_shift)];
             there = uint32_t(page) < uint32_t(c.num_pages);
             if (there)
-                row = ((page * c.kv_heads + ahead.item / blocks) << c.page_shift) +
+                row = ((page * c.kv_heads + ahead.head) << c.page_shift) +
                       (j & ((1 << c.page_shift) - 1));
             else
                 atomicOr(c.error, BITNET_CACHE_ERR_PAGE);
         }
-        if (++looked < u1) walk_next(p, sh, items, ahead);
+        if (++looked < n_units) walk_next<UNIT>(p, sh, blocks, ahead);
     };
-    // Loads of the unit that was looked up last, into ring stage loaded % S; one commit group per
-    // call, empty behind the end.
+    // Loads of the unit that was looked up last into a ring stage; one commit group per call, empty
+    // behind the end.
     auto load = [&](int stage) {
-        if (loaded < u1) {
-            const uint32_t mask = __ballot_sync(0xFFFFFFFFu, there) & 0xFFFFu;
+        if (loaded < n_units) {
+            const uint32_t mask = __ballot_sync(0xFFFFFFFFu, there) & (T == 32 ? ~0u : 0xFFFFu);
             if (lane == 0) sh.mask[warp][stage] = mask;
             const uint32_t at = ring_at + stage * Sh::kStageBytes;
             constexpr int kLanes = RB / 16, kStep = 32 / kLanes;
 #pragma unroll
-            for (int i = 0; i < kTile / kStep; ++i) {
+            for (int i = 0; i < T / kStep; ++i) {
                 const int r = i * kStep + lane / kLanes, ch = lane % kLanes;
-                const int64_t from = __shfl_sync(0xFFFFFFFFu, row, r);
+                const int64_t from =
+                    int64_t(__shfl_sync(0xFFFFFFFFu, row, r)) * RB + ch * 16;
                 const bool ok = mask >> r & 1;
                 const uint32_t to = at + tile_at<RB>(r, ch);
-                cp_async16(to, static_cast<const uint8_t*>(p.layer.k) + from * RB + ch * 16, ok);
-                cp_async16(to + Sh::kPool,
-                           static_cast<const uint8_t*>(p.layer.v) + from * RB + ch * 16, ok);
+                cp_async16(to, static_cast<const uint8_t*>(p.layer.k) + from, ok);
+                cp_async16(to + Sh::kPool, static_cast<const uint8_t*>(p.layer.v) + from, ok);
             }
-            if (I8)
-                cp_async4(at + 2 * Sh::kPool + lane * 4,
-                          (lane < 16 ? p.layer.k_scale : p.layer.v_scale) + row, there);
+            if (I8) {
+                const uint32_t to = at + 2 * Sh::kPool + lane * 4;
+                if (T == 32) {
+                    cp_async4(to, p.layer.k_scale + row, there);
+                    cp_async4(to + 4 * T, p.layer.v_scale + row, there);
+                } else {
+                    cp_async4(to, (lane < T ? p.layer.k_scale : p.layer.v_scale) + row, there);
+                }
+            }
             ++loaded;
         }
         cp_async_commit();
@@ -360,14 +380,14 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8>::kCtas)
     uint32_t q[D / 16][4];
     float o[D / 8][4], m[2], l[2];
     bool fresh = true;  // an item begins
-    int stage = 0;
+    int stage = 0, rows = 0, head0 = 0;
     const float sc = p.scale * kLog2e;
 
-    for (int64_t u = u0; u < u1; ++u) {
-        const int rows = min(kRows, group - cur.item % blocks * kRows);
-        const int head0 = cur.item / blocks * group + cur.item % blocks * kRows;
+    for (int32_t u = 0; u < n_units; ++u) {
         if (fresh) {
             fresh = false;
+            rows = min(kRows, group - cur.block * kRows);
+            head0 = cur.head * group + cur.block * kRows;
             const uint16_t* qb = p.q + (int64_t(cur.b) * p.heads + head0) * D;
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
@@ -375,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8>::kCtas)
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
                     uint32_t x = 0, y = 0;
-                    if (r < rows) {
+                    if (hf < H && r < rows) {
                         if (I8) {  // the order in which the bytes of K are unpacked
                             const uint2 w = *reinterpret_cast<const uint2*>(qb + r * D + 16 * ks +
                                                                             4 * cq);
@@ -405,50 +425,85 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8>::kCtas)
         const uint32_t mask = sh.mask[warp][stage];
         if (mask) {
             const uint32_t kt = ring_at + stage * Sh::kStageBytes, vt = kt + Sh::kPool;
-            float z[2][4] = {};
+            // One division per token: its factors replace its scales in shared memory (they are
+            // read behind the products).
+            float* scales =
+                reinterpret_cast<float*>(ring + stage * Sh::kStageBytes + 2 * Sh::kPool);
+            if (I8) {
+                if (T == 32) {
+                    scales[lane] = sc / scales[lane];
+                    scales[T + lane] = 1.0f / scales[T + lane];
+                } else {
+                    scales[lane] = (lane < T ? sc : 1.0f) / scales[lane];
+                }
+                __syncwarp();
+            }
+            float z[NT][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) z[n][0] = z[n][1] = z[n][2] = z[n][3] = 0.0f;
             const int krow = (lane & 7) + (lane >> 4 << 3), kch = lane >> 3 & 1;
             if (I8) {
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
-                    uint32_t r[4];
-                    ldmatrix4(r, kt + tile_at<RB>(krow, 2 * i + kch));
+                for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        mma_bf16(z[0], q[2 * i + h], bytes_to_bf16(r[h], false),
-                                 bytes_to_bf16(r[h], true));
-                        mma_bf16(z[1], q[2 * i + h], bytes_to_bf16(r[2 + h], false),
-                                 bytes_to_bf16(r[2 + h], true));
+                    for (int n = 0; n < NT; n += 2) {
+                        uint32_t r[4];
+                        ldmatrix4(r, kt + tile_at<RB>(8 * n + krow, 2 * i + kch));
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            mma_bf16(z[n], q[2 * i + h], bytes_to_bf16(r[h], false),
+                                     bytes_to_bf16(r[h], true));
+                            mma_bf16(z[n + 1], q[2 * i + h], bytes_to_bf16(r[2 + h], false),
+                                     bytes_to_bf16(r[2 + h], true));
+                        }
                     }
-                }
             } else {
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    uint32_t r[4];
-                    ldmatrix4(r, kt + tile_at<RB>(krow, 2 * ks + kch));
-                    mma_bf16(z[0], q[ks], r[0], r[1]);
-                    mma_bf16(z[1], q[ks], r[2], r[3]);
-                }
+                for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+                    for (int n = 0; n < NT; n += 2) {
+                        uint32_t r[4];
+                        ldmatrix4(r, kt + tile_at<RB>(8 * n + krow, 2 * ks + kch));
+                        mma_bf16(z[n], q[ks], r[0], r[1]);
+                        mma_bf16(z[n + 1], q[ks], r[2], r[3]);
+                    }
             }
             // z[n][2 hf + e]: head g + 8 hf, token 8 n + 2 cq + e.
-            float vs[2][2];
-            const float* scales = reinterpret_cast<const float*>(ring + stage * Sh::kStageBytes +
-                                                                 2 * Sh::kPool);
+            float2 vs[NT];
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int t = 8 * n + 2 * cq + e;
-                    const bool vis = mask >> t & 1;
-                    const float f = I8 ? sc / scales[t] : sc;
-                    if (I8) vs[n][e] = vis ? 1.0f / scales[16 + t] : 0.0f;
-                    z[n][e] = vis ? z[n][e] * f : -INFINITY;
-                    z[n][2 + e] = vis ? z[n][2 + e] * f : -INFINITY;
+            for (int n = 0; n < NT; ++n) {
+                float2 f = make_float2(sc, sc);
+                if (I8) {
+                    f = *reinterpret_cast<const float2*>(scales + 8 * n + 2 * cq);
+                    vs[n] = *reinterpret_cast<const float2*>(scales + T + 8 * n + 2 * cq);
                 }
-            float keep[2];
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                float top = fmaxf(fmaxf(z[0][2 * hf], z[0][2 * hf + 1]),
-                                  fmaxf(z[1][2 * hf], z[1][2 * hf + 1]));
+                for (int hf = 0; hf < H; ++hf) {
+                    z[n][2 * hf] *= f.x;
+                    z[n][2 * hf + 1] *= f.y;
+                }
+            }
+            if (mask != (T == 32 ? ~0u : 0xFFFFu)) {
+                // Hidden tokens get weight 0, and a factor that is not the reciprocal of nothing.
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const bool a = mask >> (8 * n + 2 * cq) & 1, b = mask >> (8 * n + 2 * cq + 1) & 1;
+#pragma unroll
+                    for (int hf = 0; hf < H; ++hf) {
+                        if (!a) z[n][2 * hf] = -INFINITY;
+                        if (!b) z[n][2 * hf + 1] = -INFINITY;
+                    }
+                    if (I8 && !a) vs[n].x = 0.0f;
+                    if (I8 && !b) vs[n].y = 0.0f;
+                }
+            }
+            float keep[2] = {1.0f, 1.0f};
+#pragma unroll
+            for (int hf = 0; hf < H; ++hf) {
+                float top = fmaxf(z[0][2 * hf], z[0][2 * hf + 1]);
+#pragma unroll
+                for (int n = 1; n < NT; ++n)
+                    top = fmaxf(top, fmaxf(z[n][2 * hf], z[n][2 * hf + 1]));
                 top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
                 top = fmaxf(top, m[hf]);
@@ -457,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8>::kCtas)
                 m[hf] = top;
                 float part = 0.0f;
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         z[n][2 * hf + e] = exp2_fast(z[n][2 * hf + e] - base);
@@ -467,54 +522,56 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8>::kCtas)
             }
             if (__any_sync(0xFFFFFFFFu, keep[0] != 1.0f || keep[1] != 1.0f)) {
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    o[i][0] *= keep[0];
-                    o[i][1] *= keep[0];
-                    o[i][2] *= keep[1];
-                    o[i][3] *= keep[1];
-                }
+                for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+                    for (int hf = 0; hf < H; ++hf) {
+                        o[i][2 * hf] *= keep[hf];
+                        o[i][2 * hf + 1] *= keep[hf];
+                    }
             }
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    const float a = z[n][2 * hf], b = z[n][2 * hf + 1];
-                    // a token of weight 0 must not meet its scale, which may be anything
-                    hi[2 * n + hf] = split_bf16(I8 ? a * vs[n][0] : a, I8 ? b * vs[n][1] : b,
-                                                lo[2 * n + hf]);
-                }
             const int vrow = lane & 15, vch = lane >> 4;
-            if (I8) {
 #pragma unroll
-                for (int i = 0; i < D / 16; i += 2) {
-                    uint32_t r[4];
-                    ldmatrix4_trans(r, vt + tile_at<RB>(vrow, i + vch));
+            for (int k = 0; k < NT / 2; ++k) {  // 16 tokens at a time
+                uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
+                for (int n = 0; n < 2; ++n)
 #pragma unroll
-                        for (int odd = 0; odd < 2; ++odd) {
-                            const uint32_t b0 = bytes_to_bf16(r[2 * h], odd);
-                            const uint32_t b1 = bytes_to_bf16(r[2 * h + 1], odd);
-                            mma_bf16(o[2 * (i + h) + odd], hi, b0, b1);
-                            mma_bf16(o[2 * (i + h) + odd], lo, b0, b1);
-                        }
-                }
-            } else {
+                    for (int hf = 0; hf < H; ++hf) {
+                        const float a = z[2 * k + n][2 * hf], b = z[2 * k + n][2 * hf + 1];
+                        hi[2 * n + hf] = split_bf16(I8 ? a * vs[2 * k + n].x : a,
+                                                    I8 ? b * vs[2 * k + n].y : b, lo[2 * n + hf]);
+                    }
+                if (I8) {
 #pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    uint32_t r[4];
-                    ldmatrix4_trans(r, vt + tile_at<RB>(vrow, 2 * i + vch));
-                    mma_bf16(o[2 * i], hi, r[0], r[1]);
-                    mma_bf16(o[2 * i + 1], hi, r[2], r[3]);
-                    mma_bf16(o[2 * i], lo, r[0], r[1]);
-                    mma_bf16(o[2 * i + 1], lo, r[2], r[3]);
+                    for (int i = 0; i < D / 16; i += 2) {
+                        uint32_t r[4];
+                        ldmatrix4_trans(r, vt + tile_at<RB>(16 * k + vrow, i + vch));
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int odd = 0; odd < 2; ++odd) {
+                                const uint32_t b0 = bytes_to_bf16(r[2 * h], odd);
+                                const uint32_t b1 = bytes_to_bf16(r[2 * h + 1], odd);
+                                mma_bf16(o[2 * (i + h) + odd], hi, b0, b1);
+                                mma_bf16(o[2 * (i + h) + odd], lo, b0, b1);
+                            }
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        uint32_t r[4];
+                        ldmatrix4_trans(r, vt + tile_at<RB>(16 * k + vrow, 2 * i + vch));
+                        mma_bf16(o[2 * i], hi, r[0], r[1]);
+                        mma_bf16(o[2 * i + 1], hi, r[2], r[3]);
+                        mma_bf16(o[2 * i], lo, r[0], r[1]);
+                        mma_bf16(o[2 * i + 1], lo, r[2], r[3]);
+                    }
                 }
             }
         }
         stage = stage + 1 == S ? 0 : stage + 1;
 
-        if (cur.t + 1 == cur.units || u + 1 == u1) {
+        if (cur.t + 1 == cur.units || u + 1 == n_units) {
             // Join the warps' states.
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
@@ -534,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8>::kCtas)
                 const float base = top[hf] == -INFINITY ? 0.0f : top[hf];
                 f[hf] = exp2_fast(m[hf] - base);
             }
-            const bool begun = int64_t(u) - cur.t >= u0, ended = cur.t + 1 == cur.units;
+            const bool begun = u >= cur.t, ended = cur.t + 1 == cur.units;
             const bool whole = begun && ended;
             float* part = ws.part + (int64_t(blockIdx.x) * 2 + begun) * (kRows * D + 2 * kRows);
             // Columns go through shared memory in pieces that hold all warps' rows.
@@ -546,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8>::kCtas)
 #pragma unroll
                 for (int i = 0; i < D / 8; ++i)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
+                    for (int e = 0; e < 2 * H; ++e) {
                         const int r = g + (e >> 1) * 8;
                         const int d = I8 ? 16 * (i >> 1) + 4 * cq + 2 * (e & 1) + (i & 1)
                                          : 8 * i + 2 * cq + (e & 1);
@@ -590,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8>::kCtas)
             __syncthreads();
             fresh = true;
         }
-        if (u + 1 < u1) walk_next(p, sh, items, cur);
+        if (u + 1 < n_units) walk_next<UNIT>(p, sh, blocks, cur);
     }
     cp_async_wait<0>();
 }
@@ -673,17 +730,23 @@ int attn_ctas(int head_dim, bool i8) {
     return tc_num_sms() * per;
 }
 
-template <int D, bool I8>
+template <int D, bool I8, bool WIDE>
 cudaError_t launch_one(const AttnParams& p, cudaStream_t stream) {
     using Sh = Shape<D, I8>;
-    cudaError_t e = cudaFuncSetAttribute(attn_kernel<D, I8>,
+    cudaError_t e = cudaFuncSetAttribute(attn_kernel<D, I8, WIDE>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(attn_kernel<D, I8>, static_cast<unsigned>(attn_ctas(D, I8)), kThreads, Sh::kSmem,
-                   stream, p);
+    e = launch_pdl(attn_kernel<D, I8, WIDE>, static_cast<unsigned>(attn_ctas(D, I8)), kThreads,
+                   Sh::kSmem, stream, p);
     if (e != cudaSuccess) return e;
     return launch_pdl(join_kernel<D>, static_cast<unsigned>(int64_t(p.B) * p.heads), kJoinThreads, 0,
                       stream, p);
+}
+
+template <int D, bool I8>
+cudaError_t launch_groups(const AttnParams& p, cudaStream_t stream) {
+    return p.heads / p.c.kv_heads > 8 ? launch_one<D, I8, true>(p, stream)
+                                      : launch_one<D, I8, false>(p, stream);
 }
 
 }  // namespace
@@ -696,8 +759,8 @@ size_t attn_ws_bytes(int32_t, int32_t head_dim, int64_t B, int64_t) {
 
 cudaError_t launch_paged_attention(const AttnParams& p, cudaStream_t stream) {
     if (p.c.head_dim == 64)
-        return p.c.i8 ? launch_one<64, true>(p, stream) : launch_one<64, false>(p, stream);
-    return p.c.i8 ? launch_one<128, true>(p, stream) : launch_one<128, false>(p, stream);
+        return p.c.i8 ? launch_groups<64, true>(p, stream) : launch_groups<64, false>(p, stream);
+    return p.c.i8 ? launch_groups<128, true>(p, stream) : launch_groups<128, false>(p, stream);
 }
 
 }  // namespace bitnet
