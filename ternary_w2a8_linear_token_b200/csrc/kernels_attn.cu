@@ -202,6 +202,13 @@ __device__ __forceinline__ uint32_t bytes_to_bf16(uint32_t w, bool odd) {
     return *reinterpret_cast<uint32_t*>(&r);
 }
 
+// The 8 x 8 matrix of 16-bit values that the warp's registers hold, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
 __device__ __forceinline__ float exp2_fast(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -224,15 +231,14 @@ __device__ __forceinline__ uint32_t tile_at(int row, int chunk) {
     return uint32_t(row * RB + ((chunk ^ swz) << 4));
 }
 
-// WIDE: items of more than 8 heads; otherwise the lower half of the products' rows is unused, and
-// what belongs to it is left out where that saves instructions.
-template <int D, bool I8, bool WIDE>
+// NH: blocks of eight heads in an item. Tokens (scores) and dimensions (output) are the rows of the
+// products and heads their columns, so that up to eight heads cost one column block.
+template <int D, bool I8, int NH>
 __global__ void __launch_bounds__(kThreads, Shape<D, I8>::kCtas)
     attn_kernel(const __grid_constant__ AttnParams p) {
     using Sh = Shape<D, I8>;
     constexpr int RB = Sh::kRowBytes, S = Sh::kStages, T = Sh::kTile, UNIT = Sh::kUnit;
-    constexpr int NT = T / 8;            // token tiles of eight, the products' columns
-    constexpr int H = WIDE ? 2 : 1;      // halves of the rows that are used
+    constexpr int MT = T / 16;  // token tiles of sixteen
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Shared sh;
     const CacheView& c = p.c;
@@ -377,8 +383,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8>::kCtas)
     }
 
     const int g = lane >> 2, cq = lane & 3;
-    uint32_t q[D / 16][4];
-    float o[D / 8][4], m[2], l[2];
+    uint32_t q[NH][D / 16][2];
+    // o[h][i][e], m[h][e & 1], l[h][e & 1]: head 8 h + 2 cq + (e & 1), dimension dim_of(i, e >> 1).
+    float o[NH][D / 16][4], m[NH][2], l[NH][2];
+    auto dim_of = [&](int i, int half) { return 16 * i + (I8 ? 2 * g + half : g + 8 * half); };
     bool fresh = true;  // an item begins
     int stage = 0, rows = 0, head0 = 0;
     const float sc = p.scale * kLog2e;
@@ -390,12 +398,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8>::kCtas)
             head0 = cur.head * group + cur.block * kRows;
             const uint16_t* qb = p.q + (int64_t(cur.b) * p.heads + head0) * D;
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                const int r = g + 8 * hf;
+            for (int h = 0; h < NH; ++h) {
+                const int r = 8 * h + g;
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
                     uint32_t x = 0, y = 0;
-                    if (hf < H && r < rows) {
+                    if (r < rows) {
                         if (I8) {  // the order in which the bytes of K are unpacked
                             const uint2 w = *reinterpret_cast<const uint2*>(qb + r * D + 16 * ks +
                                                                             4 * cq);
@@ -407,14 +415,15 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8>::kCtas)
                                                                    2 * cq);
                         }
                     }
-                    q[ks][hf] = x;
-                    q[ks][2 + hf] = y;
+                    q[h][ks][0] = x;
+                    q[h][ks][1] = y;
                 }
-                m[hf] = -INFINITY;
-                l[hf] = 0.0f;
-            }
+                m[h][0] = m[h][1] = -INFINITY;
+                l[h][0] = l[h][1] = 0.0f;
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+                for (int i = 0; i < D / 16; ++i)
+                    o[h][i][0] = o[h][i][1] = o[h][i][2] = o[h][i][3] = 0.0f;
+            }
         }
 
         cp_async_wait<S - 2>();
@@ -438,133 +447,145 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8>::kCtas)
                 }
                 __syncwarp();
             }
-            float z[NT][4];
+            // z[h][t][2 half + e]: token 16 t + 8 half + g, head 8 h + 2 cq + e.
+            float z[NH][MT][4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) z[n][0] = z[n][1] = z[n][2] = z[n][3] = 0.0f;
-            const int krow = (lane & 7) + (lane >> 4 << 3), kch = lane >> 3 & 1;
+            for (int h = 0; h < NH; ++h)
+#pragma unroll
+                for (int t = 0; t < MT; ++t) z[h][t][0] = z[h][t][1] = z[h][t][2] = z[h][t][3] = 0.0f;
+            const int lrow = lane & 15, lch = lane >> 4;
             if (I8) {
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i)
+                for (int ks = 0; ks < D / 16; ks += 2)
 #pragma unroll
-                    for (int n = 0; n < NT; n += 2) {
+                    for (int t = 0; t < MT; ++t) {
                         uint32_t r[4];
-                        ldmatrix4(r, kt + tile_at<RB>(8 * n + krow, 2 * i + kch));
+                        ldmatrix4(r, kt + tile_at<RB>(16 * t + lrow, ks + lch));
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            mma_bf16(z[n], q[2 * i + h], bytes_to_bf16(r[h], false),
-                                     bytes_to_bf16(r[h], true));
-                            mma_bf16(z[n + 1], q[2 * i + h], bytes_to_bf16(r[2 + h], false),
-                                     bytes_to_bf16(r[2 + h], true));
+                        for (int k = 0; k < 2; ++k) {
+                            const uint32_t a[4] = {
+                                bytes_to_bf16(r[2 * k], false), bytes_to_bf16(r[2 * k + 1], false),
+                                bytes_to_bf16(r[2 * k], true), bytes_to_bf16(r[2 * k + 1], true)};
+#pragma unroll
+                            for (int h = 0; h < NH; ++h)
+                                mma_bf16(z[h][t], a, q[h][ks + k][0], q[h][ks + k][1]);
                         }
                     }
             } else {
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
-                    for (int n = 0; n < NT; n += 2) {
-                        uint32_t r[4];
-                        ldmatrix4(r, kt + tile_at<RB>(8 * n + krow, 2 * ks + kch));
-                        mma_bf16(z[n], q[ks], r[0], r[1]);
-                        mma_bf16(z[n + 1], q[ks], r[2], r[3]);
+                    for (int t = 0; t < MT; ++t) {
+                        uint32_t a[4];
+                        ldmatrix4(a, kt + tile_at<RB>(16 * t + lrow, 2 * ks + lch));
+#pragma unroll
+                        for (int h = 0; h < NH; ++h) mma_bf16(z[h][t], a, q[h][ks][0], q[h][ks][1]);
                     }
             }
-            // z[n][2 hf + e]: head g + 8 hf, token 8 n + 2 cq + e.
-            float2 vs[NT];
+            float vs[MT][2];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float2 f = make_float2(sc, sc);
-                if (I8) {
-                    f = *reinterpret_cast<const float2*>(scales + 8 * n + 2 * cq);
-                    vs[n] = *reinterpret_cast<const float2*>(scales + T + 8 * n + 2 * cq);
-                }
+            for (int t = 0; t < MT; ++t)
 #pragma unroll
-                for (int hf = 0; hf < H; ++hf) {
-                    z[n][2 * hf] *= f.x;
-                    z[n][2 * hf + 1] *= f.y;
+                for (int half = 0; half < 2; ++half) {
+                    const int tok = 16 * t + 8 * half + g;
+                    const float f = I8 ? scales[tok] : sc;
+                    if (I8) vs[t][half] = scales[T + tok];
+#pragma unroll
+                    for (int h = 0; h < NH; ++h) {
+                        z[h][t][2 * half] *= f;
+                        z[h][t][2 * half + 1] *= f;
+                    }
                 }
-            }
             if (mask != (T == 32 ? ~0u : 0xFFFFu)) {
                 // Hidden tokens get weight 0, and a factor that is not the reciprocal of nothing.
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const bool a = mask >> (8 * n + 2 * cq) & 1, b = mask >> (8 * n + 2 * cq + 1) & 1;
+                for (int t = 0; t < MT; ++t)
 #pragma unroll
-                    for (int hf = 0; hf < H; ++hf) {
-                        if (!a) z[n][2 * hf] = -INFINITY;
-                        if (!b) z[n][2 * hf + 1] = -INFINITY;
-                    }
-                    if (I8 && !a) vs[n].x = 0.0f;
-                    if (I8 && !b) vs[n].y = 0.0f;
+                    for (int half = 0; half < 2; ++half)
+                        if (!(mask >> (16 * t + 8 * half + g) & 1)) {
+                            if (I8) vs[t][half] = 0.0f;
+#pragma unroll
+                            for (int h = 0; h < NH; ++h)
+                                z[h][t][2 * half] = z[h][t][2 * half + 1] = -INFINITY;
+                        }
+            }
+            float keep[NH][2];
+            bool grown = false;
+#pragma unroll
+            for (int h = 0; h < NH; ++h)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float top = fmaxf(z[h][0][e], z[h][0][2 + e]);
+#pragma unroll
+                    for (int t = 1; t < MT; ++t) top = fmaxf(top, fmaxf(z[h][t][e], z[h][t][2 + e]));
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1)
+                        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+                    top = fmaxf(top, m[h][e]);
+                    const float base = top == -INFINITY ? 0.0f : top;
+                    keep[h][e] = exp2_fast(m[h][e] - base);
+                    grown |= top != m[h][e];
+                    m[h][e] = top;
+                    float part = 0.0f;
+#pragma unroll
+                    for (int t = 0; t < MT; ++t)
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            z[h][t][2 * half + e] = exp2_fast(z[h][t][2 * half + e] - base);
+                            part += z[h][t][2 * half + e];
+                        }
+                    l[h][e] = l[h][e] * keep[h][e] + part;
                 }
+            if (__any_sync(0xFFFFFFFFu, grown)) {
+#pragma unroll
+                for (int h = 0; h < NH; ++h)
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[h][i][e] *= keep[h][e & 1];
             }
-            float keep[2] = {1.0f, 1.0f};
 #pragma unroll
-            for (int hf = 0; hf < H; ++hf) {
-                float top = fmaxf(z[0][2 * hf], z[0][2 * hf + 1]);
+            for (int t = 0; t < MT; ++t) {  // 16 tokens at a time
+                // Weights with tokens along the lanes' pairs, as the second product takes them.
+                uint32_t hi[NH][2], lo[NH][2];
 #pragma unroll
-                for (int n = 1; n < NT; ++n)
-                    top = fmaxf(top, fmaxf(z[n][2 * hf], z[n][2 * hf + 1]));
-                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-                top = fmaxf(top, m[hf]);
-                const float base = top == -INFINITY ? 0.0f : top;
-                keep[hf] = exp2_fast(m[hf] - base);
-                m[hf] = top;
-                float part = 0.0f;
+                for (int h = 0; h < NH; ++h)
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        z[n][2 * hf + e] = exp2_fast(z[n][2 * hf + e] - base);
-                        part += z[n][2 * hf + e];
-                    }
-                l[hf] = l[hf] * keep[hf] + part;
-            }
-            if (__any_sync(0xFFFFFFFFu, keep[0] != 1.0f || keep[1] != 1.0f)) {
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-                    for (int hf = 0; hf < H; ++hf) {
-                        o[i][2 * hf] *= keep[hf];
-                        o[i][2 * hf + 1] *= keep[hf];
-                    }
-            }
-            const int vrow = lane & 15, vch = lane >> 4;
-#pragma unroll
-            for (int k = 0; k < NT / 2; ++k) {  // 16 tokens at a time
-                uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int hf = 0; hf < H; ++hf) {
-                        const float a = z[2 * k + n][2 * hf], b = z[2 * k + n][2 * hf + 1];
-                        hi[2 * n + hf] = split_bf16(I8 ? a * vs[2 * k + n].x : a,
-                                                    I8 ? b * vs[2 * k + n].y : b, lo[2 * n + hf]);
+                    for (int half = 0; half < 2; ++half) {
+                        const float f = I8 ? vs[t][half] : 1.0f;
+                        uint32_t rest;
+                        hi[h][half] = transpose8(
+                            split_bf16(z[h][t][2 * half] * f, z[h][t][2 * half + 1] * f, rest));
+                        lo[h][half] = transpose8(rest);
                     }
                 if (I8) {
 #pragma unroll
                     for (int i = 0; i < D / 16; i += 2) {
                         uint32_t r[4];
-                        ldmatrix4_trans(r, vt + tile_at<RB>(16 * k + vrow, i + vch));
+                        ldmatrix4_trans(r, vt + tile_at<RB>(16 * t + lrow, i + lch));
 #pragma unroll
-                        for (int h = 0; h < 2; ++h)
+                        for (int k = 0; k < 2; ++k) {
+                            const uint32_t a[4] = {
+                                bytes_to_bf16(r[2 * k], false), bytes_to_bf16(r[2 * k], true),
+                                bytes_to_bf16(r[2 * k + 1], false), bytes_to_bf16(r[2 * k + 1], true)};
 #pragma unroll
-                            for (int odd = 0; odd < 2; ++odd) {
-                                const uint32_t b0 = bytes_to_bf16(r[2 * h], odd);
-                                const uint32_t b1 = bytes_to_bf16(r[2 * h + 1], odd);
-                                mma_bf16(o[2 * (i + h) + odd], hi, b0, b1);
-                                mma_bf16(o[2 * (i + h) + odd], lo, b0, b1);
+                            for (int h = 0; h < NH; ++h) {
+                                mma_bf16(o[h][i + k], a, hi[h][0], hi[h][1]);
+                                mma_bf16(o[h][i + k], a, lo[h][0], lo[h][1]);
                             }
+                        }
                     }
                 } else {
 #pragma unroll
                     for (int i = 0; i < D / 16; ++i) {
-                        uint32_t r[4];
-                        ldmatrix4_trans(r, vt + tile_at<RB>(16 * k + vrow, 2 * i + vch));
-                        mma_bf16(o[2 * i], hi, r[0], r[1]);
-                        mma_bf16(o[2 * i + 1], hi, r[2], r[3]);
-                        mma_bf16(o[2 * i], lo, r[0], r[1]);
-                        mma_bf16(o[2 * i + 1], lo, r[2], r[3]);
+                        uint32_t a[4];
+                        ldmatrix4_trans(a, vt + tile_at<RB>(16 * t + (lane & 7) + (lane >> 4 << 3),
+                                                            2 * i + (lane >> 3 & 1)));
+#pragma unroll
+                        for (int h = 0; h < NH; ++h) {
+                            mma_bf16(o[h][i], a, hi[h][0], hi[h][1]);
+                            mma_bf16(o[h][i], a, lo[h][0], lo[h][1]);
+                        }
                     }
                 }
             }
@@ -574,23 +595,28 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8>::kCtas)
         if (cur.t + 1 == cur.units || u + 1 == n_units) {
             // Join the warps' states.
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                l[hf] += __shfl_xor_sync(0xFFFFFFFFu, l[hf], 1);
-                l[hf] += __shfl_xor_sync(0xFFFFFFFFu, l[hf], 2);
-                if (cq == 0) {
-                    sh.m[warp][g + 8 * hf] = m[hf];
-                    sh.l[warp][g + 8 * hf] = l[hf];
-                }
-            }
-            __syncthreads();
-            float top[2], f[2], total[2];
+            for (int h = 0; h < NH; ++h)
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                const int r = g + 8 * hf;
-                top[hf] = fmaxf(fmaxf(sh.m[0][r], sh.m[1][r]), fmaxf(sh.m[2][r], sh.m[3][r]));
-                const float base = top[hf] == -INFINITY ? 0.0f : top[hf];
-                f[hf] = exp2_fast(m[hf] - base);
-            }
+                for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1)
+                        l[h][e] += __shfl_xor_sync(0xFFFFFFFFu, l[h][e], d);
+                    if (g == 0) {
+                        sh.m[warp][8 * h + 2 * cq + e] = m[h][e];
+                        sh.l[warp][8 * h + 2 * cq + e] = l[h][e];
+                    }
+                }
+            __syncthreads();
+            float f[NH][2];
+#pragma unroll
+            for (int h = 0; h < NH; ++h)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = 8 * h + 2 * cq + e;
+                    const float top =
+                        fmaxf(fmaxf(sh.m[0][r], sh.m[1][r]), fmaxf(sh.m[2][r], sh.m[3][r]));
+                    f[h][e] = exp2_fast(m[h][e] - (top == -INFINITY ? 0.0f : top));
+                }
             const bool begun = u >= cur.t, ended = cur.t + 1 == cur.units;
             const bool whole = begun && ended;
             float* part = ws.part + (int64_t(blockIdx.x) * 2 + begun) * (kRows * D + 2 * kRows);
@@ -601,15 +627,15 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8>::kCtas)
             for (int d0 = 0; d0 < D; d0 += piece) {
                 if (d0) __syncthreads();
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i)
+                for (int h = 0; h < NH; ++h)
 #pragma unroll
-                    for (int e = 0; e < 2 * H; ++e) {
-                        const int r = g + (e >> 1) * 8;
-                        const int d = I8 ? 16 * (i >> 1) + 4 * cq + 2 * (e & 1) + (i & 1)
-                                         : 8 * i + 2 * cq + (e & 1);
-                        if (r < rows && d >= d0 && d < d0 + piece)
-                            buf[(warp * rows + r) * piece + d - d0] = o[i][e] * f[e >> 1];
-                    }
+                    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int r = 8 * h + 2 * cq + (e & 1), d = dim_of(i, e >> 1);
+                            if (r < rows && d >= d0 && d < d0 + piece)
+                                buf[(warp * rows + r) * piece + d - d0] = o[h][i][e] * f[h][e & 1];
+                        }
                 __syncthreads();
                 for (int x = threadIdx.x; x < rows * piece; x += kThreads) {
                     const int r = x / piece, d = x - r * piece;
@@ -730,13 +756,13 @@ int attn_ctas(int head_dim, bool i8) {
     return tc_num_sms() * per;
 }
 
-template <int D, bool I8, bool WIDE>
+template <int D, bool I8, int NH>
 cudaError_t launch_one(const AttnParams& p, cudaStream_t stream) {
     using Sh = Shape<D, I8>;
-    cudaError_t e = cudaFuncSetAttribute(attn_kernel<D, I8, WIDE>,
+    cudaError_t e = cudaFuncSetAttribute(attn_kernel<D, I8, NH>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(attn_kernel<D, I8, WIDE>, static_cast<unsigned>(attn_ctas(D, I8)), kThreads,
+    e = launch_pdl(attn_kernel<D, I8, NH>, static_cast<unsigned>(attn_ctas(D, I8)), kThreads,
                    Sh::kSmem, stream, p);
     if (e != cudaSuccess) return e;
     return launch_pdl(join_kernel<D>, static_cast<unsigned>(int64_t(p.B) * p.heads), kJoinThreads, 0,
@@ -745,8 +771,8 @@ cudaError_t launch_one(const AttnParams& p, cudaStream_t stream) {
 
 template <int D, bool I8>
 cudaError_t launch_groups(const AttnParams& p, cudaStream_t stream) {
-    return p.heads / p.c.kv_heads > 8 ? launch_one<D, I8, true>(p, stream)
-                                      : launch_one<D, I8, false>(p, stream);
+    return p.heads / p.c.kv_heads > 8 ? launch_one<D, I8, 2>(p, stream)
+                                      : launch_one<D, I8, 1>(p, stream);
 }
 
 }  // namespace
