@@ -20,6 +20,7 @@
 // the CTA's share, the four states are joined in shared memory, and the result goes out, or into
 // the workspace if other CTAs hold parts of the item. A second kernel joins those, in order.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <type_traits>
@@ -38,6 +39,7 @@ constexpr int kRows = 16;         // heads per item
 constexpr int kJoinBytes = 8192;  // shared memory in which the warps' states are joined
 constexpr int kMinUnits = 2;      // fewest units that are worth a CTA of their own
 constexpr int kJoinThreads = 512;
+constexpr float kLag = 8.0f;  // powers of two that weights may exceed 1 by
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // A unit is kTile tokens for each warp: 16 of 256 bytes (a row of K or V), 32 of 128 or 64, so
@@ -192,6 +194,25 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Signed bytes 0 and 2 of w (odd: 1 and 3), sign bits turned before, as an fp16 pair, exactly: the
+// byte under the exponent of 1024 reads 1024 + 128 + q.
+__device__ __forceinline__ uint32_t bytes_to_f16(uint32_t turned, bool odd) {
+    uint32_t q;
+    asm("add.rn.f16x2 %0, %1, %2;"
+        : "=r"(q)
+        : "r"(__byte_perm(turned, 0x64646464u, odd ? 0x4341 : 0x4240)), "r"(0xE480E480u));  // - 1152
+    return q;
 }
 
 // Signed bytes 0 and 2 of w (odd: 1 and 3) as a bf16 pair, exactly. The byte with its sign bit
@@ -401,7 +422,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8>::kCtas)
     const int g = lane >> 2, cq = lane & 3;
     uint32_t q[NH][D / 16][2];
     // o[h][i][e], m[h][e & 1], l[h][e & 1]: head 8 h + 2 cq + (e & 1), dimension dim_of(i, e >> 1).
-    float o[NH][D / 16][4], m[NH][2], l[NH][2];
+    // m is the maximum that the sums stand on, which may lag behind by kLag (below). qx: in 8 bits the
+    // power of two that q was divided by to fit fp16.
+    float o[NH][D / 16][4], m[NH][2], l[NH][2], qx[NH][2];
     auto dim_of = [&](int i, int half) { return 16 * i + (I8 ? 2 * g + half : g + 8 * half); };
     bool fresh = true;  // an item begins
     int stage = 0, rows = 0, head0 = 0;
@@ -416,23 +439,43 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8>::kCtas)
 #pragma unroll
             for (int h = 0; h < NH; ++h) {
                 const int r = 8 * h + g;
+                float amax = 0.0f;
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
-                    uint32_t x = 0, y = 0;
+                    uint2 w = make_uint2(0, 0);
+                    const uint16_t* at = qb + r * D + 16 * ks;
                     if (r < rows) {
-                        if (I8) {  // the order in which the bytes of K are unpacked
-                            const uint2 w = *reinterpret_cast<const uint2*>(qb + r * D + 16 * ks +
-                                                                            4 * cq);
-                            x = __byte_perm(w.x, w.y, 0x5410);
-                            y = __byte_perm(w.x, w.y, 0x7632);
-                        } else {
-                            x = *reinterpret_cast<const uint32_t*>(qb + r * D + 16 * ks + 2 * cq);
-                            y = *reinterpret_cast<const uint32_t*>(qb + r * D + 16 * ks + 8 +
-                                                                   2 * cq);
-                        }
+                        if (I8)
+                            w = *reinterpret_cast<const uint2*>(at + 4 * cq);
+                        else
+                            w = make_uint2(*reinterpret_cast<const uint32_t*>(at + 2 * cq),
+                                           *reinterpret_cast<const uint32_t*>(at + 8 + 2 * cq));
                     }
-                    q[h][ks][0] = x;
-                    q[h][ks][1] = y;
+                    q[h][ks][0] = w.x;
+                    q[h][ks][1] = w.y;
+                    if (I8)
+                        amax = fmaxf(amax, fmaxf(fmaxf(fabsf(bf16_lo(w.x)), fabsf(bf16_hi(w.x))),
+                                                 fmaxf(fabsf(bf16_lo(w.y)), fabsf(bf16_hi(w.y)))));
+                }
+                if (I8) {
+                    // fp16 holds q exactly once its largest value is in [1, 2): smaller ones lose
+                    // bits only below 2^-24 of it. Pairs go in the order of the unpacked bytes.
+                    amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+                    amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+                    const int ex = min(max(int(__float_as_uint(amax) >> 23), 1), 253);
+                    const float down = __uint_as_float(uint32_t(254 - ex) << 23);
+                    const float up = __uint_as_float(uint32_t(ex) << 23);
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        const uint32_t x = q[h][ks][0], y = q[h][ks][1];
+                        const __half2 a = __floats2half2_rn(bf16_lo(x) * down, bf16_lo(y) * down);
+                        const __half2 b = __floats2half2_rn(bf16_hi(x) * down, bf16_hi(y) * down);
+                        q[h][ks][0] = *reinterpret_cast<const uint32_t*>(&a);
+                        q[h][ks][1] = *reinterpret_cast<const uint32_t*>(&b);
+                    }
+                    // this lane's columns are heads 2 cq and 2 cq + 1, held by lanes 8 cq and + 4
+                    qx[h][0] = __shfl_sync(0xFFFFFFFFu, up, 8 * cq);
+                    qx[h][1] = __shfl_sync(0xFFFFFFFFu, up, 8 * cq + 4);
                 }
                 m[h][0] = m[h][1] = -INFINITY;
                 l[h][0] = l[h][1] = 0.0f;
@@ -479,12 +522,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8>::kCtas)
                         ldmatrix4(r, kt + tile_at<RB>(16 * t + lrow, ks + lch));
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            const uint32_t a[4] = {
-                                bytes_to_bf16(r[2 * k], false), bytes_to_bf16(r[2 * k + 1], false),
-                                bytes_to_bf16(r[2 * k], true), bytes_to_bf16(r[2 * k + 1], true)};
+                            const uint32_t x = r[2 * k] ^ 0x80808080u, y = r[2 * k + 1] ^ 0x80808080u;
+                            const uint32_t a[4] = {bytes_to_f16(x, false), bytes_to_f16(y, false),
+                                                   bytes_to_f16(x, true), bytes_to_f16(y, true)};
 #pragma unroll
                             for (int h = 0; h < NH; ++h)
-                                mma_bf16(z[h][t], a, q[h][ks + k][0], q[h][ks + k][1]);
+                                mma_f16(z[h][t], a, q[h][ks + k][0], q[h][ks + k][1]);
                         }
                     }
             } else {
@@ -498,68 +541,82 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8>::kCtas)
                         for (int h = 0; h < NH; ++h) mma_bf16(z[h][t], a, q[h][ks][0], q[h][ks][1]);
                     }
             }
-            float vs[MT][2];
+            // Base-2 scores, less m. Hidden tokens get weight 0, and a factor that is not the
+            // reciprocal of nothing.
+            float f[MT][2], vs[MT][2], w[NH][MT][4];
 #pragma unroll
             for (int t = 0; t < MT; ++t)
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    const int tok = 16 * t + 8 * half + g;
-                    const float f = I8 ? scales[tok] : sc;
-                    if (I8) vs[t][half] = scales[T + tok];
-#pragma unroll
-                    for (int h = 0; h < NH; ++h) {
-                        z[h][t][2 * half] *= f;
-                        z[h][t][2 * half + 1] *= f;
-                    }
+                    f[t][half] = I8 ? scales[16 * t + 8 * half + g] : sc;
+                    if (I8) vs[t][half] = scales[T + 16 * t + 8 * half + g];
                 }
+            auto score = [&](int h, int t, int x) {
+                return I8 ? z[h][t][x] * (f[t][x >> 1] * qx[h][x & 1]) : z[h][t][x] * sc;
+            };
+#pragma unroll
+            for (int h = 0; h < NH; ++h)
+#pragma unroll
+                for (int t = 0; t < MT; ++t)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) w[h][t][x] = score(h, t, x);
             if (mask != kAll) {
-                // Hidden tokens get weight 0, and a factor that is not the reciprocal of nothing.
 #pragma unroll
                 for (int t = 0; t < MT; ++t)
 #pragma unroll
                     for (int half = 0; half < 2; ++half)
                         if (!(mask >> (16 * t + 8 * half + g) & 1)) {
-                            if (I8) vs[t][half] = 0.0f;
+                            vs[t][half] = 0.0f;
 #pragma unroll
                             for (int h = 0; h < NH; ++h)
-                                z[h][t][2 * half] = z[h][t][2 * half + 1] = -INFINITY;
+                                w[h][t][2 * half] = w[h][t][2 * half + 1] = -INFINITY;
                         }
             }
-            float keep[NH][2];
             bool grown = false;
 #pragma unroll
             for (int h = 0; h < NH; ++h)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float top = fmaxf(z[h][0][e], z[h][0][2 + e]);
+                for (int t = 0; t < MT; ++t)
 #pragma unroll
-                    for (int t = 1; t < MT; ++t) top = fmaxf(top, fmaxf(z[h][t][e], z[h][t][2 + e]));
-#pragma unroll
-                    for (int d = 4; d < 32; d <<= 1)
-                        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-                    top = fmaxf(top, m[h][e]);
-                    const float base = top == -INFINITY ? 0.0f : top;
-                    keep[h][e] = exp2_fast(m[h][e] - base);
-                    grown |= top != m[h][e];
-                    m[h][e] = top;
-                    float part = 0.0f;
-#pragma unroll
-                    for (int t = 0; t < MT; ++t)
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            z[h][t][2 * half + e] = exp2_fast(z[h][t][2 * half + e] - base);
-                            part += z[h][t][2 * half + e];
-                        }
-                    l[h][e] = l[h][e] * keep[h][e] + part;
-                }
+                    for (int x = 0; x < 4; ++x) grown |= w[h][t][x] > m[h][x & 1] + kLag;
+            // m follows the scores' maximum only when a weight would pass 2^kLag, so that most
+            // tiles need neither the exchange between lanes nor a rescaling.
             if (__any_sync(0xFFFFFFFFu, grown)) {
 #pragma unroll
                 for (int h = 0; h < NH; ++h)
 #pragma unroll
-                    for (int i = 0; i < D / 16; ++i)
+                    for (int e = 0; e < 2; ++e) {
+                        float top = m[h][e];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) o[h][i][e] *= keep[h][e & 1];
+                        for (int t = 0; t < MT; ++t)
+                            top = fmaxf(top, fmaxf(w[h][t][e], w[h][t][2 + e]));
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1)
+                            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+                        const float keep = exp2_fast(m[h][e] - (top == -INFINITY ? 0.0f : top));
+                        m[h][e] = top;
+                        l[h][e] *= keep;
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i) {
+                            o[h][i][e] *= keep;
+                            o[h][i][2 + e] *= keep;
+                        }
+                    }
             }
+#pragma unroll
+            for (int h = 0; h < NH; ++h)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float base = m[h][e] == -INFINITY ? 0.0f : m[h][e];
+#pragma unroll
+                    for (int t = 0; t < MT; ++t)
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            const int x = 2 * half + e;
+                            w[h][t][x] = exp2_fast(w[h][t][x] - base);
+                            l[h][e] += w[h][t][x];
+                        }
+                }
 #pragma unroll
             for (int t = 0; t < MT; ++t) {  // 16 tokens at a time
                 // Weights with tokens along the lanes' pairs, as the second product takes them.
@@ -568,10 +625,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8>::kCtas)
                 for (int h = 0; h < NH; ++h)
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        const float f = I8 ? vs[t][half] : 1.0f;
                         uint32_t rest;
                         hi[h][half] = transpose8(
-                            split_bf16(z[h][t][2 * half] * f, z[h][t][2 * half + 1] * f, rest));
+                            split_bf16(I8 ? w[h][t][2 * half] * vs[t][half] : w[h][t][2 * half],
+                                       I8 ? w[h][t][2 * half + 1] * vs[t][half]
+                                          : w[h][t][2 * half + 1],
+                                       rest));
                         lo[h][half] = transpose8(rest);
                     }
                 if (I8) {
