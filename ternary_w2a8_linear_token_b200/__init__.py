@@ -544,51 +544,43 @@ def bitnet_linear_b3(x: torch.Tensor, packed_b3: torch.Tensor, s_w: torch.Tensor
 
 
 # ----------------------------------------------------------------------------- decode step
-# The operators of a decode step beside the ternary projections. Their device work runs on the
-# device of their tensors, whichever is current, and scratch that a call allocates is kept from
-# reuse until `stream` is done with it.
-class _Launch:
-    """The device of a call's tensors made current, and the stream that the call runs on."""
-
-    __slots__ = ("handle", "_guard", "_stream")
-
-    def __init__(self, device: torch.device, stream: Optional[torch.cuda.Stream]):
-        if device.type != "cuda":
-            raise ValueError(f"tensors must be on a CUDA device, got {device}")
-        self._guard = None
-        self._stream = stream
-        if stream is not None and stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-        if device.index != torch.cuda.current_device():
-            self._guard = torch.cuda.device(device)
-        if stream is None:
-            self.handle = torch.cuda.current_stream(device).cuda_stream
-        else:
-            self.handle = stream.cuda_stream
-
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
-
-    def scratch(self, n: int, dtype: torch.dtype, device: torch.device) -> torch.Tensor:
-        t = torch.empty(n, dtype=dtype, device=device)
-        return self.keep(t)
-
-    def keep(self, t: torch.Tensor) -> torch.Tensor:
-        """t was allocated on the current stream; it may not be reused before `stream` is done."""
-        if self._stream is not None:
-            t.record_stream(self._stream)
-        return t
+# The operators of a decode step beside the ternary projections. They run on the device of their
+# tensors, whichever is current; what a call allocates is kept from reuse until `stream` is done
+# with it. A call's host time is that of a decode step's, so the checks are few and flat.
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(
+    torch._C, "_cuda_getCurrentRawStream") else (
+    lambda i: torch.cuda.current_stream(i).cuda_stream)
+_current = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else (
+    torch.cuda.current_device)
 
 
-def _on(t: torch.Tensor, dtype: torch.dtype, device: torch.device, name: str) -> int:
-    if t.dtype != dtype or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor on {device}, got {t.dtype} on "
+def _elsewhere(dev: int, call, *args, **kw):
+    """call(...) with device `dev`, which is not the current one, made current."""
+    if dev < 0:
+        raise ValueError(f"{call.__name__}: the tensors must be on a CUDA device")
+    with torch.cuda.device(dev):
+        return call(*args, **kw)
+
+
+def _handle(stream: Optional[torch.cuda.Stream], dev: int) -> int:
+    if stream is None:
+        return _raw_stream(dev)
+    if stream.device.index != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{dev}")
+    return stream.cuda_stream
+
+
+def _keep(stream: Optional[torch.cuda.Stream], *tensors):
+    """The tensors were allocated on the current stream: not to be reused before `stream` is done."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def _on(t: torch.Tensor, dtype: torch.dtype, dev: int, name: str) -> int:
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on cuda:{dev}, got {t.dtype} on "
                          f"{t.device}" + ("" if t.is_contiguous() else ", not contiguous"))
     return t.data_ptr()
 
@@ -596,18 +588,19 @@ def _on(t: torch.Tensor, dtype: torch.dtype, device: torch.device, name: str) ->
 def bitnet_pack_w4(W: torch.Tensor, group: int = 128, stream=None):
     """Latent weights (N, K) fp32 -> 4-bit weights (N, 64 ceil(K / 128)) uint8 and their scales
     (N, ceil(K / group)) bf16, group = 32, 64 or 128."""
+    dev = W.get_device()
     if W.dim() != 2:
         raise ValueError(f"W must be (N, K), got {tuple(W.shape)}")
     if group not in (32, 64, 128):
         raise ValueError(f"group must be 32, 64 or 128, got {group}")
+    if dev < 0 or dev != _current():
+        return _elsewhere(dev, bitnet_pack_w4, W, group, stream)
     N, K = W.shape
-    dev = W.device
-    with _Launch(dev, stream) as on:
-        packed = on.keep(torch.empty((N, int(lib.bitnet_w4_row_bytes(K))), dtype=torch.uint8,
-                                     device=dev))
-        scales = on.keep(torch.empty((N, -(-K // group)), dtype=torch.bfloat16, device=dev))
-        _check(lib.bitnet_pack_w4(_on(W, torch.float32, dev, "W"), N, K, group, packed.data_ptr(),
-                                  scales.data_ptr(), on.handle), "bitnet_pack_w4")
+    packed = W.new_empty((N, -(-K // 128) * 64), dtype=torch.uint8)
+    scales = W.new_empty((N, -(-K // group)), dtype=torch.bfloat16)
+    _check(lib.bitnet_pack_w4(_on(W, torch.float32, dev, "W"), N, K, group, packed.data_ptr(),
+                              scales.data_ptr(), _handle(stream, dev)), "bitnet_pack_w4")
+    _keep(stream, packed, scales)
     return packed, scales
 
 
@@ -616,24 +609,30 @@ def bitnet_linear_w4(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor
                      stream=None) -> torch.Tensor:
     """y (M, N) = x (M, K) bf16 times 4-bit weights with group scales (bitnet_pack_w4)."""
     M, K = x.shape
-    N = packed.shape[0]
-    if packed.dim() != 2 or packed.shape[1] != -(-K // 128) * 64:
-        raise ValueError(f"packed must be (N, {-(-K // 128) * 64}), got {tuple(packed.shape)}")
     if group not in (32, 64, 128):
         raise ValueError(f"group must be 32, 64 or 128, got {group}")
-    if tuple(scales.shape) != (N, -(-K // group)):
-        raise ValueError(f"scales must be ({N}, {-(-K // group)}), got {tuple(scales.shape)}")
-    dev = x.device
-    with _Launch(dev, stream) as on:
-        if y is None:
-            y = on.keep(torch.empty((M, N), dtype=out_dtype, device=dev))
+    N, row_bytes = packed.shape
+    if row_bytes != -(-K // 128) * 64 or scales.shape != (N, -(-K // group)):
+        raise ValueError(f"packed must be (N, {-(-K // 128) * 64}) and scales (N, {-(-K // group)}), "
+                         f"got {tuple(packed.shape)} and {tuple(scales.shape)}")
+    dev = x.get_device()
+    if dev < 0 or dev != _current():
+        return _elsewhere(dev, bitnet_linear_w4, x, packed, scales, group, out_dtype, y, stream)
+    if y is None:
+        if out_dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError(f"out_dtype must be bfloat16 or float32, got {out_dtype}")
+        y = torch.empty((M, N), dtype=out_dtype, device=x.device)
+        _keep(stream, y)
+    else:
         _check_out(y, M, N)
-        od = OUT_BF16 if y.dtype == torch.bfloat16 else OUT_F32
-        _check(lib.bitnet_linear_w4(_on(x, torch.bfloat16, dev, "x"), M, K,
-                                    _on(packed, torch.uint8, dev, "packed"),
-                                    _on(scales, torch.bfloat16, dev, "scales"), group, N,
-                                    _on(y, y.dtype, dev, "y"), od, on.handle),
-               "bitnet_linear_w4")
+    st = lib.bitnet_linear_w4(_on(x, torch.bfloat16, dev, "x"), M, K,
+                              _on(packed, torch.uint8, dev, "packed"),
+                              _on(scales, torch.bfloat16, dev, "scales"), group, N,
+                              _on(y, y.dtype, dev, "y"),
+                              OUT_BF16 if y.dtype is torch.bfloat16 else OUT_F32,
+                              _handle(stream, dev))
+    if st:
+        _check(st, "bitnet_linear_w4")
     return y
 
 
@@ -650,9 +649,9 @@ class PagedCache:
 
     def __init__(self, table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor,
                  layers: Sequence, error: Optional[torch.Tensor] = None):
-        dev = table.device
-        if dev.type != "cuda":
-            raise ValueError(f"table must be a CUDA tensor, got {dev}")
+        dev = table.get_device()
+        if dev < 0:
+            raise ValueError(f"table must be a CUDA tensor, got {table.device}")
         if table.dim() != 2 or lens.shape != table.shape[:1] or refs.dim() != 1:
             raise ValueError("table must be (max_seqs, max_pages), lens (max_seqs), refs (num_pages)")
         if not 1 <= len(layers) <= CACHE_MAX_LAYERS:
@@ -666,14 +665,15 @@ class PagedCache:
         i8 = k0.dtype == torch.int8
         self.table, self.lens, self.refs = table, lens, refs
         self.layers = [tuple(layer) for layer in layers]
-        self.device, self.dtype = dev, k0.dtype
+        self.device, self.dtype = table.device, k0.dtype
         self.num_pages, self.kv_heads, self.page_size, self.head_dim = k0.shape
         self.max_seqs, self.max_pages = table.shape
         if error is None:
-            error = torch.zeros(1, dtype=torch.int32, device=dev)
+            error = torch.zeros(1, dtype=torch.int32, device=table.device)
         if error.numel() != 1:
             raise ValueError("error must have 1 element")
         self.error = error
+        self._dev = dev
         self._layers = (bitnet_cache_layer * len(layers))()
         for c_layer, layer in zip(self._layers, self.layers):
             pools, scales = layer[:2], [t for t in layer[2:] if t is not None]
@@ -687,6 +687,7 @@ class PagedCache:
             if i8:
                 c_layer.k_scale, c_layer.v_scale = (_on(t, torch.float32, dev, "scale")
                                                     for t in scales)
+        self._layer_refs = [ctypes.byref(c_layer) for c_layer in self._layers]
         self._c = bitnet_cache(_on(table, torch.int32, dev, "table"),
                                _on(lens, torch.int32, dev, "lens"),
                                _on(refs, torch.int32, dev, "refs"),
@@ -694,14 +695,27 @@ class PagedCache:
                                self.max_seqs, self.max_pages, self.page_size, self.kv_heads,
                                self.head_dim, CACHE_I8 if i8 else CACHE_BF16)
         self._ref = ctypes.byref(self._c)
+        self._sizes = {}  # workspace bytes by call
 
-    def layer(self, i: int):
+    def _layer(self, i: int):
         if not 0 <= i < len(self.layers):
             raise IndexError(f"layer {i} of {len(self.layers)}")
-        return ctypes.byref(self._layers[i])
+        return self._layer_refs[i]
 
     def workspace_size(self, n: int) -> int:
-        return int(lib.bitnet_cache_workspace_size(self._ref, n))
+        """Bytes of scratch for upkeep calls on lists of n slots."""
+        size = self._sizes.get(n)
+        if size is None:
+            size = self._sizes[n] = int(lib.bitnet_cache_workspace_size(self._ref, n))
+        return size
+
+    def attention_workspace_size(self, B: int, heads: int) -> int:
+        """Bytes of scratch for bitnet_paged_attention of B queries."""
+        size = self._sizes.get((B, heads))
+        if size is None:
+            size = self._sizes[B, heads] = int(
+                lib.bitnet_paged_attention_workspace_size(self._ref, B, heads))
+        return size
 
     def errors(self) -> int:
         """Reads and clears the error word (synchronises)."""
@@ -730,42 +744,45 @@ def make_cache(num_pages: int, max_seqs: int, max_pages: int, kv_heads: int, hea
                       torch.zeros(num_pages, dtype=torch.int32, device=dev), made)
 
 
-def _slots(cache: PagedCache, t: torch.Tensor, name: str, n: Optional[int] = None) -> int:
-    if t.dim() != 1 or (n is not None and t.shape[0] != n):
-        raise ValueError(f"{name} must be one list" + ("" if n is None else f" of {n}")
-                         + f", got {tuple(t.shape)}")
-    return _on(t, torch.int32, cache.device, name)
+def _slots(cache: PagedCache, t: torch.Tensor, name: str, n: int) -> int:
+    if t.shape != (n,):
+        raise ValueError(f"{name} must be a list of {n}, got {tuple(t.shape)}")
+    return _on(t, torch.int32, cache._dev, name)
 
 
-def _cache_ws(cache: PagedCache, on: _Launch, n: int, workspace: Optional[torch.Tensor]):
+def _scratch(cache: PagedCache, workspace: Optional[torch.Tensor], size: int, stream):
+    """The workspace of a call, its address and its bytes."""
     if workspace is None:
-        workspace = on.scratch(cache.workspace_size(n), torch.uint8, cache.device)
-    elif workspace.device != cache.device or not workspace.is_contiguous():
+        workspace = torch.empty(size, dtype=torch.uint8, device=cache.device)
+        _keep(stream, workspace)
+        return workspace, workspace.data_ptr(), size
+    if workspace.get_device() != cache._dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous on {cache.device}")
-    return workspace, workspace.numel() * workspace.element_size()
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _copies(cache: PagedCache, room: int, copies: Optional[torch.Tensor], stream):
+    """A list of page copies with room for `room` pairs: int32 [count, 0, from, to, from, ...]."""
+    if copies is None:
+        copies = torch.empty(2 + 2 * room, dtype=torch.int32, device=cache.device)
+        _keep(stream, copies)
+        return copies, copies.data_ptr(), room
+    if copies.dim() != 1 or copies.shape[0] < 2 + 2 * room:
+        raise ValueError(f"copies must be one list of at least {2 + 2 * room}")
+    return copies, _on(copies, torch.int32, cache._dev, "copies"), (copies.shape[0] - 2) // 2
 
 
 def bitnet_cache_fork(cache: PagedCache, src: torch.Tensor, dst: torch.Tensor,
                       workspace: Optional[torch.Tensor] = None, stream=None) -> None:
     """Slots dst[i] (empty ones) become copies of slots src[i] that share their pages."""
-    n = src.shape[0]
-    if n == 0:
-        return
-    with _Launch(cache.device, stream) as on:
-        ws, wb = _cache_ws(cache, on, n, workspace)
-        _check(lib.bitnet_cache_fork(cache._ref, _slots(cache, src, "src"),
-                                     _slots(cache, dst, "dst", n), n, ws.data_ptr(), wb, on.handle),
-               "bitnet_cache_fork")
-
-
-def _copies(cache: PagedCache, on: _Launch, room: int, copies: Optional[torch.Tensor]):
-    """A list of page copies with room for `room` pairs: int32 [count, 0, from, to, from, ...]."""
-    if copies is None:
-        return on.scratch(2 + 2 * room, torch.int32, cache.device)
-    if copies.dim() != 1 or copies.shape[0] < 2 + 2 * room:
-        raise ValueError(f"copies must be one list of at least {2 + 2 * room}")
-    _on(copies, torch.int32, cache.device, "copies")
-    return copies
+    dev, n = cache._dev, src.shape[0]
+    if dev != _current():
+        return _elsewhere(dev, bitnet_cache_fork, cache, src, dst, workspace, stream)
+    ws, wp, wb = _scratch(cache, workspace, cache.workspace_size(n), stream)
+    st = lib.bitnet_cache_fork(cache._ref, _slots(cache, src, "src", n),
+                               _slots(cache, dst, "dst", n), n, wp, wb, _handle(stream, dev))
+    if st:
+        _check(st, "bitnet_cache_fork")
 
 
 def bitnet_cache_extend(cache: PagedCache, seqs: torch.Tensor, add: torch.Tensor,
@@ -773,53 +790,60 @@ def bitnet_cache_extend(cache: PagedCache, seqs: torch.Tensor, add: torch.Tensor
                         workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Slots seqs[i] grow by add[i] tokens. Returns the page copies that bitnet_cache_copy has
     to make before the tokens are written: int32 [count, 0, from, to, from, to, ...]."""
-    n = seqs.shape[0]
-    with _Launch(cache.device, stream) as on:
-        copies = _copies(cache, on, n, copies)
-        if n == 0:
-            raise ValueError("seqs is empty")
-        ws, wb = _cache_ws(cache, on, n, workspace)
-        _check(lib.bitnet_cache_extend(cache._ref, _slots(cache, seqs, "seqs"),
-                                       _slots(cache, add, "add", n), n, copies.data_ptr(),
-                                       (copies.shape[0] - 2) // 2, ws.data_ptr(), wb, on.handle),
-               "bitnet_cache_extend")
+    dev, n = cache._dev, seqs.shape[0]
+    if dev != _current():
+        return _elsewhere(dev, bitnet_cache_extend, cache, seqs, add, copies, workspace, stream)
+    copies, cp, room = _copies(cache, n, copies, stream)
+    ws, wp, wb = _scratch(cache, workspace, cache.workspace_size(n), stream)
+    st = lib.bitnet_cache_extend(cache._ref, _slots(cache, seqs, "seqs", n),
+                                 _slots(cache, add, "add", n), n, cp, room, wp, wb,
+                                 _handle(stream, dev))
+    if st:
+        _check(st, "bitnet_cache_extend")
     return copies
 
 
 def bitnet_cache_free(cache: PagedCache, seqs: torch.Tensor,
                       workspace: Optional[torch.Tensor] = None, stream=None) -> None:
     """Slots seqs[i] become empty."""
-    n = seqs.shape[0]
-    if n == 0:
-        return
-    with _Launch(cache.device, stream) as on:
-        ws, wb = _cache_ws(cache, on, n, workspace)
-        _check(lib.bitnet_cache_free(cache._ref, _slots(cache, seqs, "seqs"), n, ws.data_ptr(), wb,
-                                     on.handle), "bitnet_cache_free")
+    dev, n = cache._dev, seqs.shape[0]
+    if dev != _current():
+        return _elsewhere(dev, bitnet_cache_free, cache, seqs, workspace, stream)
+    ws, wp, wb = _scratch(cache, workspace, cache.workspace_size(n), stream)
+    st = lib.bitnet_cache_free(cache._ref, _slots(cache, seqs, "seqs", n), n, wp, wb,
+                               _handle(stream, dev))
+    if st:
+        _check(st, "bitnet_cache_free")
 
 
 def bitnet_cache_compact(cache: PagedCache, copies: Optional[torch.Tensor] = None,
                          workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Moves the pages in use to the front of the pool. Returns the moves for bitnet_cache_copy,
     which must run before the cache is read or written again."""
-    with _Launch(cache.device, stream) as on:
-        copies = _copies(cache, on, cache.num_pages // 2, copies)
-        ws, wb = _cache_ws(cache, on, 0, workspace)
-        _check(lib.bitnet_cache_compact(cache._ref, copies.data_ptr(), (copies.shape[0] - 2) // 2,
-                                        ws.data_ptr(), wb, on.handle), "bitnet_cache_compact")
+    dev = cache._dev
+    if dev != _current():
+        return _elsewhere(dev, bitnet_cache_compact, cache, copies, workspace, stream)
+    copies, cp, room = _copies(cache, cache.num_pages // 2, copies, stream)
+    ws, wp, wb = _scratch(cache, workspace, cache.workspace_size(0), stream)
+    st = lib.bitnet_cache_compact(cache._ref, cp, room, wp, wb, _handle(stream, dev))
+    if st:
+        _check(st, "bitnet_cache_compact")
     return copies
 
 
 def bitnet_cache_copy(cache: PagedCache, copies: torch.Tensor, stream=None) -> None:
     """Copies pages from -> to in every layer of the cache, for a list that bitnet_cache_extend or
     bitnet_cache_compact returned."""
-    room = (copies.shape[0] - 2) // 2
-    if copies.dim() != 1 or room < 0:
+    dev = cache._dev
+    if dev != _current():
+        return _elsewhere(dev, bitnet_cache_copy, cache, copies, stream)
+    if copies.dim() != 1 or copies.shape[0] < 2:
         raise ValueError("copies must be [count, 0, from, to, ...]")
-    with _Launch(cache.device, stream) as on:
-        _check(lib.bitnet_cache_copy(cache._ref, cache._layers, len(cache.layers),
-                                     _on(copies, torch.int32, cache.device, "copies"), room,
-                                     on.handle), "bitnet_cache_copy")
+    st = lib.bitnet_cache_copy(cache._ref, cache._layers, len(cache.layers),
+                               _on(copies, torch.int32, dev, "copies"),
+                               (copies.shape[0] - 2) // 2, _handle(stream, dev))
+    if st:
+        _check(st, "bitnet_cache_copy")
 
 
 def bitnet_cache_append(cache: PagedCache, layer: int, k: torch.Tensor, v: torch.Tensor,
@@ -827,28 +851,22 @@ def bitnet_cache_append(cache: PagedCache, layer: int, k: torch.Tensor, v: torch
                         stream=None) -> None:
     """Writes T tokens, k and v (T, kv_heads, head_dim) or (T, kv_heads * head_dim) bf16, into a
     layer's pages: token t at position pos[t] (default: the last) of slot seqs[t] (default: t)."""
-    T = k.shape[0]
+    dev, T = cache._dev, k.shape[0]
+    if dev != _current():
+        return _elsewhere(dev, bitnet_cache_append, cache, layer, k, v, seqs, pos, stream)
     flat, heads = (T, cache.kv_heads * cache.head_dim), (T, cache.kv_heads, cache.head_dim)
-    if tuple(k.shape) not in (flat, heads) or tuple(v.shape) not in (flat, heads):
+    if k.shape not in (flat, heads) or v.shape not in (flat, heads):
         raise ValueError(f"k and v must be (T, {cache.kv_heads}, {cache.head_dim}), got "
                          f"{tuple(k.shape)} and {tuple(v.shape)}")
-    if T == 0:
-        return
     if seqs is None and T > cache.max_seqs:
         raise ValueError(f"{T} tokens for {cache.max_seqs} slots: give seqs")
-    with _Launch(cache.device, stream) as on:
-        _check(lib.bitnet_cache_append(
-            cache._ref, cache.layer(layer), _on(k, torch.bfloat16, cache.device, "k"),
-            _on(v, torch.bfloat16, cache.device, "v"), T,
-            None if seqs is None else _slots(cache, seqs, "seqs", T),
-            None if pos is None else _slots(cache, pos, "pos", T), on.handle),
-            "bitnet_cache_append")
-
-
-@functools.lru_cache(maxsize=4096)
-def _attention_ws(kv_heads: int, head_dim: int, B: int, heads: int) -> int:
-    c = bitnet_cache(1 << 8, 1 << 8, 1 << 8, 1 << 8, 1, 1, 1, 16, kv_heads, head_dim, CACHE_BF16)
-    return int(lib.bitnet_paged_attention_workspace_size(ctypes.byref(c), B, heads))
+    st = lib.bitnet_cache_append(
+        cache._ref, cache._layer(layer), _on(k, torch.bfloat16, dev, "k"),
+        _on(v, torch.bfloat16, dev, "v"), T,
+        None if seqs is None else _slots(cache, seqs, "seqs", T),
+        None if pos is None else _slots(cache, pos, "pos", T), _handle(stream, dev))
+    if st:
+        _check(st, "bitnet_cache_append")
 
 
 def bitnet_paged_attention(q: torch.Tensor, cache: PagedCache, layer: int = 0,
@@ -860,33 +878,39 @@ def bitnet_paged_attention(q: torch.Tensor, cache: PagedCache, layer: int = 0,
     bf16 over slot seqs[b] (default: b) of the cache. scale defaults to head_dim ** -0.5; window
     and sinks hide all but the first `sinks` and the last `window` tokens. Returns out (shaped as
     q), or (out, lse) with lse (B, heads) fp32 if return_lse or a tensor for it is given."""
-    D, B = cache.head_dim, q.shape[0]
-    heads = (q.shape[1] if q.dim() == 3 else q.numel() // max(B * D, 1))
-    if q.numel() != B * heads * D or (q.dim() == 3 and q.shape[2] != D) or q.dim() not in (2, 3):
-        raise ValueError(f"q must be (B, heads, {D}), got {tuple(q.shape)}")
+    dev, D = cache._dev, cache.head_dim
+    if dev != _current():
+        return _elsewhere(dev, bitnet_paged_attention, q, cache, layer, seqs, scale, window, sinks,
+                          out, return_lse, lse, workspace, stream)
+    shape = q.shape
+    B = shape[0]
+    if len(shape) == 3 and shape[2] == D:
+        heads = shape[1]
+    elif len(shape) == 2 and shape[1] % D == 0:
+        heads = shape[1] // D
+    else:
+        raise ValueError(f"q must be (B, heads, {D}), got {tuple(shape)}")
     if seqs is None and B > cache.max_seqs:
         raise ValueError(f"{B} queries for {cache.max_seqs} slots: give seqs")
-    dev = cache.device
-    with _Launch(dev, stream) as on:
-        if out is None:
-            out = on.keep(torch.empty_like(q))
-        elif out.shape != q.shape:
-            raise ValueError(f"out must be {tuple(q.shape)}, got {tuple(out.shape)}")
-        if lse is None and return_lse:
-            lse = on.scratch(B * heads, torch.float32, dev).view(B, heads)
-        elif lse is not None and tuple(lse.shape) != (B, heads):
-            raise ValueError(f"lse must be ({B}, {heads}), got {tuple(lse.shape)}")
-        if workspace is None:
-            workspace = on.scratch(_attention_ws(cache.kv_heads, D, B, heads), torch.uint8, dev)
-        elif workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be contiguous on {dev}")
-        _check(lib.bitnet_paged_attention(
-            cache._ref, cache.layer(layer), _on(q, torch.bfloat16, dev, "q"), B, heads,
-            None if seqs is None else _slots(cache, seqs, "seqs", B),
-            D ** -0.5 if scale is None else scale, window, sinks,
-            _on(out, torch.bfloat16, dev, "out"),
-            None if lse is None else _on(lse, torch.float32, dev, "lse"), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), on.handle), "bitnet_paged_attention")
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
+        _keep(stream, out)
+    elif out.shape != shape:
+        raise ValueError(f"out must be {tuple(shape)}, got {tuple(out.shape)}")
+    if lse is None:
+        if return_lse:
+            lse = torch.empty((B, heads), dtype=torch.float32, device=cache.device)
+            _keep(stream, lse)
+    elif lse.shape != (B, heads):
+        raise ValueError(f"lse must be ({B}, {heads}), got {tuple(lse.shape)}")
+    ws, wp, wb = _scratch(cache, workspace, cache.attention_workspace_size(B, heads), stream)
+    st = lib.bitnet_paged_attention(
+        cache._ref, cache._layer(layer), _on(q, torch.bfloat16, dev, "q"), B, heads,
+        None if seqs is None else _slots(cache, seqs, "seqs", B), D ** -0.5 if scale is None else scale,
+        window, sinks, _on(out, torch.bfloat16, dev, "out"),
+        None if lse is None else _on(lse, torch.float32, dev, "lse"), wp, wb, _handle(stream, dev))
+    if st:
+        _check(st, "bitnet_paged_attention")
     return out if lse is None else (out, lse)
 
 

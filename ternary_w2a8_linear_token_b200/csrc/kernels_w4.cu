@@ -3,6 +3,8 @@
 #include <cuda_runtime.h>
 
 #include "act_quant_device.cuh"
+#include "bitnet_device.cuh"
+#include "bitnet_internal.h"
 #include "cache_internal.h"
 
 namespace bitnet {
@@ -47,41 +49,202 @@ __global__ void __launch_bounds__(kW4Threads) pack_w4_kernel(const float* __rest
         scales[n * ((K + group - 1) / group) + k / group] = __bfloat16_as_ushort(sb);
 }
 
-// The forward, plainly: one warp per weight row, a lane per word of 8 weights, one token after
-// the other.
-__global__ void __launch_bounds__(kW4Threads) linear_w4_kernel(
-    const uint16_t* __restrict__ x, int64_t M, int64_t K, const uint8_t* __restrict__ packed,
-    const uint16_t* __restrict__ scales, int group, int64_t N, void* __restrict__ y, int out_f32) {
-    const int lane = threadIdx.x & 31;
-    const int64_t n = int64_t(blockIdx.x) * (kW4Threads / 32) + (threadIdx.x >> 5);
-    if (n >= N) return;
-    const uint32_t* row = reinterpret_cast<const uint32_t*>(packed + n * w4_row_bytes(K));
-    const uint16_t* srow = scales + n * ((K + group - 1) / group);
-    for (int64_t m = 0; m < M; ++m) {
-        float acc = 0.0f;
-        for (int64_t wd = lane; wd * 8 < w4_row_bytes(K) * 2; wd += 32) {
-            const int64_t k = wd / 16 * 128 + wd % 4 * 32 + wd % 16 / 4 * 8;
-            if (k >= K) continue;
-            const uint32_t word = row[wd];
-            const uint4 xv = *reinterpret_cast<const uint4*>(x + m * K + k);
-            const uint32_t xs[4] = {xv.x, xv.y, xv.z, xv.w};
-            float part = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                part += bf16_lo(xs[i]) * float(int(word >> (4 * i) & 15) - 8);
-                part += bf16_hi(xs[i]) * float(int(word >> (4 * i + 16) & 15) - 8);
+// The forward. Bound by HBM: half a byte per weight, read once per tile of up to 32 tokens; the
+// arithmetic is there to keep up with it (two weights per bf16 instruction, the products on
+// mma.sync with 16 weight rows as its rows and 8 tokens as its columns, so one to eight tokens cost
+// the same; tcgen05 has no use for 16-row tiles, and its operands would have to be unpacked into
+// shared or tensor memory first).
+//
+// Rows are dealt out evenly, rows N c / G .. N (c + 1) / G to CTA c of G, in tiles of 16; the eight
+// warps of a CTA take every eighth block of 128 weights of a tile (512 bytes of a row per step of
+// the CTA) and add their sums in shared memory, in order. A warp's next P blocks (P KB) are
+// always on their way in registers, across tiles, the first of them before the previous kernel
+// of the stream has ended (weights do not depend on it).
+constexpr int kW4Warps = kW4Threads / 32;
+constexpr int kW4Pad = 20;  // floats per token in the reduction buffer: no bank conflicts
+
+struct W4Params {
+    const uint16_t* x;
+    const uint8_t* packed;
+    const uint16_t* scales;
+    void* y;
+    int64_t K, N, M;
+    int32_t blocks;  // of 128 weights per row
+    int32_t groups;  // scales per row
+    int32_t out_f32;
+};
+
+__device__ __forceinline__ uint4 load_stream(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+// Weights 2 i and 2 i + 1 of a word as a bf16 pair, exactly: 128 + code, less 136.
+__device__ __forceinline__ uint32_t w4_pair(uint32_t word, int i) {
+    const uint32_t v = (word >> (4 * i) & 0x000F000Fu) | 0x43004300u;
+    uint32_t r;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x43084308u));
+    return r;
+}
+
+__device__ __forceinline__ void w4_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                       uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// NT: tiles of 8 tokens; NG: groups per block (1, 2 or 4); P: blocks in flight per warp.
+template <int NT, int NG, int P>
+__global__ void __launch_bounds__(kW4Threads, NT == 4 ? 1 : 2)
+    linear_w4_kernel(const __grid_constant__ W4Params p) {
+    __shared__ float red[2][kW4Warps][NT * 8 * kW4Pad];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+    const int64_t r0 = p.N * blockIdx.x / gridDim.x, r1 = p.N * (blockIdx.x + 1) / gridDim.x;
+    const int64_t m0 = int64_t(blockIdx.y) * (8 * NT);
+    const int tiles = static_cast<int>((r1 - r0 + 15) / 16);
+    const int mine = (p.blocks - warp + kW4Warps - 1) / kW4Warps;  // this warp's blocks of a tile
+    const int64_t row_bytes = int64_t(p.blocks) * 64;
+
+    uint4 wa[P], wb[P];
+    uint32_t sa[P], sb[P];  // bf16 bits: scales of rows g and g + 8, of group c if NG > 1
+    int lt = 0, lb = 0;     // the next tile and block (of this warp's) to load
+    auto load = [&](int i) {
+        wa[i] = wb[i] = make_uint4(0, 0, 0, 0);
+        sa[i] = sb[i] = 0;
+        if (lt < tiles) {
+            const int blk = warp + lb * kW4Warps;
+            const int64_t ra = r0 + lt * 16 + g;
+            const int sg = blk * NG + (NG > 1 ? c : 0);
+            const bool scaled = sg < p.groups && (NG == 1 || c < NG);
+            if (ra < r1) {
+                wa[i] = load_stream(p.packed + ra * row_bytes + blk * 64 + c * 16);
+                if (scaled) sa[i] = __ldg(p.scales + ra * p.groups + sg);
             }
-            acc += part * __uint_as_float(uint32_t(srow[k / group]) << 16);
+            if (ra + 8 < r1) {
+                wb[i] = load_stream(p.packed + (ra + 8) * row_bytes + blk * 64 + c * 16);
+                if (scaled) sb[i] = __ldg(p.scales + (ra + 8) * p.groups + sg);
+            }
+            if (++lb == mine) {
+                lb = 0;
+                ++lt;
+            }
         }
+    };
+
+    pdl_trigger();
+    if (mine > 0) {
 #pragma unroll
-        for (int d = 16; d; d >>= 1) acc += __shfl_xor_sync(0xFFFFFFFFu, acc, d);
-        if (lane == 0) {
-            if (out_f32)
-                static_cast<float*>(y)[m * N + n] = acc;
-            else
-                static_cast<__nv_bfloat16*>(y)[m * N + n] = __float2bfloat16_rn(acc);
+        for (int i = 0; i < P; ++i) load(i);
+    }
+    pdl_wait();
+
+    float acc[NT][4] = {};
+    int tile = 0, bi = 0;
+    auto finish = [&]() {  // a tile is done: the warps' sums, in order
+        float* mybuf = red[tile & 1][warp];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                mybuf[(8 * t + 2 * c + (e & 1)) * kW4Pad + g + 8 * (e >> 1)] = acc[t][e];
+                acc[t][e] = 0.0f;
+            }
+        __syncthreads();  // (two buffers: the next tile writes the other one)
+        for (int i = threadIdx.x; i < NT * 128; i += kW4Threads) {
+            const int64_t m = m0 + (i >> 4), n = r0 + tile * 16 + (i & 15);
+            float v = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kW4Warps; ++w) v += red[tile & 1][w][(i >> 4) * kW4Pad + (i & 15)];
+            if (m < p.M && n < r1) {
+                if (p.out_f32)
+                    static_cast<float*>(p.y)[m * p.N + n] = v;
+                else
+                    static_cast<__nv_bfloat16*>(p.y)[m * p.N + n] = __float2bfloat16_rn(v);
+            }
+        }
+        ++tile;
+        bi = 0;
+    };
+    if (mine <= 0) {  // more warps than blocks: nothing to add
+        while (tile < tiles) finish();
+        return;
+    }
+
+    while (tile < tiles) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            if (tile < tiles) {
+                const int64_t k0 = int64_t(warp + bi * kW4Warps) * 128 + 8 * c;
+                float part[NT][4] = {};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t a = (&wa[i].x)[j], b = (&wb[i].x)[j];
+                    const bool inside = k0 + 32 * j < p.K;
+                    const uint32_t a0 = w4_pair(a, 0), a1 = w4_pair(a, 1), a2 = w4_pair(a, 2),
+                                   a3 = w4_pair(a, 3);
+                    const uint32_t b0 = w4_pair(b, 0), b1 = w4_pair(b, 1), b2 = w4_pair(b, 2),
+                                   b3 = w4_pair(b, 3);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        const int64_t m = m0 + 8 * t + g;
+                        uint4 xv = make_uint4(0, 0, 0, 0);
+                        if (inside && m < p.M)
+                            xv = __ldg(reinterpret_cast<const uint4*>(p.x + m * p.K + k0 + 32 * j));
+                        w4_mma(part[t], a0, b0, a1, b1, xv.x, xv.y);
+                        w4_mma(part[t], a2, b2, a3, b3, xv.z, xv.w);
+                    }
+                    constexpr int kWords = 4 / NG;
+                    if (j % kWords == kWords - 1) {  // a group ends
+                        uint32_t fa = sa[i], fb = sb[i];
+                        if (NG > 1) {
+                            fa = __shfl_sync(0xFFFFFFFFu, fa, (lane & ~3) + j / kWords);
+                            fb = __shfl_sync(0xFFFFFFFFu, fb, (lane & ~3) + j / kWords);
+                        }
+                        const float s0 = __uint_as_float(fa << 16), s1 = __uint_as_float(fb << 16);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            acc[t][0] += s0 * part[t][0];
+                            acc[t][1] += s0 * part[t][1];
+                            acc[t][2] += s1 * part[t][2];
+                            acc[t][3] += s1 * part[t][3];
+                            part[t][0] = part[t][1] = part[t][2] = part[t][3] = 0.0f;
+                        }
+                    }
+                }
+                load(i);
+                if (++bi == mine) finish();
+            }
         }
     }
+}
+
+template <int NT, int NG, int P>
+cudaError_t launch_w4(const W4Params& p, cudaStream_t stream) {
+    const int64_t tiles = (p.N + 15) / 16, most = int64_t(tc_num_sms()) * (NT == 4 ? 1 : 2);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles < most ? tiles : most),
+                       static_cast<unsigned>((p.M + 8 * NT - 1) / (8 * NT)));
+    cfg.blockDim = dim3(kW4Threads);
+    cfg.stream = stream;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, linear_w4_kernel<NT, NG, P>, p);
+}
+
+template <int NG>
+cudaError_t launch_w4_tokens(const W4Params& p, cudaStream_t stream) {
+    if (p.M <= 8) return launch_w4<1, NG, 4>(p, stream);
+    if (p.M <= 16) return launch_w4<2, NG, 3>(p, stream);
+    return launch_w4<4, NG, 4>(p, stream);
 }
 
 }  // namespace
@@ -98,9 +261,20 @@ cudaError_t launch_pack_w4(const float* W, int64_t N, int64_t K, int group, uint
 cudaError_t launch_linear_w4(const uint16_t* x, int64_t M, int64_t K, const uint8_t* packed,
                              const uint16_t* scales, int group, int64_t N, void* y, int out_f32,
                              cudaStream_t stream) {
-    linear_w4_kernel<<<static_cast<unsigned>((N + 7) / 8), kW4Threads, 0, stream>>>(
-        x, M, K, packed, scales, group, N, y, out_f32);
-    return cudaGetLastError();
+    W4Params p = {x, packed, scales, y, K, N, M, static_cast<int32_t>((K + 127) / 128),
+                  static_cast<int32_t>((K + group - 1) / group), out_f32};
+    // 65535 token tiles of 32 per launch; a launch more only past two million tokens.
+    constexpr int64_t kMost = 65535 * 32;
+    for (int64_t m = 0; m < M; m += kMost) {
+        p.x = x + m * K;
+        p.y = static_cast<char*>(y) + m * N * (out_f32 ? 4 : 2);
+        p.M = M - m < kMost ? M - m : kMost;
+        const cudaError_t e = group == 128  ? launch_w4_tokens<1>(p, stream)
+                              : group == 64 ? launch_w4_tokens<2>(p, stream)
+                                            : launch_w4_tokens<4>(p, stream);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace bitnet
