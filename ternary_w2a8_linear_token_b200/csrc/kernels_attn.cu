@@ -222,8 +222,8 @@ __device__ __forceinline__ uint32_t bytes_to_f16(uint32_t turned, bool odd) {
 // and one instead: 170 against ... µs).
 __device__ __forceinline__ uint32_t bytes_to_bf16(uint32_t w, bool odd) {
     if (odd) w >>= 8;
-    const uint32_t f = (w & 0x00FF00FFu) ^ 0x43804380u;
-    uint32_t t, r, q;
+    uint32_t f, t, r, q;
+    asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(f) : "r"(w), "n"(0x00FF00FF), "r"(0x43804380));
     asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(t) : "r"(f), "r"(0xC380C380u));  // - 256
     asm("fma.rn.relu.bf16x2 %0, %1, %2, %3;"
         : "=r"(r)

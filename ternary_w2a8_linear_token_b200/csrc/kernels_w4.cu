@@ -82,10 +82,14 @@ __device__ __forceinline__ uint4 load_stream(const void* p) {
     return v;
 }
 
-// Weights 2 i and 2 i + 1 of a word as a bf16 pair, exactly: 128 + code, less 136.
+// Weights 2 i and 2 i + 1 of a word as a bf16 pair, exactly: 128 + code, less 136. The mask and
+// the exponent go into one three-input logic instruction (written out: from C the compiler makes
+// two, and the logic pipe is what comes next after HBM).
 __device__ __forceinline__ uint32_t w4_pair(uint32_t word, int i) {
-    const uint32_t v = (word >> (4 * i) & 0x000F000Fu) | 0x43004300u;
-    uint32_t r;
+    uint32_t v, r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;"
+        : "=r"(v)
+        : "r"(word >> (4 * i)), "n"(0x000F000F), "r"(0x43004300));
     asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x43084308u));
     return r;
 }
@@ -113,27 +117,35 @@ __global__ void __launch_bounds__(kW4Threads, NT == 4 ? 1 : 2)
 
     uint4 wa[P], wb[P];
     uint32_t sa[P], sb[P];  // bf16 bits: scales of rows g and g + 8, of group c if NG > 1
-    int lt = 0, lb = 0;     // the next tile and block (of this warp's) to load
+    // Where the next block to load lies: this lane's 16 bytes of row g, and its scale.
+    const int rows = static_cast<int>(r1 - r0);
+    const uint8_t* wp = p.packed + (r0 + g) * row_bytes + warp * 64 + c * 16;
+    const uint16_t* sp = p.scales + (r0 + g) * p.groups + warp * NG + (NG > 1 ? c : 0);
+    const int64_t w8 = 8 * row_bytes, s8 = 8 * int64_t(p.groups);
+    int left = mine;      // blocks of the tile to load
+    int ra = g;           // row within the CTA's, `rows` and more behind the last tile
+    int sg = warp * NG + (NG > 1 ? c : 0);
     auto load = [&](int i) {
         wa[i] = wb[i] = make_uint4(0, 0, 0, 0);
         sa[i] = sb[i] = 0;
-        if (lt < tiles) {
-            const int blk = warp + lb * kW4Warps;
-            const int64_t ra = r0 + lt * 16 + g;
-            const int sg = blk * NG + (NG > 1 ? c : 0);
-            const bool scaled = sg < p.groups && (NG == 1 || c < NG);
-            if (ra < r1) {
-                wa[i] = load_stream(p.packed + ra * row_bytes + blk * 64 + c * 16);
-                if (scaled) sa[i] = __ldg(p.scales + ra * p.groups + sg);
-            }
-            if (ra + 8 < r1) {
-                wb[i] = load_stream(p.packed + (ra + 8) * row_bytes + blk * 64 + c * 16);
-                if (scaled) sb[i] = __ldg(p.scales + (ra + 8) * p.groups + sg);
-            }
-            if (++lb == mine) {
-                lb = 0;
-                ++lt;
-            }
+        const bool scaled = sg < p.groups && (NG != 2 || c < NG);
+        if (ra < rows) {
+            wa[i] = load_stream(wp);
+            if (scaled) sa[i] = __ldg(sp);
+        }
+        if (ra + 8 < rows) {
+            wb[i] = load_stream(wp + w8);
+            if (scaled) sb[i] = __ldg(sp + s8);
+        }
+        wp += kW4Warps * 64;
+        sp += kW4Warps * NG;
+        sg += kW4Warps * NG;
+        if (--left == 0) {
+            left = mine;
+            ra += 16;
+            wp += 2 * w8 - mine * (kW4Warps * 64);
+            sp += 2 * s8 - mine * (kW4Warps * NG);
+            sg -= mine * (kW4Warps * NG);
         }
     };
 
@@ -145,7 +157,16 @@ __global__ void __launch_bounds__(kW4Threads, NT == 4 ? 1 : 2)
     pdl_wait();
 
     float acc[NT][4] = {};
-    int tile = 0, bi = 0;
+    int tile = 0, todo = mine;
+    // This lane's x: token 8 t + g of the tile, 8 values of the block (zeros without a token).
+    const uint16_t* xp[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const int64_t m = m0 + 8 * t + g;
+        xp[t] = m < p.M ? p.x + m * p.K + warp * 128 + 8 * c : nullptr;
+    }
+    // The last block is half empty if K is not a multiple of 128; it falls to one warp.
+    const bool cut = p.K % 128 != 0 && (p.blocks - 1) % kW4Warps == warp;
     auto finish = [&]() {  // a tile is done: the warps' sums, in order
         float* mybuf = red[tile & 1][warp];
 #pragma unroll
@@ -169,7 +190,7 @@ __global__ void __launch_bounds__(kW4Threads, NT == 4 ? 1 : 2)
             }
         }
         ++tile;
-        bi = 0;
+        todo = mine;
     };
     if (mine <= 0) {  // more warps than blocks: nothing to add
         while (tile < tiles) finish();
@@ -180,22 +201,21 @@ __global__ void __launch_bounds__(kW4Threads, NT == 4 ? 1 : 2)
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             if (tile < tiles) {
-                const int64_t k0 = int64_t(warp + bi * kW4Warps) * 128 + 8 * c;
+                const int64_t x0 = int64_t(mine - todo) * (kW4Warps * 128);
+                const bool half = cut && todo == 1;
                 float part[NT][4] = {};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const uint32_t a = (&wa[i].x)[j], b = (&wb[i].x)[j];
-                    const bool inside = k0 + 32 * j < p.K;
                     const uint32_t a0 = w4_pair(a, 0), a1 = w4_pair(a, 1), a2 = w4_pair(a, 2),
                                    a3 = w4_pair(a, 3);
                     const uint32_t b0 = w4_pair(b, 0), b1 = w4_pair(b, 1), b2 = w4_pair(b, 2),
                                    b3 = w4_pair(b, 3);
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
-                        const int64_t m = m0 + 8 * t + g;
                         uint4 xv = make_uint4(0, 0, 0, 0);
-                        if (inside && m < p.M)
-                            xv = __ldg(reinterpret_cast<const uint4*>(p.x + m * p.K + k0 + 32 * j));
+                        if (xp[t] && !(j >= 2 && half))
+                            xv = __ldg(reinterpret_cast<const uint4*>(xp[t] + x0 + 32 * j));
                         w4_mma(part[t], a0, b0, a1, b1, xv.x, xv.y);
                         w4_mma(part[t], a2, b2, a3, b3, xv.z, xv.w);
                     }
@@ -218,7 +238,7 @@ __global__ void __launch_bounds__(kW4Threads, NT == 4 ? 1 : 2)
                     }
                 }
                 load(i);
-                if (++bi == mine) finish();
+                if (--todo == 0) finish();
             }
         }
     }
