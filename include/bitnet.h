@@ -374,9 +374,13 @@ bitnet_status bitnet_linear_b3(const uint16_t* x, int64_t M, int64_t K, const ui
  *   binary32 (sums within a group, times the scale, added over the groups in a fixed order, so
  *   results are the same on every run), and y is rounded once at the end.
  *   A row of x that holds an Inf or NaN gives unspecified values in that row of y only.
+ *   Rows of up to BITNET_W4_MAX_GROUPS groups (BITNET_ERR_UNSUPPORTED beyond). Under programmatic
+ *   dependent launch the weights are read before the previous kernel of the stream has ended: a
+ *   kernel that writes them must not let its successors start early.
  * x, packed, W and y 16-byte aligned, scales 2-byte aligned. No workspace. Asynchronous on
  * `stream`; argument errors as for the other calls.
  */
+#define BITNET_W4_MAX_GROUPS 1024
 int64_t bitnet_w4_row_bytes(int64_t K);
 bitnet_status bitnet_pack_w4(const float* W, int64_t N, int64_t K, int32_t group,
                              uint8_t* packed, uint16_t* scales, void* stream);

@@ -98,6 +98,7 @@ bitnet_status bitnet_linear_w4(const uint16_t* x, int64_t M, int64_t K, const ui
     if ((st = check_n(N)) != BITNET_OK) return st;
     if (group != 32 && group != 64 && group != 128) return BITNET_ERR_UNSUPPORTED;
     if (out_dtype != BITNET_OUT_BF16 && out_dtype != BITNET_OUT_F32) return BITNET_ERR_UNSUPPORTED;
+    if (K > int64_t(group) * BITNET_W4_MAX_GROUPS) return BITNET_ERR_UNSUPPORTED;
     if (!aligned(x, 16) || !aligned(packed, 16) || !aligned(scales, 2) || !aligned(y, 16))
         return BITNET_ERR_ALIGN;
     return from_cuda(launch_linear_w4(x, M, K, packed, scales, group, N, y,

@@ -55,12 +55,17 @@ __global__ void __launch_bounds__(kW4Threads) pack_w4_kernel(const float* __rest
 // the same; tcgen05 has no use for 16-row tiles, and its operands would have to be unpacked into
 // shared or tensor memory first).
 //
-// Rows are dealt out evenly, rows N c / G .. N (c + 1) / G to CTA c of G, in tiles of 16; the eight
-// warps of a CTA take every eighth block of 128 weights of a tile (512 bytes of a row per step of
-// the CTA) and add their sums in shared memory, in order. A warp's next P blocks (P KB) are
-// always on their way in registers, across tiles, the first of them before the previous kernel
-// of the stream has ended (weights do not depend on it).
-constexpr int kW4Warps = kW4Threads / 32;
+// A CTA has two teams of eight warps. Rows are dealt out evenly, rows N t / T .. N (t + 1) / T to
+// team t of T, in tiles of 16 RT; a team's warps take every eighth block of 128 weights of a tile
+// (512 bytes of a row per step of the team) and add their sums in shared memory, in order. Every
+// warp loads its blocks through a ring of its own (cp.async, no barrier between warps), across
+// tiles, and fills it before the previous kernel of the stream has ended (weights do not depend on
+// it). x and the scales come from shared memory: read by fragments from global memory, the eight
+// rows of an instruction cost the L1 a tag lookup each.
+constexpr int kW4Warps = 8;  // of a team
+constexpr int kW4Teams = 2;
+constexpr int kW4Block = 32 * kW4Warps * kW4Teams;  // threads of a CTA
+constexpr int kW4Stages = 4;
 constexpr int kW4Pad = 20;  // floats per token in the reduction buffer: no bank conflicts
 
 struct W4Params {
@@ -74,11 +79,12 @@ struct W4Params {
     int32_t out_f32;
 };
 
-__device__ __forceinline__ uint4 load_stream(const void* p) {
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
+                 : "r"(at)
+                 : "memory");
     return v;
 }
 
@@ -103,168 +109,293 @@ __device__ __forceinline__ void w4_mma(float (&d)[4], uint32_t a0, uint32_t a1, 
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// NT: tiles of 8 tokens; NG: groups per block (1, 2 or 4); P: blocks in flight per warp.
-template <int NT, int NG, int P>
-__global__ void __launch_bounds__(kW4Threads, NT == 4 ? 1 : 2)
-    linear_w4_kernel(const __grid_constant__ W4Params p) {
-    __shared__ float red[2][kW4Warps][NT * 8 * kW4Pad];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
-    const int64_t r0 = p.N * blockIdx.x / gridDim.x, r1 = p.N * (blockIdx.x + 1) / gridDim.x;
-    const int64_t m0 = int64_t(blockIdx.y) * (8 * NT);
-    const int tiles = static_cast<int>((r1 - r0 + 15) / 16);
-    const int mine = (p.blocks - warp + kW4Warps - 1) / kW4Warps;  // this warp's blocks of a tile
-    const int64_t row_bytes = int64_t(p.blocks) * 64;
+// Shared memory of a call: the rings, the teams' reduction buffers, two tiles' scales for each team
+// (rows of an odd number of words, those of a last, half block filled up with zeros), and x as
+// (block, quarter, token, 64 bytes), zeros behind K.
+struct W4Layout {
+    uint32_t red, scales, x, bytes;  // offsets; the rings come first
+};
+__host__ __device__ inline int w4_scale_pitch(int filled) { return ((filled + 1) / 2 | 1) * 2; }
+__host__ __device__ inline W4Layout w4_layout(int nt, int ng, int rt, int blocks, int tokens,
+                                              bool xs) {
+    W4Layout l;
+    l.red = kW4Teams * kW4Warps * kW4Stages * rt * 1024;
+    l.scales = l.red + kW4Teams * kW4Warps * nt * 8 * rt * kW4Pad * 4;
+    l.x = l.scales + (kW4Teams * 2 * 16 * rt * 2 * w4_scale_pitch(blocks * ng) + 15) / 16 * 16;
+    l.bytes = l.x + (xs ? blocks * 256 * tokens : 0);
+    return l;
+}
 
-    uint4 wa[P], wb[P];
-    uint32_t sa[P], sb[P];  // bf16 bits: scales of rows g and g + 8, of group c if NG > 1
-    // Where the next block to load lies: this lane's 16 bytes of row g, and its scale.
-    const int rows = static_cast<int>(r1 - r0);
-    const uint8_t* wp = p.packed + (r0 + g) * row_bytes + warp * 64 + c * 16;
-    const uint16_t* sp = p.scales + (r0 + g) * p.groups + warp * NG + (NG > 1 ? c : 0);
-    const int64_t w8 = 8 * row_bytes, s8 = 8 * int64_t(p.groups);
-    int left = mine;      // blocks of the tile to load
-    int ra = g;           // row within the CTA's, `rows` and more behind the last tile
-    int sg = warp * NG + (NG > 1 ? c : 0);
+// NT: tiles of 8 tokens; NG: groups per block (1, 2 or 4); RT: tiles of 16 rows that share a load
+// of x; XS: x is in shared memory (otherwise read through L1).
+template <int NT, int NG, int RT, bool XS>
+__global__ void __launch_bounds__(kW4Block, 1)
+    linear_w4_kernel(const __grid_constant__ W4Params p) {
+    constexpr int S = kW4Stages;
+    constexpr int kRowsTile = 16 * RT;
+    constexpr int kStage = RT * 1024;      // bytes of a block of a tile
+    constexpr int kStep = kW4Warps * 64;   // bytes from one block of a warp to its next
+    constexpr int kHeld = 4;               // scales per lane and row that are prefetched
+    extern __shared__ __align__(128) uint8_t w4_dyn[];
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const int team = threadIdx.x >> 8, warp = threadIdx.x >> 5 & (kW4Warps - 1);
+    const int64_t teams = int64_t(gridDim.x) * kW4Teams;
+    const int64_t me = int64_t(blockIdx.x) * kW4Teams + team;
+    const int64_t r0 = p.N * me / teams, r1 = p.N * (me + 1) / teams;
+    const int64_t m0 = int64_t(blockIdx.y) * (8 * NT);
+    const int tokens = static_cast<int>(p.M - m0 < 8 * NT ? p.M - m0 : 8 * NT);
+    const int rows = static_cast<int>(r1 - r0), tiles = (rows + kRowsTile - 1) / kRowsTile;
+    // This warp's blocks of a tile (a team may be without rows).
+    const int mine = tiles ? (p.blocks - warp + kW4Warps - 1) / kW4Warps : 0;
+    const int64_t row_bytes = int64_t(p.blocks) * 64;
+    const int filled = p.blocks * NG, pitch = w4_scale_pitch(filled);
+    const W4Layout lay = w4_layout(NT, NG, RT, p.blocks, tokens, XS);
+    float* const red = reinterpret_cast<float*>(w4_dyn + lay.red) +
+                       team * (kW4Warps * NT * 8 * RT * kW4Pad);
+    uint16_t* const scales = reinterpret_cast<uint16_t*>(w4_dyn + lay.scales) +
+                             team * (2 * kRowsTile * pitch);
+    const uint32_t ring = smem_addr(w4_dyn) + (team * kW4Warps + warp) * (S * kStage);
+
+    // The blocks to load: tile, how many of it are left, and where this lane's 16 bytes of rows g,
+    // g + 8, ... lie (rows behind the team's last repeat that one and are not written).
+    int lt = 0, left = mine;
+    const uint8_t* from[2 * RT];
+    auto aim = [&]() {
+#pragma unroll
+        for (int r = 0; r < 2 * RT; ++r)
+            from[r] = p.packed + (r0 + min(lt * kRowsTile + 8 * r + g, rows - 1)) * row_bytes +
+                      warp * 64 + c * 16;
+    };
     auto load = [&](int i) {
-        wa[i] = wb[i] = make_uint4(0, 0, 0, 0);
-        sa[i] = sb[i] = 0;
-        const bool scaled = sg < p.groups && (NG != 2 || c < NG);
-        if (ra < rows) {
-            wa[i] = load_stream(wp);
-            if (scaled) sa[i] = __ldg(sp);
+        if (i < left) {
+#pragma unroll
+            for (int r = 0; r < 2 * RT; ++r)
+                cp_async16(ring + i * kStage + (8 * r + g) * 64 + c * 16, from[r] + i * kStep, true);
         }
-        if (ra + 8 < rows) {
-            wb[i] = load_stream(wp + w8);
-            if (scaled) sb[i] = __ldg(sp + s8);
+        cp_async_commit();
+    };
+    auto advance = [&]() {  // past S blocks
+        left -= S;
+#pragma unroll
+        for (int r = 0; r < 2 * RT; ++r) from[r] += S * kStep;
+        if (left <= 0) {
+            left = ++lt < tiles ? mine : 0;
+            if (left > 0) aim();
         }
-        wp += kW4Warps * 64;
-        sp += kW4Warps * NG;
-        sg += kW4Warps * NG;
-        if (--left == 0) {
-            left = mine;
-            ra += 16;
-            wp += 2 * w8 - mine * (kW4Warps * 64);
-            sp += 2 * s8 - mine * (kW4Warps * NG);
-            sg -= mine * (kW4Warps * NG);
+    };
+    // Scales of a tile: a warp brings rows warp, warp + 8, ..., in registers until the tile before it
+    // is done.
+    uint16_t held[2 * RT][kHeld];
+    auto scale_row = [&](int tile, int r) {
+        return p.scales + (r0 + min(tile * kRowsTile + 8 * r + warp, rows - 1)) * p.groups;
+    };
+    auto fetch_scales = [&](int tile) {
+#pragma unroll
+        for (int r = 0; r < 2 * RT; ++r)
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i)
+                held[r][i] = 32 * i + lane < p.groups ? __ldg(scale_row(tile, r) + 32 * i + lane) : 0;
+    };
+    auto store_scales = [&](int tile) {
+#pragma unroll
+        for (int r = 0; r < 2 * RT; ++r) {
+            uint16_t* to = scales + ((tile & 1) * kRowsTile + 8 * r + warp) * pitch;
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i)
+                if (32 * i + lane < filled) to[32 * i + lane] = held[r][i];
+            for (int i = 32 * kHeld + lane; i < filled; i += 32)
+                to[i] = i < p.groups ? __ldg(scale_row(tile, r) + i) : uint16_t(0);
         }
+    };
+    auto team_sync = [&]() {
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(32 * kW4Warps) : "memory");
     };
 
     pdl_trigger();
-    if (mine > 0) {
+    if (tiles) {
+        aim();
 #pragma unroll
-        for (int i = 0; i < P; ++i) load(i);
+        for (int i = 0; i < S; ++i) load(i);
+        advance();
+        fetch_scales(0);
+        store_scales(0);
     }
     pdl_wait();
+    if (XS) {
+        for (int i = threadIdx.x; i < p.blocks * 16 * tokens; i += kW4Block) {
+            // 16 lanes copy a block (256 bytes) of one token
+            const int part = i & 15, at = i >> 4, blk = at / tokens, m = at - blk * tokens;
+            const int k = blk * 128 + part * 8;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (k < p.K) v = __ldg(reinterpret_cast<const uint4*>(p.x + (m0 + m) * p.K + k));
+            *reinterpret_cast<uint4*>(w4_dyn + lay.x + ((blk * 4 + (part >> 2)) * tokens + m) * 64 +
+                                      (part & 3) * 16) = v;
+        }
+    }
+    __syncthreads();
 
-    float acc[NT][4] = {};
-    int tile = 0, todo = mine;
-    // This lane's x: token 8 t + g of the tile, 8 values of the block (zeros without a token).
-    const uint16_t* xp[NT];
+    // This lane's x: token 8 t + g of the tile, 8 values of a quarter block. Columns behind the last
+    // token repeat it and are not written.
+    uint32_t xo[NT];
+    const uint16_t* xg[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-        const int64_t m = m0 + 8 * t + g;
-        xp[t] = m < p.M ? p.x + m * p.K + warp * 128 + 8 * c : nullptr;
+        const int m = min(8 * t + g, tokens - 1);
+        xo[t] = smem_addr(w4_dyn) + lay.x + uint32_t(warp * 4 * tokens + m) * 64 + c * 16;
+        xg[t] = p.x + (m0 + m) * p.K + warp * 128 + 8 * c;
     }
-    // The last block is half empty if K is not a multiple of 128; it falls to one warp.
-    const bool cut = p.K % 128 != 0 && (p.blocks - 1) % kW4Warps == warp;
-    auto finish = [&]() {  // a tile is done: the warps' sums, in order
-        float* mybuf = red[tile & 1][warp];
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                mybuf[(8 * t + 2 * c + (e & 1)) * kW4Pad + g + 8 * (e >> 1)] = acc[t][e];
-                acc[t][e] = 0.0f;
-            }
-        __syncthreads();  // (two buffers: the next tile writes the other one)
-        for (int i = threadIdx.x; i < NT * 128; i += kW4Threads) {
-            const int64_t m = m0 + (i >> 4), n = r0 + tile * 16 + (i & 15);
-            float v = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kW4Warps; ++w) v += red[tile & 1][w][(i >> 4) * kW4Pad + (i & 15)];
-            if (m < p.M && n < r1) {
-                if (p.out_f32)
-                    static_cast<float*>(p.y)[m * p.N + n] = v;
-                else
-                    static_cast<__nv_bfloat16*>(p.y)[m * p.N + n] = __float2bfloat16_rn(v);
-            }
-        }
-        ++tile;
-        todo = mine;
-    };
-    if (mine <= 0) {  // more warps than blocks: nothing to add
-        while (tile < tiles) finish();
-        return;
-    }
+    // Without XS the last block's empty half is not read; it falls to one warp.
+    const bool cut = !XS && p.K % 128 != 0 && (p.blocks - 1) % kW4Warps == warp;
 
-    while (tile < tiles) {
+    for (int tile = 0; tile < tiles; ++tile) {
+        if (tile + 1 < tiles) fetch_scales(tile + 1);
+        const int below = min(rows - tile * kRowsTile, kRowsTile);  // rows of this tile
+        float acc[RT][NT][4] = {};
+        const uint16_t* sa = scales + ((tile & 1) * kRowsTile + g) * pitch + warp * NG;
+        uint32_t xa = 0;  // bytes from the warp's first block of x to this one
+        int64_t xv0 = 0;
+        for (int todo = mine; todo > 0; todo -= S) {
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-            if (tile < tiles) {
-                const int64_t x0 = int64_t(mine - todo) * (kW4Warps * 128);
-                const bool half = cut && todo == 1;
-                float part[NT][4] = {};
+            for (int i = 0; i < S; ++i) {
+                if (i < todo) {
+                    cp_async_wait<S - 1>();
+                    __syncwarp();  // the block is in, from all lanes
+                    const uint32_t at = ring + i * kStage + g * 64 + c * 16;
+                    uint4 wa[RT], wb[RT];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t a = (&wa[i].x)[j], b = (&wb[i].x)[j];
-                    const uint32_t a0 = w4_pair(a, 0), a1 = w4_pair(a, 1), a2 = w4_pair(a, 2),
-                                   a3 = w4_pair(a, 3);
-                    const uint32_t b0 = w4_pair(b, 0), b1 = w4_pair(b, 1), b2 = w4_pair(b, 2),
-                                   b3 = w4_pair(b, 3);
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        uint4 xv = make_uint4(0, 0, 0, 0);
-                        if (xp[t] && !(j >= 2 && half))
-                            xv = __ldg(reinterpret_cast<const uint4*>(xp[t] + x0 + 32 * j));
-                        w4_mma(part[t], a0, b0, a1, b1, xv.x, xv.y);
-                        w4_mma(part[t], a2, b2, a3, b3, xv.z, xv.w);
+                    for (int r = 0; r < RT; ++r) {
+                        wa[r] = lds128(at + r * 1024);
+                        wb[r] = lds128(at + r * 1024 + 512);
                     }
-                    constexpr int kWords = 4 / NG;
-                    if (j % kWords == kWords - 1) {  // a group ends
-                        uint32_t fa = sa[i], fb = sb[i];
-                        if (NG > 1) {
-                            fa = __shfl_sync(0xFFFFFFFFu, fa, (lane & ~3) + j / kWords);
-                            fb = __shfl_sync(0xFFFFFFFFu, fb, (lane & ~3) + j / kWords);
-                        }
-                        const float s0 = __uint_as_float(fa << 16), s1 = __uint_as_float(fb << 16);
+                    float part[RT][NT][4] = {};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint4 xv[NT];
 #pragma unroll
                         for (int t = 0; t < NT; ++t) {
-                            acc[t][0] += s0 * part[t][0];
-                            acc[t][1] += s0 * part[t][1];
-                            acc[t][2] += s1 * part[t][2];
-                            acc[t][3] += s1 * part[t][3];
-                            part[t][0] = part[t][1] = part[t][2] = part[t][3] = 0.0f;
+                            xv[t] = make_uint4(0, 0, 0, 0);
+                            if (XS)
+                                xv[t] = lds128(xo[t] + xa + uint32_t(j * tokens) * 64);
+                            else if (j < 2 || !(cut && i == todo - 1))
+                                xv[t] = __ldg(reinterpret_cast<const uint4*>(xg[t] + xv0 + 32 * j));
+                        }
+#pragma unroll
+                        for (int r = 0; r < RT; ++r) {
+                            if (r && below <= 16 * r) continue;  // no such rows
+                            const uint32_t a = (&wa[r].x)[j], b = (&wb[r].x)[j];
+                            const uint32_t a0 = w4_pair(a, 0), a1 = w4_pair(a, 1),
+                                           a2 = w4_pair(a, 2), a3 = w4_pair(a, 3);
+                            const uint32_t b0 = w4_pair(b, 0), b1 = w4_pair(b, 1),
+                                           b2 = w4_pair(b, 2), b3 = w4_pair(b, 3);
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) {
+                                w4_mma(part[r][t], a0, b0, a1, b1, xv[t].x, xv[t].y);
+                                w4_mma(part[r][t], a2, b2, a3, b3, xv[t].z, xv[t].w);
+                            }
+                            constexpr int kWords = 4 / NG;
+                            if (j % kWords == kWords - 1) {  // a group ends
+                                const uint16_t* q = sa + 16 * r * pitch + j / kWords;
+                                const float s0 = __uint_as_float(uint32_t(q[0]) << 16);
+                                const float s1 = __uint_as_float(uint32_t(q[8 * pitch]) << 16);
+#pragma unroll
+                                for (int t = 0; t < NT; ++t) {
+                                    acc[r][t][0] += s0 * part[r][t][0];
+                                    acc[r][t][1] += s0 * part[r][t][1];
+                                    acc[r][t][2] += s1 * part[r][t][2];
+                                    acc[r][t][3] += s1 * part[r][t][3];
+                                    part[r][t][0] = part[r][t][1] = 0.0f;
+                                    part[r][t][2] = part[r][t][3] = 0.0f;
+                                }
+                            }
                         }
                     }
+                    __syncwarp();  // all lanes have read the stage
                 }
                 load(i);
-                if (--todo == 0) finish();
+                sa += kW4Warps * NG;
+                xa += uint32_t(kW4Warps * 256) * tokens;
+                xv0 += kW4Warps * 128;
+            }
+            advance();
+        }
+        // A tile is done: the warps' sums, in order.
+        float* own = red + warp * (NT * 8 * RT * kW4Pad);
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    own[((8 * t + 2 * c + (e & 1)) * RT + r) * kW4Pad + g + 8 * (e >> 1)] =
+                        acc[r][t][e];
+        if (tile + 1 < tiles) store_scales(tile + 1);
+        team_sync();
+        for (int i = threadIdx.x & (32 * kW4Warps - 1); i < NT * 8 * kRowsTile; i += 32 * kW4Warps) {
+            const int m = i / kRowsTile, row = i % kRowsTile;
+            const int64_t n = r0 + tile * kRowsTile + row;
+            float v = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kW4Warps; ++w)
+                v += red[(w * (NT * 8) + m) * (RT * kW4Pad) + (row >> 4) * kW4Pad + (row & 15)];
+            if (m < tokens && n < r1) {
+                const int64_t to = (m0 + m) * p.N + n;
+                if (p.out_f32)
+                    static_cast<float*>(p.y)[to] = v;
+                else
+                    static_cast<__nv_bfloat16*>(p.y)[to] = __float2bfloat16_rn(v);
             }
         }
+        team_sync();  // the buffer is free
     }
+    cp_async_wait<0>();
 }
 
-template <int NT, int NG, int P>
-cudaError_t launch_w4(const W4Params& p, cudaStream_t stream) {
-    const int64_t tiles = (p.N + 15) / 16, most = int64_t(tc_num_sms()) * (NT == 4 ? 1 : 2);
+static_assert(BITNET_W4_MAX_GROUPS == 1024, "what launch_w4_tokens finds room for");
+
+template <int NT, int NG, int RT, bool XS>
+cudaError_t launch_w4_as(const W4Params& p, uint32_t smem, cudaStream_t stream) {
+    auto kern = linear_w4_kernel<NT, NG, RT, XS>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    const int64_t ctas = (p.N + 15) / 16, sms = tc_num_sms();
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles < most ? tiles : most),
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas < sms ? ctas : sms),
                        static_cast<unsigned>((p.M + 8 * NT - 1) / (8 * NT)));
-    cfg.blockDim = dim3(kW4Threads);
+    cfg.blockDim = dim3(kW4Block);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute at;
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, linear_w4_kernel<NT, NG, P>, p);
+    return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
+constexpr uint32_t kW4Room = 227 * 1024;
+
+// x goes through shared memory where it fits.
+template <int NT, int NG, int RT>
+cudaError_t launch_w4(const W4Params& p, cudaStream_t stream) {
+    const int tokens = static_cast<int>(p.M < 8 * NT ? p.M : 8 * NT);
+    const uint32_t with_x = w4_layout(NT, NG, RT, p.blocks, tokens, true).bytes;
+    if (with_x <= kW4Room) return launch_w4_as<NT, NG, RT, true>(p, with_x, stream);
+    return launch_w4_as<NT, NG, RT, false>(
+        p, w4_layout(NT, NG, RT, p.blocks, tokens, false).bytes, stream);
+}
+
+// The tile shape: as many tokens as there are, up to 32, and two row tiles sharing the reads of x
+// where every team has more than one; smaller ones where the scales of long rows take the room
+// (with 8 or 16 tokens and one row tile BITNET_W4_MAX_GROUPS fit).
 template <int NG>
 cudaError_t launch_w4_tokens(const W4Params& p, cudaStream_t stream) {
-    if (p.M <= 8) return launch_w4<1, NG, 4>(p, stream);
-    if (p.M <= 16) return launch_w4<2, NG, 3>(p, stream);
-    return launch_w4<4, NG, 4>(p, stream);
+    auto fits = [&](int nt, int rt) { return w4_layout(nt, NG, rt, p.blocks, 0, false).bytes <= kW4Room; };
+    if (p.M > 16 && fits(4, 1)) return launch_w4<4, NG, 1>(p, stream);
+    if (p.M > 8) return launch_w4<2, NG, 1>(p, stream);
+    if (p.N > 16 * kW4Teams * int64_t(tc_num_sms()) && fits(1, 2))
+        return launch_w4<1, NG, 2>(p, stream);
+    return launch_w4<1, NG, 1>(p, stream);
 }
 
 }  // namespace

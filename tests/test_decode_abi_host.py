@@ -48,6 +48,7 @@ def test_w4_refusals(bn):
     assert pack(W=FAKE + 4) == lin(x=FAKE + 2) == lin(y=FAKE + 4) == bn.ERR_ALIGN
     assert lin(M=0) == lin(M=1 << 31) == bn.ERR_SHAPE
     assert lin(od=2) == lin(od=-1) == bn.ERR_UNSUPPORTED
+    assert lin(K=64 * 1024 + 64) == lin(K=32 * 1024 + 64, group=32) == bn.ERR_UNSUPPORTED
 
 
 def _cache(bn, **kw):

@@ -69,11 +69,14 @@ def test_linear_more_rows_than_one_wave(bn):
     _check(y, x, t, scales, 64)
 
 
-def test_linear_long_rows(bn):
-    x, t, scales = _case(5, 24, 64 * 1031, 128, 3)
+@pytest.mark.parametrize("M,K,group", [(5, 64 * 1031, 128), (2, 32768, 32), (1, 65536, 64),
+                                       (17, 32704, 32), (9, 32768, 32), (40, 131072, 128)])
+def test_linear_long_rows(bn, M, K, group):
+    """Up to the longest rows; x past what shared memory holds."""
+    x, t, scales = _case(M, 24, K, group, 3)
     y = bn.bitnet_linear_w4(x.cuda(), torch.from_numpy(ref.w4_pack_codes(t)).cuda(), scales.cuda(),
-                            128, out_dtype=torch.float32)
-    _check(y, x, t, scales, 128)
+                            group, out_dtype=torch.float32)
+    _check(y, x, t, scales, group)
 
 
 def test_rows_of_x_do_not_meet(bn):
