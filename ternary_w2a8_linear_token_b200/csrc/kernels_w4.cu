@@ -2,6 +2,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "act_quant_device.cuh"
 #include "bitnet_device.cuh"
 #include "bitnet_internal.h"
@@ -79,15 +81,6 @@ struct W4Params {
     int32_t out_f32;
 };
 
-__device__ __forceinline__ uint4 lds128(uint32_t at) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(at)
-                 : "memory");
-    return v;
-}
-
 // Weights 2 i and 2 i + 1 of a word as a bf16 pair, exactly: 128 + code, less 136. The mask and
 // the exponent go into one three-input logic instruction (written out: from C the compiler makes
 // two, and the logic pipe is what comes next after HBM).
@@ -107,6 +100,16 @@ __device__ __forceinline__ void w4_mma(float (&d)[4], uint32_t a0, uint32_t a1, 
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same on zeros.
+__device__ __forceinline__ void w4_mma_new(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                           uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 // Shared memory of a call: the rings, the teams' reduction buffers, two tiles' scales for each team
@@ -154,7 +157,8 @@ __global__ void __launch_bounds__(kW4Block, 1)
                        team * (kW4Warps * NT * 8 * RT * kW4Pad);
     uint16_t* const scales = reinterpret_cast<uint16_t*>(w4_dyn + lay.scales) +
                              team * (2 * kRowsTile * pitch);
-    const uint32_t ring = smem_addr(w4_dyn) + (team * kW4Warps + warp) * (S * kStage);
+    const uint8_t* const ring = w4_dyn + (team * kW4Warps + warp) * (S * kStage);
+    const uint32_t ring_at = smem_addr(ring);
 
     // The blocks to load: tile, how many of it are left, and where this lane's 16 bytes of rows g,
     // g + 8, ... lie (rows behind the team's last repeat that one and are not written).
@@ -170,7 +174,7 @@ __global__ void __launch_bounds__(kW4Block, 1)
         if (i < left) {
 #pragma unroll
             for (int r = 0; r < 2 * RT; ++r)
-                cp_async16(ring + i * kStage + (8 * r + g) * 64 + c * 16, from[r] + i * kStep, true);
+                cp_async16(ring_at + i * kStage + (8 * r + g) * 64 + c * 16, from[r] + i * kStep, true);
         }
         cp_async_commit();
     };
@@ -236,23 +240,76 @@ __global__ void __launch_bounds__(kW4Block, 1)
 
     // This lane's x: token 8 t + g of the tile, 8 values of a quarter block. Columns behind the last
     // token repeat it and are not written.
-    uint32_t xo[NT];
+    const uint8_t* xo[NT];
     const uint16_t* xg[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         const int m = min(8 * t + g, tokens - 1);
-        xo[t] = smem_addr(w4_dyn) + lay.x + uint32_t(warp * 4 * tokens + m) * 64 + c * 16;
+        xo[t] = w4_dyn + lay.x + (warp * 4 * tokens + m) * 64 + c * 16;
         xg[t] = p.x + (m0 + m) * p.K + warp * 128 + 8 * c;
     }
     // Without XS the last block's empty half is not read; it falls to one warp.
     const bool cut = !XS && p.K % 128 != 0 && (p.blocks - 1) % kW4Warps == warp;
+
+    // One block of 128 weights by the tile's first R row tiles (the others have no rows).
+    auto block = [&](auto R, const uint8_t* at, const uint16_t* sa, int xa, int64_t xv0, bool half,
+                     float (&acc)[RT][NT][4]) {
+        constexpr int kR = decltype(R)::value, kWords = 4 / NG;
+        uint4 wa[kR], wb[kR];
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+            wa[r] = *reinterpret_cast<const uint4*>(at + r * 1024);
+            wb[r] = *reinterpret_cast<const uint4*>(at + r * 1024 + 512);
+        }
+        float part[kR][NT][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint4 xv[NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                xv[t] = make_uint4(0, 0, 0, 0);
+                if (XS)
+                    xv[t] = *reinterpret_cast<const uint4*>(xo[t] + xa + j * tokens * 64);
+                else if (j < 2 || !half)
+                    xv[t] = __ldg(reinterpret_cast<const uint4*>(xg[t] + xv0 + 32 * j));
+            }
+#pragma unroll
+            for (int r = 0; r < kR; ++r) {
+                const uint32_t a = (&wa[r].x)[j], b = (&wb[r].x)[j];
+                const uint32_t a0 = w4_pair(a, 0), a1 = w4_pair(a, 1), a2 = w4_pair(a, 2),
+                               a3 = w4_pair(a, 3);
+                const uint32_t b0 = w4_pair(b, 0), b1 = w4_pair(b, 1), b2 = w4_pair(b, 2),
+                               b3 = w4_pair(b, 3);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    if (j % kWords == 0)
+                        w4_mma_new(part[r][t], a0, b0, a1, b1, xv[t].x, xv[t].y);
+                    else
+                        w4_mma(part[r][t], a0, b0, a1, b1, xv[t].x, xv[t].y);
+                    w4_mma(part[r][t], a2, b2, a3, b3, xv[t].z, xv[t].w);
+                }
+                if (j % kWords == kWords - 1) {  // a group ends
+                    const uint16_t* q = sa + 16 * r * pitch + j / kWords;
+                    const float s0 = __uint_as_float(uint32_t(q[0]) << 16);
+                    const float s1 = __uint_as_float(uint32_t(q[8 * pitch]) << 16);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        acc[r][t][0] += s0 * part[r][t][0];
+                        acc[r][t][1] += s0 * part[r][t][1];
+                        acc[r][t][2] += s1 * part[r][t][2];
+                        acc[r][t][3] += s1 * part[r][t][3];
+                    }
+                }
+            }
+        }
+    };
 
     for (int tile = 0; tile < tiles; ++tile) {
         if (tile + 1 < tiles) fetch_scales(tile + 1);
         const int below = min(rows - tile * kRowsTile, kRowsTile);  // rows of this tile
         float acc[RT][NT][4] = {};
         const uint16_t* sa = scales + ((tile & 1) * kRowsTile + g) * pitch + warp * NG;
-        uint32_t xa = 0;  // bytes from the warp's first block of x to this one
+        int xa = 0;  // bytes from the warp's first block of x to this one
         int64_t xv0 = 0;
         for (int todo = mine; todo > 0; todo -= S) {
 #pragma unroll
@@ -260,60 +317,17 @@ __global__ void __launch_bounds__(kW4Block, 1)
                 if (i < todo) {
                     cp_async_wait<S - 1>();
                     __syncwarp();  // the block is in, from all lanes
-                    const uint32_t at = ring + i * kStage + g * 64 + c * 16;
-                    uint4 wa[RT], wb[RT];
-#pragma unroll
-                    for (int r = 0; r < RT; ++r) {
-                        wa[r] = lds128(at + r * 1024);
-                        wb[r] = lds128(at + r * 1024 + 512);
-                    }
-                    float part[RT][NT][4] = {};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint4 xv[NT];
-#pragma unroll
-                        for (int t = 0; t < NT; ++t) {
-                            xv[t] = make_uint4(0, 0, 0, 0);
-                            if (XS)
-                                xv[t] = lds128(xo[t] + xa + uint32_t(j * tokens) * 64);
-                            else if (j < 2 || !(cut && i == todo - 1))
-                                xv[t] = __ldg(reinterpret_cast<const uint4*>(xg[t] + xv0 + 32 * j));
-                        }
-#pragma unroll
-                        for (int r = 0; r < RT; ++r) {
-                            if (r && below <= 16 * r) continue;  // no such rows
-                            const uint32_t a = (&wa[r].x)[j], b = (&wb[r].x)[j];
-                            const uint32_t a0 = w4_pair(a, 0), a1 = w4_pair(a, 1),
-                                           a2 = w4_pair(a, 2), a3 = w4_pair(a, 3);
-                            const uint32_t b0 = w4_pair(b, 0), b1 = w4_pair(b, 1),
-                                           b2 = w4_pair(b, 2), b3 = w4_pair(b, 3);
-#pragma unroll
-                            for (int t = 0; t < NT; ++t) {
-                                w4_mma(part[r][t], a0, b0, a1, b1, xv[t].x, xv[t].y);
-                                w4_mma(part[r][t], a2, b2, a3, b3, xv[t].z, xv[t].w);
-                            }
-                            constexpr int kWords = 4 / NG;
-                            if (j % kWords == kWords - 1) {  // a group ends
-                                const uint16_t* q = sa + 16 * r * pitch + j / kWords;
-                                const float s0 = __uint_as_float(uint32_t(q[0]) << 16);
-                                const float s1 = __uint_as_float(uint32_t(q[8 * pitch]) << 16);
-#pragma unroll
-                                for (int t = 0; t < NT; ++t) {
-                                    acc[r][t][0] += s0 * part[r][t][0];
-                                    acc[r][t][1] += s0 * part[r][t][1];
-                                    acc[r][t][2] += s1 * part[r][t][2];
-                                    acc[r][t][3] += s1 * part[r][t][3];
-                                    part[r][t][0] = part[r][t][1] = 0.0f;
-                                    part[r][t][2] = part[r][t][3] = 0.0f;
-                                }
-                            }
-                        }
-                    }
+                    const uint8_t* at = ring + i * kStage + g * 64 + c * 16;
+                    const bool half = cut && i == todo - 1;
+                    if (RT == 1 || below > 16)
+                        block(std::integral_constant<int, RT>(), at, sa, xa, xv0, half, acc);
+                    else
+                        block(std::integral_constant<int, 1>(), at, sa, xa, xv0, half, acc);
                     __syncwarp();  // all lanes have read the stage
                 }
                 load(i);
                 sa += kW4Warps * NG;
-                xa += uint32_t(kW4Warps * 256) * tokens;
+                xa += kW4Warps * 256 * tokens;
                 xv0 += kW4Warps * 128;
             }
             advance();
