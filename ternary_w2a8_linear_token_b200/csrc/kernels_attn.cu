@@ -792,22 +792,6 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     if (p.lse && d == 0) p.lse[at] = total > 0.0f ? (top + log2f(total)) * kLn2 : -INFINITY;
 }
 
-template <typename... A>
-cudaError_t launch_pdl(void (*kernel)(A...), unsigned grid, unsigned threads, size_t smem,
-                       cudaStream_t stream, A... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 // CTAs of the split: as many as the GPU holds at once, whatever the lengths will be.
 int attn_ctas(int head_dim, bool i8) {
     const int per = head_dim == 64 ? (i8 ? Shape<64, true>::kCtas : Shape<64, false>::kCtas)
@@ -818,14 +802,13 @@ int attn_ctas(int head_dim, bool i8) {
 template <int D, bool I8, int NH>
 cudaError_t launch_one(const AttnParams& p, cudaStream_t stream) {
     using Sh = Shape<D, I8>;
-    cudaError_t e = cudaFuncSetAttribute(attn_kernel<D, I8, NH>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
+    static std::atomic<uint64_t> allowed;
+    cudaError_t e = allow_smem(attn_kernel<D, I8, NH>, Sh::kSmem, allowed);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(attn_kernel<D, I8, NH>, static_cast<unsigned>(attn_ctas(D, I8)), kThreads,
-                   Sh::kSmem, stream, p);
+    e = launch_pdl(attn_kernel<D, I8, NH>, dim3(attn_ctas(D, I8)), kThreads, Sh::kSmem, stream, p);
     if (e != cudaSuccess) return e;
-    return launch_pdl(join_kernel<D>, static_cast<unsigned>(int64_t(p.B) * p.heads), kJoinThreads, 0,
-                      stream, p);
+    return launch_pdl(join_kernel<D>, dim3(static_cast<unsigned>(int64_t(p.B) * p.heads)),
+                      kJoinThreads, 0, stream, p);
 }
 
 template <int D, bool I8>

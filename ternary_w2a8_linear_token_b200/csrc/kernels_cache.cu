@@ -9,6 +9,8 @@
 #include <cuda_runtime.h>
 
 #include "act_quant_device.cuh"
+#include "bitnet_device.cuh"
+#include "bitnet_internal.h"
 #include "cache_internal.h"
 
 namespace bitnet {
@@ -97,15 +99,21 @@ __device__ __forceinline__ uint32_t live_word(const CacheView& c, int64_t base) 
     return word;
 }
 
-// Marks every slot of a list and reports slots that are out of range or named twice. All threads
-// of the CTA call it; *bad is shared and must be 0 on entry (and synchronised).
+// Marks every slot of a list and reports slots that are out of range or named twice: in a bitmap
+// in shared memory, or for more slots than that holds in the workspace. All threads of the CTA
+// call it; *bad is shared and must be 0 on entry (and synchronised).
+constexpr int kMarkWords = 4096;
 __device__ __forceinline__ void mark_slots(const CacheView& c, const Ws& w, const int32_t* also,
                                            const int32_t* seqs, int64_t n, int* bad) {
+    __shared__ uint32_t bits[kMarkWords];
+    const bool small = c.max_seqs <= 32 * kMarkWords;
     for (int64_t i = threadIdx.x; i < n; i += kPlanThreads) {
         const int32_t s = seqs[i];
         if (s < 0 || (also && also[i] < 0)) continue;
         if (s >= c.max_seqs || (also && also[i] >= c.max_seqs))
             atomicOr(bad, BITNET_CACHE_ERR_SEQ);
+        else if (small)
+            bits[s >> 5] = 0;
         else
             w.mark[s] = 0;
     }
@@ -113,29 +121,56 @@ __device__ __forceinline__ void mark_slots(const CacheView& c, const Ws& w, cons
     for (int64_t i = threadIdx.x; i < n; i += kPlanThreads) {
         const int32_t s = seqs[i];
         if (s < 0 || s >= c.max_seqs || (also && also[i] < 0)) continue;
-        if (atomicAdd(&w.mark[s], 1) != 0) atomicOr(bad, BITNET_CACHE_ERR_SEQ);
+        const bool again = small ? atomicOr(&bits[s >> 5], 1u << (s & 31)) >> (s & 31) & 1
+                                 : atomicAdd(&w.mark[s], 1) != 0;
+        if (again) atomicOr(bad, BITNET_CACHE_ERR_SEQ);
     }
 }
 
+// Pages j of an entry of a fork: shared by one more slot.
+__device__ __forceinline__ void fork_page(const CacheView& c, const Item& it, int64_t j) {
+    const int32_t p = c.table[int64_t(it.from) * c.max_pages + j];
+    c.table[int64_t(it.to) * c.max_pages + j] = p;
+    if (uint32_t(p) < uint32_t(c.num_pages))
+        atomicAdd(&c.refs[p], 1);
+    else
+        atomicOr(c.error, BITNET_CACHE_ERR_PAGE);
+}
+
+// Pages j of an entry of a free: held by one slot less.
+__device__ __forceinline__ void free_page(const CacheView& c, const Item& it, int64_t j) {
+    const int32_t p = c.table[int64_t(it.from) * c.max_pages + j];
+    if (uint32_t(p) < uint32_t(c.num_pages))
+        atomicSub(&c.refs[p], 1);
+    else
+        atomicOr(c.error, BITNET_CACHE_ERR_PAGE);
+}
+
 // Plans a fork (src given) or a free (src null): validates the list, then notes for each entry
-// the slots, pages and length, so that the apply grid reads no length that it also writes.
+// the slots, pages and length, so that what follows reads no length that it also writes. What
+// follows is the apply grid, or with `alone` the same CTA, a warp per entry: for small tables that
+// saves a launch (fork of 6 slots of up to 39 pages, both in a chain of calls: ... against ... µs).
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(CacheView c, Ws w, const int32_t* src,
-                                                            const int32_t* dst, int64_t n) {
+                                                            const int32_t* dst, int64_t n,
+                                                            int alone) {
     __shared__ int bad;
+    pdl_trigger();
     if (threadIdx.x == 0) bad = 0;
+    pdl_wait();
     __syncthreads();
     mark_slots(c, w, src, dst, n, &bad);
     for (int64_t i = threadIdx.x; i < n; i += kPlanThreads) {
         const int32_t to = dst[i], from = src ? src[i] : to;
         Item it = {-1, to, 0, 0};
         if (to >= 0 && from >= 0 && to < c.max_seqs && from < c.max_seqs) {
+            const int32_t len = c.lens[from];
             if (src && c.lens[to] != 0) atomicOr(&bad, BITNET_CACHE_ERR_SEQ);
-            it.len = c.lens[from];
-            if (!len_fits(c, it.len)) {
+            if (!len_fits(c, len)) {
                 atomicOr(&bad, BITNET_CACHE_ERR_LEN);
             } else {
+                it.len = len;
                 it.from = from;
-                it.pages = pages_of(c, it.len);
+                it.pages = pages_of(c, len);
             }
         }
         w.item[i] = it;
@@ -145,88 +180,80 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(CacheView c, Ws w, c
         w.head[0] = bad == 0;
         if (bad) atomicOr(c.error, bad);
     }
-}
-
-// Applies a planned fork: blockIdx.x walks the pages of a row in chunks, blockIdx.y the list.
-__global__ void __launch_bounds__(kApplyThreads) fork_kernel(CacheView c, Ws w, int64_t n) {
-    if (!w.head[0]) return;
-    for (int64_t i = blockIdx.y; i < n; i += gridDim.y) {
+    if (!alone || bad) return;
+    for (int64_t i = threadIdx.x >> 5; i < n; i += kPlanThreads / 32) {
         const Item it = w.item[i];
         if (it.from < 0) continue;
-        const int32_t* row = c.table + int64_t(it.from) * c.max_pages;
-        int32_t* to = c.table + int64_t(it.to) * c.max_pages;
-        for (int64_t j0 = int64_t(blockIdx.x) * kApplyChunk; j0 < it.pages;
-             j0 += int64_t(gridDim.x) * kApplyChunk) {
-#pragma unroll
-            for (int u = 0; u < kApplyChunk / kApplyThreads; ++u) {
-                const int64_t j = j0 + u * kApplyThreads + threadIdx.x;
-                if (j >= it.pages) continue;
-                const int32_t p = row[j];
-                to[j] = p;
-                if (uint32_t(p) < uint32_t(c.num_pages))
-                    atomicAdd(&c.refs[p], 1);
-                else
-                    atomicOr(c.error, BITNET_CACHE_ERR_PAGE);
-            }
+        for (int64_t j = threadIdx.x & 31; j < it.pages; j += 32) {
+            if (src)
+                fork_page(c, it, j);
+            else
+                free_page(c, it, j);
         }
-        if (blockIdx.x == 0 && threadIdx.x == 0) c.lens[it.to] = it.len;
+        if ((threadIdx.x & 31) == 0) c.lens[it.to] = src ? it.len : 0;
     }
 }
 
-// Applies a planned free.
-__global__ void __launch_bounds__(kApplyThreads) free_kernel(CacheView c, Ws w, int64_t n) {
+// Applies a planned fork or free: blockIdx.x walks the pages of a row in chunks, blockIdx.y the list.
+template <bool FORK>
+__global__ void __launch_bounds__(kApplyThreads) apply_kernel(CacheView c, Ws w, int64_t n) {
+    pdl_trigger();
+    pdl_wait();
     if (!w.head[0]) return;
     for (int64_t i = blockIdx.y; i < n; i += gridDim.y) {
         const Item it = w.item[i];
         if (it.from < 0) continue;
-        const int32_t* row = c.table + int64_t(it.from) * c.max_pages;
         for (int64_t j0 = int64_t(blockIdx.x) * kApplyChunk; j0 < it.pages;
              j0 += int64_t(gridDim.x) * kApplyChunk) {
 #pragma unroll
             for (int u = 0; u < kApplyChunk / kApplyThreads; ++u) {
                 const int64_t j = j0 + u * kApplyThreads + threadIdx.x;
                 if (j >= it.pages) continue;
-                const int32_t p = row[j];
-                if (uint32_t(p) < uint32_t(c.num_pages))
-                    atomicSub(&c.refs[p], 1);
+                if (FORK)
+                    fork_page(c, it, j);
                 else
-                    atomicOr(c.error, BITNET_CACHE_ERR_PAGE);
+                    free_page(c, it, j);
             }
         }
-        if (blockIdx.x == 0 && threadIdx.x == 0) c.lens[it.from] = 0;
+        if (blockIdx.x == 0 && threadIdx.x == 0) c.lens[it.to] = FORK ? it.len : 0;
     }
 }
 
 // Extend, in one CTA: validate, decide the copies on write, find the free pages, and only then
 // change the tables. Bound by latency: the list is short (one entry per sequence of a batch), and
-// 32768 reference counts are read per round until enough free ones are found.
+// 32768 reference counts are read per round until enough free ones are found. ONE: at most one
+// entry per thread, kept in registers between the steps instead of the workspace.
+template <bool ONE>
 __global__ void __launch_bounds__(kPlanThreads) extend_kernel(CacheView c, Ws w,
                                                               const int32_t* seqs,
                                                               const int32_t* add, int64_t n,
                                                               int32_t* copies) {
     __shared__ int bad;
-    __shared__ unsigned long long want;  // pages that the call needs
-    if (threadIdx.x == 0) {
-        bad = 0;
-        want = 0;
-    }
+    __shared__ long long wants[kPlanThreads / 32];
+    pdl_trigger();
+    if (threadIdx.x == 0) bad = 0;
+    pdl_wait();
     __syncthreads();
     const int32_t ps = 1 << c.page_shift;
     mark_slots(c, w, nullptr, seqs, n, &bad);
     // Item here: from = last page if it is shared and must not be written, else -1; to = slot
     // (-1: skipped); pages = pages held; len = length held.
+    Item own = {-1, -1, 0, 0};
+    int32_t own_add = 0;
+    auto item = [&](int64_t i) { return ONE ? own : w.item[i]; };
+    auto more = [&](int64_t i) { return ONE ? own_add : add[i]; };
     for (int64_t i = threadIdx.x; i < n; i += kPlanThreads) {
-        const int32_t s = seqs[i];
+        const int32_t s = seqs[i], grow = add[i];
         Item it = {-1, -1, 0, 0};
         if (s >= 0 && s < c.max_seqs) {
-            const int32_t len = c.lens[s], more = add[i];
-            if (more < 0 || !len_fits(c, len) || !len_fits(c, int64_t(len) + more)) {
+            const int32_t len = c.lens[s];
+            if (grow < 0 || !len_fits(c, len) || !len_fits(c, int64_t(len) + grow)) {
                 atomicOr(&bad, BITNET_CACHE_ERR_LEN);
             } else {
                 it.to = s;
                 it.pages = pages_of(c, len);
                 it.len = len;
-                if (more > 0 && (len & (ps - 1)) != 0) {
+                if (grow > 0 && (len & (ps - 1)) != 0) {
                     const int32_t p = c.table[int64_t(s) * c.max_pages + it.pages - 1];
                     if (uint32_t(p) >= uint32_t(c.num_pages)) {
                         atomicOr(&bad, BITNET_CACHE_ERR_PAGE);
@@ -238,7 +265,12 @@ __global__ void __launch_bounds__(kPlanThreads) extend_kernel(CacheView c, Ws w,
                 }
             }
         }
-        w.item[i] = it;
+        if (ONE) {
+            own = it;
+            own_add = grow;
+        } else {
+            w.item[i] = it;
+        }
     }
     __syncthreads();
     if (bad) {
@@ -250,22 +282,33 @@ __global__ void __launch_bounds__(kPlanThreads) extend_kernel(CacheView c, Ws w,
         return;
     }
     for (int64_t i = threadIdx.x; i < n; i += kPlanThreads) {
-        const int32_t p = w.item[i].from;
+        const int32_t p = item(i).from;
         if (p < 0) continue;
         atomicAdd(&w.a[p], 1);
         atomicMax(&w.b[p], static_cast<int32_t>(i));
     }
     __syncthreads();
+    long long want = 0;  // pages that the call needs
     for (int64_t i = threadIdx.x; i < n; i += kPlanThreads) {
-        Item it = w.item[i];
+        Item it = item(i);
         if (it.to < 0) continue;
-        if (it.from >= 0 && w.a[it.from] == c.refs[it.from] && w.b[it.from] == i)
-            w.item[i].from = it.from = -1;  // all holders grow, and this is the last: it keeps it
-        const int32_t grown = pages_of(c, it.len + add[i]);
-        atomicAdd(&want, static_cast<unsigned long long>(grown - it.pages + (it.from >= 0)));
+        if (it.from >= 0 && __ldcg(&w.a[it.from]) == c.refs[it.from] &&
+            __ldcg(&w.b[it.from]) == i) {
+            it.from = -1;  // all holders grow, and this is the last: it keeps the page
+            if (ONE)
+                own.from = -1;
+            else
+                w.item[i].from = -1;
+        }
+        want += pages_of(c, it.len + more(i)) - it.pages + (it.from >= 0);
     }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) want += __shfl_xor_sync(0xFFFFFFFFu, want, d);
+    if ((threadIdx.x & 31) == 0) wants[threadIdx.x >> 5] = want;
     __syncthreads();
-    const int64_t total = static_cast<int64_t>(want);
+    int64_t total = 0;
+#pragma unroll
+    for (int i = 0; i < kPlanThreads / 32; ++i) total += wants[i];
     // The lowest `total` free pages, ascending, into a (the marks in a and b are done with).
     int64_t found = 0;
     for (int64_t base = 0; base < c.num_pages && found < total; base += 32768) {
@@ -276,6 +319,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_kernel(CacheView c, Ws w,
         const int32_t first = static_cast<int32_t>(base) + 32 * threadIdx.x;
         for (; word && rank < total; word &= word - 1) w.a[rank++] = first + __ffs(word) - 1;
     }
+    __syncthreads();
     if (found < total) {
         if (threadIdx.x == 0) {
             atomicOr(c.error, BITNET_CACHE_ERR_FULL);
@@ -291,10 +335,10 @@ __global__ void __launch_bounds__(kPlanThreads) extend_kernel(CacheView c, Ws w,
         const int64_t i = i0 + threadIdx.x;
         Item it = {-1, -1, 0, 0};
         int need = 0, grown = 0;
-        if (i < n) it = w.item[i];
+        if (i < n) it = item(i);
         const bool cow = it.to >= 0 && it.from >= 0;
         if (it.to >= 0) {
-            grown = pages_of(c, it.len + add[i]);
+            grown = pages_of(c, it.len + more(i));
             need = grown - it.pages + cow;
         }
         int pages_all, copies_all;
@@ -305,9 +349,8 @@ __global__ void __launch_bounds__(kPlanThreads) extend_kernel(CacheView c, Ws w,
         if (it.to < 0) continue;
         int32_t* row = c.table + int64_t(it.to) * c.max_pages;
         if (cow) {
-            const int32_t p = w.a[rank];
             copies[2 + 2 * int64_t(slot)] = it.from;
-            copies[3 + 2 * int64_t(slot)] = p;
+            copies[3 + 2 * int64_t(slot)] = w.a[rank];
             atomicSub(&c.refs[it.from], 1);
         }
         for (int j = it.pages - cow; j < grown; ++j) {
@@ -315,7 +358,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_kernel(CacheView c, Ws w,
             row[j] = p;
             c.refs[p] = 1;
         }
-        c.lens[it.to] = it.len + add[i];
+        c.lens[it.to] = it.len + more(i);
     }
     if (threadIdx.x == 0) {
         copies[0] = copy_base;
@@ -323,79 +366,115 @@ __global__ void __launch_bounds__(kPlanThreads) extend_kernel(CacheView c, Ws w,
     }
 }
 
+// Slot s after a compaction: a[old] = new for its pages from `live` on.
+__device__ __forceinline__ void move_page(const CacheView& c, const Ws& w, int32_t live,
+                                          int32_t* entry) {
+    const int32_t p = *entry;
+    const int32_t to = uint32_t(p) >= uint32_t(c.num_pages) ? -1 : p < live ? p : w.a[p];
+    if (to < 0)
+        atomicOr(c.error, BITNET_CACHE_ERR_PAGE);
+    else if (to != p)
+        *entry = to;
+}
+
+// Pages that slot s holds, 0 (and a report) for a length that does not fit.
+__device__ __forceinline__ int32_t slot_pages(const CacheView& c, int64_t s, bool report) {
+    const int32_t len = c.lens[s];
+    if (len_fits(c, len)) return pages_of(c, len);
+    if (report) atomicOr(c.error, BITNET_CACHE_ERR_LEN);
+    return 0;
+}
+
 // Compact, first step, in one CTA: with L pages in use, pairs the used pages from L on with the
 // free ones below L, both ascending, moves their counts and leaves a[old] = new for the tables.
-// a[k] (free pages) and a[old] do not meet: k < L <= old.
+// a[k] (free pages) and a[old] do not meet: k < L <= old. `alone`: the same CTA rewrites the tables
+// too, a warp per slot.
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(CacheView c, Ws w,
-                                                                    int32_t* copies) {
+                                                                    int32_t* copies, int alone) {
+    pdl_trigger();
+    pdl_wait();
+    auto valid_of = [&](int64_t base) {
+        const int64_t rest = c.num_pages - (base + 32 * threadIdx.x);
+        return rest >= 32 ? ~0u : rest <= 0 ? 0u : (1u << rest) - 1;
+    };
     int live = 0;
+    uint32_t word = 0;  // of the last 32768 pages: all of them, in most pools
     for (int64_t base = 0; base < c.num_pages; base += 32768) {
-        const int64_t first = base + 32 * threadIdx.x;
-        const int64_t rest = c.num_pages - first;
-        const uint32_t valid = rest >= 32 ? ~0u : rest <= 0 ? 0u : (1u << rest) - 1;
         int all;
-        block_scan(__popc(live_word(c, base) & valid), &all);
+        word = live_word(c, base) & valid_of(base);
+        block_scan(__popc(word), &all);
         live += all;
     }
     int holes = 0, movers = 0;
     for (int64_t base = 0; base < c.num_pages; base += 32768) {
         const int32_t first = static_cast<int32_t>(base) + 32 * threadIdx.x;
-        const int64_t rest = c.num_pages - first, low = int64_t(live) - first;
-        const uint32_t valid = rest >= 32 ? ~0u : rest <= 0 ? 0u : (1u << rest) - 1;
+        const int64_t low = int64_t(live) - first;
         const uint32_t below = low >= 32 ? ~0u : low <= 0 ? 0u : (1u << low) - 1;
-        const uint32_t word = live_word(c, base) & valid;
+        const uint32_t valid = valid_of(base);
+        if (c.num_pages > 32768) word = live_word(c, base) & valid;
         uint32_t hole = ~word & valid & below, mover = word & ~below, dead = ~word & valid & ~below;
-        int all;
-        int rank = holes + block_scan(__popc(hole), &all);
-        holes += all;
+        int all;  // both counts in one scan: at most 32768 each
+        const int ranks = block_scan(__popc(hole) | __popc(mover) << 16, &all);
+        int rank = holes + (ranks & 0xFFFF);
         for (; hole; hole &= hole - 1) w.a[rank++] = first + __ffs(hole) - 1;
-        rank = movers + block_scan(__popc(mover), &all);
-        movers += all;
+        rank = movers + (uint32_t(ranks) >> 16);
         for (; mover; mover &= mover - 1) w.b[rank++] = first + __ffs(mover) - 1;
         for (; dead; dead &= dead - 1) w.a[first + __ffs(dead) - 1] = -1;  // nobody may hold it
+        holes += all & 0xFFFF;
+        movers += uint32_t(all) >> 16;
     }
     __syncthreads();
-    for (int k = threadIdx.x; k < movers; k += kPlanThreads) {
-        const int32_t from = w.b[k], to = w.a[k];
-        copies[2 + 2 * int64_t(k)] = from;
-        copies[3 + 2 * int64_t(k)] = to;
-        c.refs[to] = c.refs[from];
-        c.refs[from] = 0;
-        w.a[from] = to;
+    for (int k0 = threadIdx.x; k0 < movers; k0 += 4 * kPlanThreads) {
+        int32_t from[4], to[4], refs[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int k = k0 + u * kPlanThreads;
+            if (k < movers) {
+                from[u] = w.b[k];
+                to[u] = w.a[k];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (k0 + u * kPlanThreads < movers) refs[u] = c.refs[from[u]];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int64_t k = k0 + u * kPlanThreads;
+            if (k >= movers) continue;
+            *reinterpret_cast<int2*>(copies + 2 + 2 * k) = make_int2(from[u], to[u]);
+            c.refs[to[u]] = refs[u];
+            c.refs[from[u]] = 0;
+            w.a[from[u]] = to[u];
+        }
     }
     if (threadIdx.x == 0) {
         copies[0] = movers;
         copies[1] = 0;
         w.head[1] = live;
     }
+    if (!alone) return;
+    __syncthreads();
+    for (int64_t s = threadIdx.x >> 5; s < c.max_seqs; s += kPlanThreads / 32) {
+        const int32_t pages = slot_pages(c, s, (threadIdx.x & 31) == 0);
+        for (int32_t j = threadIdx.x & 31; j < pages; j += 32)
+            move_page(c, w, live, c.table + s * c.max_pages + j);
+    }
 }
 
 // Compact, second step: the tables. blockIdx.x walks a row in chunks, blockIdx.y the slots.
 __global__ void __launch_bounds__(kApplyThreads) compact_apply_kernel(CacheView c, Ws w) {
+    pdl_trigger();
+    pdl_wait();
     const int32_t live = w.head[1];
     for (int64_t s = blockIdx.y; s < c.max_seqs; s += gridDim.y) {
-        const int32_t len = c.lens[s];
-        if (len == 0) continue;
-        if (!len_fits(c, len)) {
-            if (threadIdx.x == 0) atomicOr(c.error, BITNET_CACHE_ERR_LEN);
-            continue;
-        }
-        const int32_t pages = pages_of(c, len);
+        const int32_t pages = slot_pages(c, s, threadIdx.x == 0);
         int32_t* row = c.table + s * c.max_pages;
         for (int64_t j0 = int64_t(blockIdx.x) * kApplyChunk; j0 < pages;
              j0 += int64_t(gridDim.x) * kApplyChunk) {
 #pragma unroll
             for (int u = 0; u < kApplyChunk / kApplyThreads; ++u) {
                 const int64_t j = j0 + u * kApplyThreads + threadIdx.x;
-                if (j >= pages) continue;
-                const int32_t p = row[j];
-                const int32_t to = uint32_t(p) >= uint32_t(c.num_pages) ? -1
-                                   : p < live                           ? p
-                                                                        : w.a[p];
-                if (to < 0)
-                    atomicOr(c.error, BITNET_CACHE_ERR_PAGE);
-                else
-                    row[j] = to;
+                if (j < pages) move_page(c, w, live, row + j);
             }
         }
     }
@@ -410,6 +489,8 @@ __global__ void __launch_bounds__(kApplyThreads) copy_kernel(CacheView c,
                                                              const __grid_constant__ CacheLayers l,
                                                              int nlayers, const int32_t* copies,
                                                              int64_t max_copies) {
+    pdl_trigger();
+    pdl_wait();
     const int64_t tokens = int64_t(c.kv_heads) << c.page_shift;
     const int64_t data = tokens * c.head_dim * (c.i8 ? 1 : 2), scale = tokens * 4;
     const int64_t du = (data + kCopyUnit - 1) / kCopyUnit;
@@ -452,53 +533,89 @@ __global__ void __launch_bounds__(kApplyThreads) copy_kernel(CacheView c,
     }
 }
 
-// Writes new tokens. One thread per 8 values of a (token, pool, head) row, so D / 8 neighbouring
-// lanes hold a row and its absolute maximum is a few shuffles away. Bound by HBM (K and V read
-// once, pages written once), or by launch latency for one token per sequence.
+// Writes new tokens. A CTA takes about 1024 pieces of 8 values (kv_heads * D / 4 pieces a token),
+// four per thread on their way at once, while some of its threads look up where the tokens go;
+// D / 8 neighbouring lanes hold a row, so its absolute maximum is one warp reduction away. Bound
+// by HBM (K and V read once, pages written once), or by latency for one token per sequence.
+constexpr int kAppendPieces = 4;
+constexpr int kAppendTokens = 64;  // tokens of a CTA: 1024 pieces of the smallest
+
 template <int D>
 __global__ void __launch_bounds__(kApplyThreads) append_kernel(CacheView c, bitnet_cache_layer lay,
                                                                const uint16_t* k,
                                                                const uint16_t* v, int64_t T,
-                                                               const int32_t* seqs,
+                                                               int tokens, const int32_t* seqs,
                                                                const int32_t* pos) {
     constexpr int kLanes = D / 8;
-    const int64_t rows = 2 * T * c.kv_heads;
-    const int64_t row = (int64_t(blockIdx.x) * kApplyThreads + threadIdx.x) / kLanes;
-    const int piece = threadIdx.x % kLanes;
-    if (row >= rows) return;  // kLanes neighbours leave together
-    const bool is_v = row >= T * c.kv_heads;
-    const int64_t r = is_v ? row - T * c.kv_heads : row;
-    const int64_t t = r / c.kv_heads;
-    const int head = static_cast<int>(r - t * c.kv_heads);
-    const int64_t s = seqs ? seqs[t] : t;
-    if (s < 0) return;
-    if (s >= c.max_seqs) {
-        if (piece == 0) atomicOr(c.error, BITNET_CACHE_ERR_SEQ);
-        return;
+    __shared__ int32_t rows[kAppendTokens];  // first row of the token in the pools, or -1
+    pdl_trigger();
+    pdl_wait();
+    const int64_t t0 = int64_t(blockIdx.x) * tokens;
+    const int here = static_cast<int>(T - t0 < tokens ? T - t0 : tokens);
+    const int half = c.kv_heads * kLanes;  // pieces of a token's K
+    const int pieces = here * 2 * half;
+    for (int p0 = 0; p0 < pieces; p0 += kAppendPieces * kApplyThreads) {
+        uint4 x[kAppendPieces];
+        int tok[kAppendPieces], at[kAppendPieces];
+#pragma unroll
+        for (int u = 0; u < kAppendPieces; ++u) {
+            const int p = p0 + u * kApplyThreads + threadIdx.x;
+            tok[u] = -1;
+            if (p >= pieces) continue;
+            tok[u] = p / (2 * half);
+            at[u] = p - tok[u] * 2 * half;
+            const bool is_v = at[u] >= half;
+            x[u] = __ldg(reinterpret_cast<const uint4*>(is_v ? v : k) + (t0 + tok[u]) * half +
+                         (is_v ? at[u] - half : at[u]));
+        }
+        if (p0 == 0) {
+            if (threadIdx.x < here) {
+                const int64_t t = t0 + threadIdx.x;
+                const int64_t s = seqs ? seqs[t] : t;
+                int32_t row = -1, err = 0;
+                if (s >= c.max_seqs) {
+                    err = BITNET_CACHE_ERR_SEQ;
+                } else if (s >= 0) {
+                    const int32_t len = c.lens[s], j = pos ? pos[t] : len - 1;
+                    if (j < 0 || j >= len || !len_fits(c, len)) {
+                        err = BITNET_CACHE_ERR_LEN;
+                    } else {
+                        const int32_t page = c.table[s * c.max_pages + (j >> c.page_shift)];
+                        if (uint32_t(page) >= uint32_t(c.num_pages))
+                            err = BITNET_CACHE_ERR_PAGE;
+                        else
+                            row = ((page * c.kv_heads) << c.page_shift) +
+                                  (j & ((1 << c.page_shift) - 1));
+                    }
+                }
+                if (err) atomicOr(c.error, err);
+                rows[threadIdx.x] = row;
+            }
+            __syncthreads();
+        }
+#pragma unroll
+        for (int u = 0; u < kAppendPieces; ++u) {
+            if (tok[u] < 0 || rows[tok[u]] < 0) continue;  // kLanes neighbours alike
+            const bool is_v = at[u] >= half;
+            const int in = is_v ? at[u] - half : at[u], head = in / kLanes, piece = in % kLanes;
+            const int64_t to = rows[tok[u]] + (head << c.page_shift);
+            if (!c.i8) {
+                reinterpret_cast<uint4*>(is_v ? lay.v : lay.k)[to * kLanes + piece] = x[u];
+                continue;
+            }
+            // bf16 magnitudes order as unsigned integers: an exact maximum over the row's lanes.
+            const uint32_t lanes = ((1u << kLanes) - 1) << (threadIdx.x & 31 & ~(kLanes - 1));
+            const float amax = bf16_lo(__reduce_max_sync(lanes, absmax8_bits(x[u])));
+            const float scale = __fdiv_rn(127.0f, fmaxf(amax, kActEps));
+            reinterpret_cast<uint2*>(is_v ? lay.v : lay.k)[to * kLanes + piece] = quant8(x[u], scale);
+            if (piece == 0) (is_v ? lay.v_scale : lay.k_scale)[to] = scale;
+        }
     }
-    const int32_t len = c.lens[s], at = pos ? pos[t] : len - 1;
-    if (at < 0 || at >= len || !len_fits(c, len)) {
-        if (piece == 0) atomicOr(c.error, BITNET_CACHE_ERR_LEN);
-        return;
-    }
-    const int32_t page = c.table[s * c.max_pages + (at >> c.page_shift)];
-    if (uint32_t(page) >= uint32_t(c.num_pages)) {
-        if (piece == 0) atomicOr(c.error, BITNET_CACHE_ERR_PAGE);
-        return;
-    }
-    const uint4 x = reinterpret_cast<const uint4*>(is_v ? v : k)[r * kLanes + piece];
-    const int64_t to = ((int64_t(page) * c.kv_heads + head) << c.page_shift) +
-                       (at & ((1 << c.page_shift) - 1));
-    if (!c.i8) {
-        reinterpret_cast<uint4*>(is_v ? lay.v : lay.k)[to * kLanes + piece] = x;
-        return;
-    }
-    // bf16 magnitudes order as unsigned integers: an exact maximum over the row's lanes.
-    const uint32_t lanes = ((1u << kLanes) - 1) << (threadIdx.x & 31 & ~(kLanes - 1));
-    const float amax = bf16_lo(__reduce_max_sync(lanes, absmax8_bits(x)));
-    const float scale = __fdiv_rn(127.0f, fmaxf(amax, kActEps));
-    reinterpret_cast<uint2*>(is_v ? lay.v : lay.k)[to * kLanes + piece] = quant8(x, scale);
-    if (piece == 0) (is_v ? lay.v_scale : lay.k_scale)[to] = scale;
+}
+
+// Whether one CTA applies a plan itself: up to eight rounds of a warp per row and 32 entries.
+bool applies_alone(const CacheView& c, int64_t rows) {
+    return ((rows + 31) / 32) * ((c.max_pages + 31) / 32) <= 8;
 }
 
 dim3 apply_grid(const CacheView& c, int64_t rows) {
@@ -512,52 +629,62 @@ dim3 apply_grid(const CacheView& c, int64_t rows) {
 cudaError_t launch_cache_fork(const CacheView& c, const int32_t* src, const int32_t* dst, int64_t n,
                               void* ws, cudaStream_t stream) {
     const Ws w = ws_split(c, ws);
-    plan_kernel<<<1, kPlanThreads, 0, stream>>>(c, w, src, dst, n);
-    fork_kernel<<<apply_grid(c, n), kApplyThreads, 0, stream>>>(c, w, n);
-    return cudaGetLastError();
+    const bool alone = applies_alone(c, n);
+    const cudaError_t e =
+        launch_pdl(plan_kernel, dim3(1), kPlanThreads, 0, stream, c, w, src, dst, n, int(alone));
+    if (e != cudaSuccess || alone) return e;
+    return launch_pdl(apply_kernel<true>, apply_grid(c, n), kApplyThreads, 0, stream, c, w, n);
 }
 
 cudaError_t launch_cache_free(const CacheView& c, const int32_t* seqs, int64_t n, void* ws,
                               cudaStream_t stream) {
     const Ws w = ws_split(c, ws);
-    plan_kernel<<<1, kPlanThreads, 0, stream>>>(c, w, nullptr, seqs, n);
-    free_kernel<<<apply_grid(c, n), kApplyThreads, 0, stream>>>(c, w, n);
-    return cudaGetLastError();
+    const bool alone = applies_alone(c, n);
+    const cudaError_t e = launch_pdl(plan_kernel, dim3(1), kPlanThreads, 0, stream, c, w,
+                                     static_cast<const int32_t*>(nullptr), seqs, n, int(alone));
+    if (e != cudaSuccess || alone) return e;
+    return launch_pdl(apply_kernel<false>, apply_grid(c, n), kApplyThreads, 0, stream, c, w, n);
 }
 
 cudaError_t launch_cache_extend(const CacheView& c, const int32_t* seqs, const int32_t* add,
                                 int64_t n, int32_t* copies, void* ws, cudaStream_t stream) {
-    extend_kernel<<<1, kPlanThreads, 0, stream>>>(c, ws_split(c, ws), seqs, add, n, copies);
-    return cudaGetLastError();
+    const Ws w = ws_split(c, ws);
+    return launch_pdl(n <= kPlanThreads ? extend_kernel<true> : extend_kernel<false>, dim3(1),
+                      kPlanThreads, 0, stream, c, w, seqs, add, n, copies);
 }
 
 cudaError_t launch_cache_compact(const CacheView& c, int32_t* copies, void* ws,
                                  cudaStream_t stream) {
     const Ws w = ws_split(c, ws);
-    compact_plan_kernel<<<1, kPlanThreads, 0, stream>>>(c, w, copies);
-    compact_apply_kernel<<<apply_grid(c, c.max_seqs), kApplyThreads, 0, stream>>>(c, w);
-    return cudaGetLastError();
+    const bool alone = applies_alone(c, c.max_seqs);
+    const cudaError_t e = launch_pdl(compact_plan_kernel, dim3(1), kPlanThreads, 0, stream, c, w,
+                                     copies, int(alone));
+    if (e != cudaSuccess || alone) return e;
+    return launch_pdl(compact_apply_kernel, apply_grid(c, c.max_seqs), kApplyThreads, 0, stream, c,
+                      w);
 }
 
 cudaError_t launch_cache_copy(const CacheView& c, const CacheLayers& layers, int nlayers,
                               const int32_t* copies, int64_t max_copies, cudaStream_t stream) {
-    copy_kernel<<<148 * 8, kApplyThreads, 0, stream>>>(c, layers, nlayers, copies, max_copies);
-    return cudaGetLastError();
+    // Eight CTAs an SM, or fewer where the list cannot hold work for them.
+    const int64_t tokens = int64_t(c.kv_heads) << c.page_shift;
+    const int64_t units = 2 * nlayers * max_copies *
+                          ((tokens * c.head_dim * (c.i8 ? 1 : 2) + kCopyUnit - 1) / kCopyUnit +
+                           (c.i8 ? (tokens * 4 + kCopyUnit - 1) / kCopyUnit : 0));
+    const int64_t most = int64_t(tc_num_sms()) * 8;
+    return launch_pdl(copy_kernel, dim3(static_cast<unsigned>(units < most ? units : most)),
+                      kApplyThreads, 0, stream, c, layers, nlayers, copies, max_copies);
 }
 
 cudaError_t launch_cache_append(const CacheView& c, const bitnet_cache_layer& layer,
                                 const uint16_t* k, const uint16_t* v, int64_t T,
                                 const int32_t* seqs, const int32_t* pos, cudaStream_t stream) {
-    const int64_t threads = 2 * T * c.kv_heads * (c.head_dim / 8);
-    const int64_t blocks = (threads + kApplyThreads - 1) / kApplyThreads;
-    if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
-    if (c.head_dim == 64)
-        append_kernel<64><<<static_cast<unsigned>(blocks), kApplyThreads, 0, stream>>>(
-            c, layer, k, v, T, seqs, pos);
-    else
-        append_kernel<128><<<static_cast<unsigned>(blocks), kApplyThreads, 0, stream>>>(
-            c, layer, k, v, T, seqs, pos);
-    return cudaGetLastError();
+    const int per = c.kv_heads * (c.head_dim / 4);  // pieces of a token
+    const int tokens = per >= kAppendPieces * kApplyThreads ? 1 : kAppendPieces * kApplyThreads / per;
+    const int64_t blocks = (T + tokens - 1) / tokens;
+    return launch_pdl(c.head_dim == 64 ? append_kernel<64> : append_kernel<128>,
+                      dim3(static_cast<unsigned>(blocks)), kApplyThreads, 0, stream, c, layer, k, v,
+                      T, tokens, seqs, pos);
 }
 
 }  // namespace bitnet

@@ -68,6 +68,7 @@ constexpr int kW4Warps = 8;  // of a team
 constexpr int kW4Teams = 2;
 constexpr int kW4Block = 32 * kW4Warps * kW4Teams;  // threads of a CTA
 constexpr int kW4Stages = 4;
+constexpr uint32_t kW4Room = 227 * 1024;  // shared memory of a CTA
 constexpr int kW4Pad = 20;  // floats per token in the reduction buffer: no bank conflicts
 
 struct W4Params {
@@ -369,25 +370,15 @@ static_assert(BITNET_W4_MAX_GROUPS == 1024, "what launch_w4_tokens finds room fo
 template <int NT, int NG, int RT, bool XS>
 cudaError_t launch_w4_as(const W4Params& p, uint32_t smem, cudaStream_t stream) {
     auto kern = linear_w4_kernel<NT, NG, RT, XS>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(smem));
+    static std::atomic<uint64_t> allowed;
+    const cudaError_t e = allow_smem(kern, kW4Room, allowed);
     if (e != cudaSuccess) return e;
     const int64_t ctas = (p.N + 15) / 16, sms = tc_num_sms();
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas < sms ? ctas : sms),
-                       static_cast<unsigned>((p.M + 8 * NT - 1) / (8 * NT)));
-    cfg.blockDim = dim3(kW4Block);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, p);
+    return launch_pdl(kern,
+                      dim3(static_cast<unsigned>(ctas < sms ? ctas : sms),
+                           static_cast<unsigned>((p.M + 8 * NT - 1) / (8 * NT))),
+                      kW4Block, smem, stream, p);
 }
-
-constexpr uint32_t kW4Room = 227 * 1024;
 
 // x goes through shared memory where it fits.
 template <int NT, int NG, int RT>
