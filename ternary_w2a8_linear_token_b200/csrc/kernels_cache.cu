@@ -80,23 +80,41 @@ __device__ __forceinline__ int block_scan(int v, int* total) {
 }
 
 // Which of 32768 pages from `base` on are in use: this thread's word covers pages
-// base + 32 * threadIdx.x + bit. Loads are coalesced (a warp reads 32 runs of 32 pages).
+// base + 32 * threadIdx.x + bit, pages behind the pool in use. Loads are coalesced (a warp reads 32
+// runs of 32 pages).
 __device__ __forceinline__ uint32_t live_word(const CacheView& c, int64_t base) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t first = base + warp * 1024;
+    const int rest = static_cast<int>(c.num_pages - first < 1024 ? c.num_pages - first : 1024);
+    uint32_t word = ~0u;
+    if (rest <= 0) return word;
+    const int32_t* refs = c.refs + first + lane;
     int32_t r[32];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        const int64_t p = first + 32 * i + lane;
-        r[i] = p < c.num_pages ? c.refs[p] : 1;
-    }
-    uint32_t word = 0;
+    for (int i = 0; i < 32; ++i) r[i] = 32 * i + lane < rest ? refs[32 * i] : 1;
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
         const uint32_t m = __ballot_sync(0xFFFFFFFFu, r[i] != 0);
         if (lane == i) word = m;
     }
     return word;
+}
+
+// Calls f(rank, page) for the pages that `word` (as live_word numbers them) names, this thread's
+// first one being `rank`, ranks below `most`: a warp takes one word at a time, a lane per page, so
+// that what f stores by rank or page lies together.
+template <typename F>
+__device__ __forceinline__ void for_pages(int64_t base, uint32_t word, int64_t rank, int64_t most,
+                                          F f) {
+    const int lane = threadIdx.x & 31;
+    const int32_t first = static_cast<int32_t>(base) + (threadIdx.x >> 5) * 1024;
+    if (!__any_sync(0xFFFFFFFFu, word != 0 && rank < most)) return;
+#pragma unroll 4
+    for (int i = 0; i < 32; ++i) {
+        const uint32_t m = __shfl_sync(0xFFFFFFFFu, word, i);
+        const int64_t r = __shfl_sync(0xFFFFFFFFu, rank, i) + __popc(m & ((1u << lane) - 1));
+        if ((m >> lane & 1) && r < most) f(r, first + 32 * i + lane);
+    }
 }
 
 // Marks every slot of a list and reports slots that are out of range or named twice: in a bitmap
@@ -306,18 +324,17 @@ __global__ void __launch_bounds__(kPlanThreads) extend_kernel(CacheView c, Ws w,
     for (int d = 16; d; d >>= 1) want += __shfl_xor_sync(0xFFFFFFFFu, want, d);
     if ((threadIdx.x & 31) == 0) wants[threadIdx.x >> 5] = want;
     __syncthreads();
-    int64_t total = 0;
+    int64_t total = wants[threadIdx.x & 31];
 #pragma unroll
-    for (int i = 0; i < kPlanThreads / 32; ++i) total += wants[i];
+    for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, d);
     // The lowest `total` free pages, ascending, into a (the marks in a and b are done with).
     int64_t found = 0;
     for (int64_t base = 0; base < c.num_pages && found < total; base += 32768) {
-        uint32_t word = ~live_word(c, base);
+        const uint32_t word = ~live_word(c, base);
         int all;
-        int64_t rank = found + block_scan(__popc(word), &all);
+        const int64_t rank = found + block_scan(__popc(word), &all);
+        for_pages(base, word, rank, total, [&](int64_t r, int32_t p) { w.a[r] = p; });
         found += all;
-        const int32_t first = static_cast<int32_t>(base) + 32 * threadIdx.x;
-        for (; word && rank < total; word &= word - 1) w.a[rank++] = first + __ffs(word) - 1;
     }
     __syncthreads();
     if (found < total) {
@@ -366,15 +383,26 @@ __global__ void __launch_bounds__(kPlanThreads) extend_kernel(CacheView c, Ws w,
     }
 }
 
-// Slot s after a compaction: a[old] = new for its pages from `live` on.
+// A table entry after a compaction. The plan leaves a[k], the k-th free page below `live`, and
+// for page p from `live` on a[p] = its rank among those in use, or -1.
 __device__ __forceinline__ void move_page(const CacheView& c, const Ws& w, int32_t live,
                                           int32_t* entry) {
     const int32_t p = *entry;
-    const int32_t to = uint32_t(p) >= uint32_t(c.num_pages) ? -1 : p < live ? p : w.a[p];
-    if (to < 0)
+    if (uint32_t(p) < uint32_t(live)) return;
+    const int32_t rank = uint32_t(p) >= uint32_t(c.num_pages) ? -1 : w.a[p];
+    if (rank < 0)
         atomicOr(c.error, BITNET_CACHE_ERR_PAGE);
-    else if (to != p)
-        *entry = to;
+    else
+        *entry = w.a[rank];
+}
+
+// The k-th move of a compaction: its pair, and the counts.
+__device__ __forceinline__ void move_count(const CacheView& c, const Ws& w, int32_t* copies,
+                                           int64_t k) {
+    const int32_t from = w.b[k], to = w.a[k];
+    *reinterpret_cast<int2*>(copies + 2 + 2 * k) = make_int2(from, to);
+    c.refs[to] = c.refs[from];
+    c.refs[from] = 0;
 }
 
 // Pages that slot s holds, 0 (and a report) for a length that does not fit.
@@ -385,10 +413,9 @@ __device__ __forceinline__ int32_t slot_pages(const CacheView& c, int64_t s, boo
     return 0;
 }
 
-// Compact, first step, in one CTA: with L pages in use, pairs the used pages from L on with the
-// free ones below L, both ascending, moves their counts and leaves a[old] = new for the tables.
-// a[k] (free pages) and a[old] do not meet: k < L <= old. `alone`: the same CTA rewrites the tables
-// too, a warp per slot.
+// Compact, first step, in one CTA: with L pages in use, lists the used pages from L on (b) and the
+// free ones below L (a), both ascending. `alone`: the same CTA does the second step too, a warp per
+// slot.
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(CacheView c, Ws w,
                                                                     int32_t* copies, int alone) {
     pdl_trigger();
@@ -407,53 +434,34 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(CacheView c,
     }
     int holes = 0, movers = 0;
     for (int64_t base = 0; base < c.num_pages; base += 32768) {
-        const int32_t first = static_cast<int32_t>(base) + 32 * threadIdx.x;
-        const int64_t low = int64_t(live) - first;
+        const int64_t low = int64_t(live) - (base + 32 * threadIdx.x);
         const uint32_t below = low >= 32 ? ~0u : low <= 0 ? 0u : (1u << low) - 1;
         const uint32_t valid = valid_of(base);
         if (c.num_pages > 32768) word = live_word(c, base) & valid;
-        uint32_t hole = ~word & valid & below, mover = word & ~below, dead = ~word & valid & ~below;
+        const uint32_t hole = ~word & valid & below, mover = word & ~below;
         int all;  // both counts in one scan: at most 32768 each
         const int ranks = block_scan(__popc(hole) | __popc(mover) << 16, &all);
-        int rank = holes + (ranks & 0xFFFF);
-        for (; hole; hole &= hole - 1) w.a[rank++] = first + __ffs(hole) - 1;
-        rank = movers + (uint32_t(ranks) >> 16);
-        for (; mover; mover &= mover - 1) w.b[rank++] = first + __ffs(mover) - 1;
-        for (; dead; dead &= dead - 1) w.a[first + __ffs(dead) - 1] = -1;  // nobody may hold it
+        for_pages(base, hole, holes + (ranks & 0xFFFF), INT32_MAX,
+                  [&](int64_t r, int32_t p) { w.a[r] = p; });
+        for_pages(base, mover, movers + (uint32_t(ranks) >> 16), INT32_MAX,
+                  [&](int64_t r, int32_t p) {
+                      w.b[r] = p;
+                      w.a[p] = static_cast<int32_t>(r);
+                  });
+        for_pages(base, ~word & valid & ~below, 0, INT32_MAX,  // nobody may hold these
+                  [&](int64_t, int32_t p) { w.a[p] = -1; });
         holes += all & 0xFFFF;
         movers += uint32_t(all) >> 16;
-    }
-    __syncthreads();
-    for (int k0 = threadIdx.x; k0 < movers; k0 += 4 * kPlanThreads) {
-        int32_t from[4], to[4], refs[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int k = k0 + u * kPlanThreads;
-            if (k < movers) {
-                from[u] = w.b[k];
-                to[u] = w.a[k];
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-            if (k0 + u * kPlanThreads < movers) refs[u] = c.refs[from[u]];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int64_t k = k0 + u * kPlanThreads;
-            if (k >= movers) continue;
-            *reinterpret_cast<int2*>(copies + 2 + 2 * k) = make_int2(from[u], to[u]);
-            c.refs[to[u]] = refs[u];
-            c.refs[from[u]] = 0;
-            w.a[from[u]] = to[u];
-        }
     }
     if (threadIdx.x == 0) {
         copies[0] = movers;
         copies[1] = 0;
         w.head[1] = live;
+        w.head[2] = movers;
     }
     if (!alone) return;
     __syncthreads();
+    for (int k = threadIdx.x; k < movers; k += kPlanThreads) move_count(c, w, copies, k);
     for (int64_t s = threadIdx.x >> 5; s < c.max_seqs; s += kPlanThreads / 32) {
         const int32_t pages = slot_pages(c, s, (threadIdx.x & 31) == 0);
         for (int32_t j = threadIdx.x & 31; j < pages; j += 32)
@@ -461,11 +469,17 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(CacheView c,
     }
 }
 
-// Compact, second step: the tables. blockIdx.x walks a row in chunks, blockIdx.y the slots.
-__global__ void __launch_bounds__(kApplyThreads) compact_apply_kernel(CacheView c, Ws w) {
+// Compact, second step: the moves over all threads of the grid, then the tables, blockIdx.x walking
+// a row in chunks and blockIdx.y the slots.
+__global__ void __launch_bounds__(kApplyThreads) compact_apply_kernel(CacheView c, Ws w,
+                                                                      int32_t* copies) {
     pdl_trigger();
     pdl_wait();
-    const int32_t live = w.head[1];
+    const int32_t live = w.head[1], movers = w.head[2];
+    const int64_t ctas = int64_t(gridDim.x) * gridDim.y;
+    for (int64_t k = (int64_t(blockIdx.y) * gridDim.x + blockIdx.x) * kApplyThreads + threadIdx.x;
+         k < movers; k += ctas * kApplyThreads)
+        move_count(c, w, copies, k);
     for (int64_t s = blockIdx.y; s < c.max_seqs; s += gridDim.y) {
         const int32_t pages = slot_pages(c, s, threadIdx.x == 0);
         int32_t* row = c.table + s * c.max_pages;
@@ -661,7 +675,7 @@ cudaError_t launch_cache_compact(const CacheView& c, int32_t* copies, void* ws,
                                      copies, int(alone));
     if (e != cudaSuccess || alone) return e;
     return launch_pdl(compact_apply_kernel, apply_grid(c, c.max_seqs), kApplyThreads, 0, stream, c,
-                      w);
+                      w, copies);
 }
 
 cudaError_t launch_cache_copy(const CacheView& c, const CacheLayers& layers, int nlayers,
@@ -680,7 +694,10 @@ cudaError_t launch_cache_append(const CacheView& c, const bitnet_cache_layer& la
                                 const uint16_t* k, const uint16_t* v, int64_t T,
                                 const int32_t* seqs, const int32_t* pos, cudaStream_t stream) {
     const int per = c.kv_heads * (c.head_dim / 4);  // pieces of a token
-    const int tokens = per >= kAppendPieces * kApplyThreads ? 1 : kAppendPieces * kApplyThreads / per;
+    // as many as four pieces per thread make, but no fewer CTAs than SMs while there are tokens
+    const int full = per >= kAppendPieces * kApplyThreads ? 1 : kAppendPieces * kApplyThreads / per;
+    const int64_t even = (T + tc_num_sms() - 1) / tc_num_sms();
+    const int tokens = even < full ? static_cast<int>(even) : full;
     const int64_t blocks = (T + tokens - 1) / tokens;
     return launch_pdl(c.head_dim == 64 ? append_kernel<64> : append_kernel<128>,
                       dim3(static_cast<unsigned>(blocks)), kApplyThreads, 0, stream, c, layer, k, v,
