@@ -112,16 +112,22 @@ __device__ __forceinline__ int32_t units_of(const Seen& s) {
     return s.slot < 0 ? 0 : s.n <= UNIT ? 1 : (s.n - 1) / UNIT + 1;
 }
 
+// a / b of non-negative numbers, in 32 bits where they fit: the divisions of 64 bits were a tenth of
+// a small call's time.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return uint32_t(a) / uint32_t(b);
+    return a / b;
+}
 __device__ __forceinline__ int64_t share_begin(int64_t units, int64_t ctas, int64_t cta) {
-    return units * cta / ctas;
+    return quotient(units * cta, ctas);
 }
 __device__ __forceinline__ int64_t share_owner(int64_t units, int64_t ctas, int64_t unit) {
-    return ((unit + 1) * ctas - 1) / units;
+    return quotient((unit + 1) * ctas - 1, units);
 }
 
 struct Shared {
     Seen seen[kThreads];  // of the sequences from `base` on
-    int64_t sums[kWarps];
+    int64_t sums[kWarps], rest[kWarps];
     int64_t before;  // units before sequence `start`
     int32_t base, start;
     float m[kWarps][kRows], l[kWarps][kRows];
@@ -265,15 +271,36 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8>::kCtas)
     pdl_wait();
     pdl_trigger();
 
-    // This CTA's share of the units: their number first, then where the share begins.
-    int64_t sum = 0;
-    for (int64_t b = threadIdx.x; b < p.B; b += kThreads)
-        sum += units_of<UNIT>(seen_by(p, b, blockIdx.x == 0));
+    // This CTA's share of the units: their number first, then where the share begins. The first
+    // sequences (all, in most batches) are looked at once for both.
+    const Seen s0 = threadIdx.x < p.B ? seen_by(p, threadIdx.x, blockIdx.x == 0) : Seen{-1, 0, 0};
+    auto scan = [&](int64_t v) {  // inclusive, within the warp
 #pragma unroll
-    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-    if (lane == 0) sh.sums[warp] = sum;
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t up = __shfl_up_sync(0xFFFFFFFFu, v, d);
+            if (lane >= d) v += up;
+        }
+        return v;
+    };
+    int64_t mine = units_of<UNIT>(s0), upto = scan(mine), rest = 0;
+    for (int64_t b = threadIdx.x + kThreads; b < p.B; b += kThreads)
+        rest += units_of<UNIT>(seen_by(p, b, blockIdx.x == 0));
+    if (p.B > kThreads) rest = __shfl_sync(0xFFFFFFFFu, scan(rest), 31);
+    if (lane == 31) {
+        sh.sums[warp] = upto;
+        sh.rest[warp] = rest;
+    }
+    sh.seen[threadIdx.x] = s0;
     __syncthreads();
-    const int64_t units = (sh.sums[0] + sh.sums[1] + sh.sums[2] + sh.sums[3]) * items;
+    int64_t all = 0;
+    rest = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) upto += sh.sums[w];
+        all += sh.sums[w];
+        rest += sh.rest[w];
+    }
+    const int64_t units = (all + rest) * items;
     const int64_t want = (units + kMinUnits - 1) / kMinUnits;
     const int64_t ctas = want < gridDim.x ? want : gridDim.x;
     const bool last_cta = blockIdx.x == (ctas ? ctas - 1 : 0);
@@ -285,36 +312,33 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8>::kCtas)
     const int64_t u0 = share_begin(units, ctas, blockIdx.x);
     const int64_t u1 = share_begin(units, ctas, int64_t(blockIdx.x) + 1);
     int64_t before = 0;
-    bool placed = false;
-    for (int64_t b0 = 0; b0 < p.B && (!placed || last_cta); b0 += kThreads) {
+    for (int64_t b0 = 0;;) {
         const int64_t b = b0 + threadIdx.x;
-        const Seen s = b < p.B ? seen_by(p, b, false) : Seen{-1, 0, 0};
-        const int64_t mine = units_of<UNIT>(s);
-        int64_t upto = mine;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int64_t up = __shfl_up_sync(0xFFFFFFFFu, upto, d);
-            if (lane >= d) upto += up;
-        }
-        __syncthreads();  // sums and the last round's values have been read
-        if (lane == 31) sh.sums[warp] = upto;
-        if (!placed) sh.seen[threadIdx.x] = s;
-        __syncthreads();
-        int64_t all = 0;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) upto += sh.sums[w];
-            all += sh.sums[w];
-        }
-        upto += before;
         if (last_cta && b < p.B) ws.first[b] = upto - mine;
-        if (!placed && (upto - mine) * items <= u0 && u0 < upto * items) {
+        const bool found = u0 < (before + all) * items, here = found && u0 >= before * items;
+        if (here && (upto - mine) * items <= u0 && u0 < upto * items) {
             sh.before = (upto - mine) * items;
             sh.base = static_cast<int32_t>(b0);
             sh.start = static_cast<int32_t>(b);
         }
         before += all;
-        placed = placed || u0 < before * items;
+        b0 += kThreads;
+        if (b0 >= p.B || (found && !last_cta)) break;
+        // The next sequences; those among which the share begins stay in sh.seen.
+        const Seen s = b0 + threadIdx.x < p.B ? seen_by(p, b0 + threadIdx.x, false) : Seen{-1, 0, 0};
+        mine = units_of<UNIT>(s);
+        upto = scan(mine);
+        __syncthreads();  // sums and seen have been read
+        if (lane == 31) sh.sums[warp] = upto;
+        if (!found) sh.seen[threadIdx.x] = s;
+        __syncthreads();
+        all = 0;
+        upto += before;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) upto += sh.sums[w];
+            all += sh.sums[w];
+        }
     }
     if (last_cta && threadIdx.x == 0) ws.first[p.B] = before;
     __syncthreads();
@@ -324,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8>::kCtas)
     walk_enter<UNIT>(p, sh, ahead);
     {
         const int64_t r = u0 - sh.before;
-        const int32_t item = static_cast<int32_t>(r / ahead.units);
+        const int32_t item = static_cast<int32_t>(quotient(r, ahead.units));
         ahead.t = static_cast<int32_t>(r - int64_t(item) * ahead.units);
         ahead.head = item / blocks;
         ahead.block = item - ahead.head * blocks;
@@ -737,16 +761,16 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8>::kCtas)
     cp_async_wait<0>();
 }
 
-// Joins the parts of the items that several CTAs worked on: one CTA per (query, head), its thread
-// groups take every n-th part, in a fixed order.
+// Joins the parts of the items that several CTAs worked on: one CTA per (query, head); groups of D / 4
+// threads take every n-th part, and the groups' states join in a fixed order.
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttnParams p) {
-    constexpr int kGroups = kJoinThreads / D;
+    constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes;
     __shared__ float acc[kGroups][D], tops[kGroups], sums[kGroups];
     pdl_wait();
     const AttnWs ws = attn_ws(p.ws, p.B);
-    const int64_t b = blockIdx.x / p.heads;
-    const int h = static_cast<int>(blockIdx.x - b * p.heads);
+    const int b = static_cast<int>(blockIdx.x / uint32_t(p.heads));
+    const int h = static_cast<int>(blockIdx.x - uint32_t(b) * uint32_t(p.heads));
     const int64_t units = ws.head[0], ctas = ws.head[1];
     if (units == 0) return;  // no query at all
     const int64_t first = ws.first[b], mine = ws.first[b + 1] - first;
@@ -757,26 +781,32 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
                        (int64_t(h / group) * blocks + h % group / kRows) * mine;
     const int64_t c0 = share_owner(units, ctas, u0), c1 = share_owner(units, ctas, u0 + mine - 1);
     if (c0 == c1) return;  // whole in one CTA, which has written it
-    const int d = threadIdx.x % D, grp = threadIdx.x / D;
-    float top = -INFINITY, sum = 0.0f, o = 0.0f;
+    const int d = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
+    float top = -INFINITY, sum = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
     for (int64_t c = c0 + grp; c <= c1; c += kGroups) {
         // the item begins in c0's share and goes on in the others'
         const float* part = ws.part + (c * 2 + (c == c0)) * (kRows * D + 2 * kRows);
-        const float m = part[kRows * D + r], l = part[kRows * D + kRows + r], v = part[r * D + d];
+        const float m = part[kRows * D + r], l = part[kRows * D + kRows + r];
+        const float4 v = *reinterpret_cast<const float4*>(part + r * D + 4 * d);
         const float next = fmaxf(top, m), base = next == -INFINITY ? 0.0f : next;
         const float a = exp2_fast(top - base), f = exp2_fast(m - base);
         sum = sum * a + l * f;
-        o = o * a + v * f;
+        o.x = o.x * a + v.x * f;
+        o.y = o.y * a + v.y * f;
+        o.z = o.z * a + v.z * f;
+        o.w = o.w * a + v.w * f;
         top = next;
     }
-    acc[grp][d] = o;
+    *reinterpret_cast<float4*>(&acc[grp][4 * d]) = o;
     if (d == 0) {
         tops[grp] = top;
         sums[grp] = sum;
     }
     __syncthreads();
-    if (grp) return;
+    if (threadIdx.x >= D) return;
+    top = tops[0];
 #pragma unroll
     for (int i = 1; i < kGroups; ++i) top = fmaxf(top, tops[i]);
     const float base = top == -INFINITY ? 0.0f : top;
@@ -785,11 +815,12 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     for (int i = 0; i < kGroups; ++i) {
         const float f = exp2_fast(tops[i] - base);
         total += sums[i] * f;
-        out += acc[i][d] * f;
+        out += acc[i][threadIdx.x] * f;
     }
-    const int64_t at = b * p.heads + h;
-    p.out[at * D + d] = __bfloat16_as_ushort(__float2bfloat16_rn(total > 0.0f ? out / total : 0.0f));
-    if (p.lse && d == 0) p.lse[at] = total > 0.0f ? (top + log2f(total)) * kLn2 : -INFINITY;
+    const int64_t at = int64_t(b) * p.heads + h;
+    p.out[at * D + threadIdx.x] =
+        __bfloat16_as_ushort(__float2bfloat16_rn(total > 0.0f ? out / total : 0.0f));
+    if (p.lse && threadIdx.x == 0) p.lse[at] = total > 0.0f ? (top + log2f(total)) * kLn2 : -INFINITY;
 }
 
 // CTAs of the split: as many as the GPU holds at once, whatever the lengths will be.
