@@ -368,9 +368,9 @@ bitnet_status bitnet_linear_b3(const uint16_t* x, int64_t M, int64_t K, const ui
  * bitnet_pack_w4 — W (N, K) fp32 -> packed (N, bitnet_w4_row_bytes(K)) uint8 and scales. Per
  *   group: s = bf16(max(max |W|, 1e-5) / 7), t = clamp(rint(W / s), -8, 7) (binary32 divides,
  *   ties to even; the clamp to -8 never acts).
- * bitnet_linear_w4 — the forward for any M >= 1 in tiles of up to 32 tokens per pass over the
- *   weights: made for decode, where the time is that of reading the weights once; a prompt of M
- *   tokens reads them ceil(M / 32) times. Codes are exact in bf16; products and sums run in
+ * bitnet_linear_w4 — the forward for any M >= 1, 16 or 32 tokens per pass over the weights: made
+ *   for decode, where the time is that of reading the weights once; a prompt of M tokens reads
+ *   them M / 32 to M / 16 times. Codes are exact in bf16; products and sums run in
  *   binary32 (sums within a group, times the scale, added over the groups in a fixed order, so
  *   results are the same on every run), and y is rounded once at the end.
  *   A row of x that holds an Inf or NaN gives unspecified values in that row of y only.

@@ -51,22 +51,22 @@ __global__ void __launch_bounds__(kW4Threads) pack_w4_kernel(const float* __rest
         scales[n * ((K + group - 1) / group) + k / group] = __bfloat16_as_ushort(sb);
 }
 
-// The forward. Bound by HBM: half a byte per weight, read once per tile of up to 32 tokens; the
+// The forward. Bound by HBM: half a byte per weight, read once per 16 or 32 tokens; the
 // arithmetic is there to keep up with it (two weights per bf16 instruction, the products on
 // mma.sync with 16 weight rows as its rows and 8 tokens as its columns, so one to eight tokens cost
 // the same; tcgen05 has no use for 16-row tiles, and its operands would have to be unpacked into
 // shared or tensor memory first).
 //
-// A CTA has two teams of eight warps. Rows are dealt out evenly, rows N t / T .. N (t + 1) / T to
-// team t of T, in tiles of 16 RT; a team's warps take every eighth block of 128 weights of a tile
+// A CTA is one or two teams of eight warps (one where two CTAs fit on an SM, so that the next call's
+// can start as this one's end; two that share x where it takes more room). Rows are dealt out evenly
+// over the teams, by 16 where each has more, and done in tiles of 16 RT; a team's warps take every eighth block of 128 weights of a tile
 // (512 bytes of a row per step of the team) and add their sums in shared memory, in order. Every
 // warp loads its blocks through a ring of its own (cp.async, no barrier between warps), across
 // tiles, and fills it before the previous kernel of the stream has ended (weights do not depend on
 // it). x and the scales come from shared memory: read by fragments from global memory, the eight
 // rows of an instruction cost the L1 a tag lookup each.
 constexpr int kW4Warps = 8;  // of a team
-constexpr int kW4Teams = 2;
-constexpr int kW4Block = 32 * kW4Warps * kW4Teams;  // threads of a CTA
+constexpr int kW4Teams = 2;  // most of a CTA, and of an SM
 constexpr int kW4Stages = 4;
 constexpr uint32_t kW4Room = 227 * 1024;  // shared memory of a CTA
 constexpr int kW4Pad = 20;  // floats per token in the reduction buffer: no bank conflicts
@@ -120,12 +120,12 @@ struct W4Layout {
     uint32_t red, scales, x, bytes;  // offsets; the rings come first
 };
 __host__ __device__ inline int w4_scale_pitch(int filled) { return ((filled + 1) / 2 | 1) * 2; }
-__host__ __device__ inline W4Layout w4_layout(int nt, int ng, int rt, int blocks, int tokens,
-                                              bool xs) {
+__host__ __device__ inline W4Layout w4_layout(int teams, int nt, int ng, int rt, int blocks,
+                                              int tokens, bool xs) {
     W4Layout l;
-    l.red = kW4Teams * kW4Warps * kW4Stages * rt * 1024;
-    l.scales = l.red + kW4Teams * kW4Warps * nt * 8 * rt * kW4Pad * 4;
-    l.x = l.scales + (kW4Teams * 2 * 16 * rt * 2 * w4_scale_pitch(blocks * ng) + 15) / 16 * 16;
+    l.red = teams * kW4Warps * kW4Stages * rt * 1024;
+    l.scales = l.red + teams * kW4Warps * nt * 8 * rt * kW4Pad * 4;
+    l.x = l.scales + (teams * 2 * 16 * rt * 2 * w4_scale_pitch(blocks * ng) + 15) / 16 * 16;
     l.bytes = l.x + (xs ? blocks * 256 * tokens : 0);
     return l;
 }
@@ -133,7 +133,7 @@ __host__ __device__ inline W4Layout w4_layout(int nt, int ng, int rt, int blocks
 // NT: tiles of 8 tokens; NG: groups per block (1, 2 or 4); RT: tiles of 16 rows that share a load
 // of x; XS: x is in shared memory (otherwise read through L1).
 template <int NT, int NG, int RT, bool XS>
-__global__ void __launch_bounds__(kW4Block, 1)
+__global__ void __launch_bounds__(32 * kW4Warps * kW4Teams, 1)
     linear_w4_kernel(const __grid_constant__ W4Params p) {
     constexpr int S = kW4Stages;
     constexpr int kRowsTile = 16 * RT;
@@ -143,9 +143,13 @@ __global__ void __launch_bounds__(kW4Block, 1)
     extern __shared__ __align__(128) uint8_t w4_dyn[];
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const int team = threadIdx.x >> 8, warp = threadIdx.x >> 5 & (kW4Warps - 1);
-    const int64_t teams = int64_t(gridDim.x) * kW4Teams;
-    const int64_t me = int64_t(blockIdx.x) * kW4Teams + team;
-    const int64_t r0 = p.N * me / teams, r1 = p.N * (me + 1) / teams;
+    const int cta_teams = blockDim.x / (32 * kW4Warps);
+    const int64_t teams = int64_t(gridDim.x) * cta_teams;
+    const int64_t me = int64_t(blockIdx.x) * cta_teams + team;
+    // Where a team has more than 16 rows, they begin at a multiple of 16 (a tile that is begun costs
+    // as much as a full one).
+    const int64_t deal = p.N > 16 * teams ? 16 : 1, deals = (p.N + deal - 1) / deal;
+    const int64_t r0 = deals * me / teams * deal, r1 = min(deals * (me + 1) / teams * deal, p.N);
     const int64_t m0 = int64_t(blockIdx.y) * (8 * NT);
     const int tokens = static_cast<int>(p.M - m0 < 8 * NT ? p.M - m0 : 8 * NT);
     const int rows = static_cast<int>(r1 - r0), tiles = (rows + kRowsTile - 1) / kRowsTile;
@@ -153,7 +157,7 @@ __global__ void __launch_bounds__(kW4Block, 1)
     const int mine = tiles ? (p.blocks - warp + kW4Warps - 1) / kW4Warps : 0;
     const int64_t row_bytes = int64_t(p.blocks) * 64;
     const int filled = p.blocks * NG, pitch = w4_scale_pitch(filled);
-    const W4Layout lay = w4_layout(NT, NG, RT, p.blocks, tokens, XS);
+    const W4Layout lay = w4_layout(cta_teams, NT, NG, RT, p.blocks, tokens, XS);
     float* const red = reinterpret_cast<float*>(w4_dyn + lay.red) +
                        team * (kW4Warps * NT * 8 * RT * kW4Pad);
     uint16_t* const scales = reinterpret_cast<uint16_t*>(w4_dyn + lay.scales) +
@@ -227,15 +231,39 @@ __global__ void __launch_bounds__(kW4Block, 1)
     }
     pdl_wait();
     if (XS) {
-        for (int i = threadIdx.x; i < p.blocks * 16 * tokens; i += kW4Block) {
-            // 16 lanes copy a block (256 bytes) of one token
-            const int part = i & 15, at = i >> 4, blk = at / tokens, m = at - blk * tokens;
-            const int k = blk * 128 + part * 8;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (k < p.K) v = __ldg(reinterpret_cast<const uint4*>(p.x + (m0 + m) * p.K + k));
-            *reinterpret_cast<uint4*>(w4_dyn + lay.x + ((blk * 4 + (part >> 2)) * tokens + m) * 64 +
-                                      (part & 3) * 16) = v;
-        }
+        // Pieces of 8 values, U places of V tokens per thread on their way at once.
+        auto bring = [&](auto u_, auto v_) {
+            constexpr int U = decltype(u_)::value, V = decltype(v_)::value;
+            const int places = p.blocks * 16, step = blockDim.x;
+            for (int m1 = 0; m1 < tokens; m1 += V)
+                for (int i0 = threadIdx.x; i0 < places; i0 += U * step) {
+                    uint4 v[U][V];
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+#pragma unroll
+                        for (int m = 0; m < V; ++m) {
+                            const int i = i0 + u * step;
+                            v[u][m] = make_uint4(0, 0, 0, 0);
+                            if (m1 + m < tokens && i < places && int64_t(i) * 8 < p.K)
+                                v[u][m] = __ldg(reinterpret_cast<const uint4*>(
+                                                    p.x + (m0 + m1 + m) * p.K) + i);
+                        }
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+#pragma unroll
+                        for (int m = 0; m < V; ++m) {
+                            const int i = i0 + u * step;
+                            if (m1 + m < tokens && i < places)
+                                *reinterpret_cast<uint4*>(w4_dyn + lay.x +
+                                                          ((i >> 2) * tokens + m1 + m) * 64 +
+                                                          (i & 3) * 16) = v[u][m];
+                        }
+                }
+        };
+        if (tokens == 1)
+            bring(std::integral_constant<int, 4>(), std::integral_constant<int, 1>());
+        else
+            bring(std::integral_constant<int, 1>(), std::integral_constant<int, 8>());
     }
     __syncthreads();
 
@@ -365,41 +393,51 @@ __global__ void __launch_bounds__(kW4Block, 1)
     cp_async_wait<0>();
 }
 
-static_assert(BITNET_W4_MAX_GROUPS == 1024, "what launch_w4_tokens finds room for");
+// Without x the longest rows fit in every tile shape, in a CTA of one team.
+static_assert(kW4Warps * kW4Stages * 2048 + kW4Warps * 8 * 2 * kW4Pad * 4 +
+                      2 * 32 * 2 * (BITNET_W4_MAX_GROUPS + 2) + 16 <= kW4Room &&
+                  kW4Warps * kW4Stages * 1024 + kW4Warps * 32 * kW4Pad * 4 +
+                          2 * 16 * 2 * (BITNET_W4_MAX_GROUPS + 2) + 16 <= kW4Room,
+              "the longest rows' scales fit beside the rings");
 
 template <int NT, int NG, int RT, bool XS>
-cudaError_t launch_w4_as(const W4Params& p, uint32_t smem, cudaStream_t stream) {
+cudaError_t launch_w4_as(const W4Params& p, int teams, uint32_t smem, cudaStream_t stream) {
     auto kern = linear_w4_kernel<NT, NG, RT, XS>;
     static std::atomic<uint64_t> allowed;
     const cudaError_t e = allow_smem(kern, kW4Room, allowed);
     if (e != cudaSuccess) return e;
-    const int64_t ctas = (p.N + 15) / 16, sms = tc_num_sms();
+    const int64_t tiles = (p.N + 15) / 16, ctas = int64_t(tc_num_sms()) * kW4Teams / teams;
     return launch_pdl(kern,
-                      dim3(static_cast<unsigned>(ctas < sms ? ctas : sms),
+                      dim3(static_cast<unsigned>(tiles < ctas ? tiles : ctas),
                            static_cast<unsigned>((p.M + 8 * NT - 1) / (8 * NT))),
-                      kW4Block, smem, stream, p);
+                      32 * kW4Warps * teams, smem, stream, p);
 }
 
-// x goes through shared memory where it fits.
+// x goes through shared memory where it fits: for one team on half an SM while a copy of x for each
+// is small (one token of 14336 values, 4096 rows: 9.4 against 10.6 µs; 8 tokens of 4096 values, 14336
+// rows: 12.3 against 11.7), for two on all of it otherwise.
 template <int NT, int NG, int RT>
 cudaError_t launch_w4(const W4Params& p, cudaStream_t stream) {
     const int tokens = static_cast<int>(p.M < 8 * NT ? p.M : 8 * NT);
-    const uint32_t with_x = w4_layout(NT, NG, RT, p.blocks, tokens, true).bytes;
-    if (with_x <= kW4Room) return launch_w4_as<NT, NG, RT, true>(p, with_x, stream);
+    constexpr uint32_t kHalf = 113 * 1024, kCopy = 32 * 1024;
+    const uint32_t one = w4_layout(1, NT, NG, RT, p.blocks, tokens, true).bytes;
+    if (one <= kHalf && uint32_t(p.blocks) * 256 * tokens <= kCopy)
+        return launch_w4_as<NT, NG, RT, true>(p, 1, one, stream);
+    const uint32_t two = w4_layout(2, NT, NG, RT, p.blocks, tokens, true).bytes;
+    if (two <= kW4Room) return launch_w4_as<NT, NG, RT, true>(p, 2, two, stream);
     return launch_w4_as<NT, NG, RT, false>(
-        p, w4_layout(NT, NG, RT, p.blocks, tokens, false).bytes, stream);
+        p, 1, w4_layout(1, NT, NG, RT, p.blocks, tokens, false).bytes, stream);
 }
 
-// The tile shape: as many tokens as there are, up to 32, and two row tiles sharing the reads of x
-// where every team has more than one; smaller ones where the scales of long rows take the room
-// (with 8 or 16 tokens and one row tile BITNET_W4_MAX_GROUPS fit).
+// The tile shape: 32 tokens a pass for up to 2^25 weights (6912 x 2560, 32 tokens: 11.4 µs against
+// 13.0 in two passes of 16), 16 for more (28672 x 4096: 47 against 58; the second pass finds the
+// weights in L2, and x takes half the reads); for up to eight tokens two row tiles share the reads of
+// x where every team has more than one.
 template <int NG>
 cudaError_t launch_w4_tokens(const W4Params& p, cudaStream_t stream) {
-    auto fits = [&](int nt, int rt) { return w4_layout(nt, NG, rt, p.blocks, 0, false).bytes <= kW4Room; };
-    if (p.M > 16 && fits(4, 1)) return launch_w4<4, NG, 1>(p, stream);
+    if (p.M > 16 && p.N * p.K <= int64_t(1) << 25) return launch_w4<4, NG, 1>(p, stream);
     if (p.M > 8) return launch_w4<2, NG, 1>(p, stream);
-    if (p.N > 16 * kW4Teams * int64_t(tc_num_sms()) && fits(1, 2))
-        return launch_w4<1, NG, 2>(p, stream);
+    if (p.N > 16 * kW4Teams * int64_t(tc_num_sms())) return launch_w4<1, NG, 2>(p, stream);
     return launch_w4<1, NG, 1>(p, stream);
 }
 
@@ -419,8 +457,8 @@ cudaError_t launch_linear_w4(const uint16_t* x, int64_t M, int64_t K, const uint
                              cudaStream_t stream) {
     W4Params p = {x, packed, scales, y, K, N, M, static_cast<int32_t>((K + 127) / 128),
                   static_cast<int32_t>((K + group - 1) / group), out_f32};
-    // 65535 token tiles of 32 per launch; a launch more only past two million tokens.
-    constexpr int64_t kMost = 65535 * 32;
+    // 65535 token tiles of 16 or 32 per launch; a launch more only past a million tokens.
+    constexpr int64_t kMost = 65535 * 16;
     for (int64_t m = 0; m < M; m += kMost) {
         p.x = x + m * K;
         p.y = static_cast<char*>(y) + m * N * (out_f32 ? 4 : 2);
