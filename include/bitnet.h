@@ -407,9 +407,10 @@ bitnet_status bitnet_linear_w4(const uint16_t* x, int64_t M, int64_t K, const ui
  *
  * What the host cannot check is checked on the device and reported in the caller's word
  * cache->error, into which the calls OR BITNET_CACHE_ERR_* bits (they never clear it):
- * bitnet_cache_fork, _extend and _free then change nothing; bitnet_cache_append and
- * bitnet_paged_attention skip the tokens concerned and handle the others; bitnet_cache_copy skips
- * the pairs concerned.
+ * bitnet_cache_fork, _extend and _free then change nothing, except that a fork or free goes on
+ * past a table entry outside the pool (BITNET_CACHE_ERR_PAGE), which holds no page;
+ * bitnet_cache_append and bitnet_paged_attention skip the tokens concerned and handle the others;
+ * bitnet_cache_copy skips the pairs, and bitnet_cache_compact the table entries, concerned.
  */
 typedef enum {
     BITNET_CACHE_BF16 = 0, /* pools hold bf16 bits                                         */
@@ -428,7 +429,7 @@ typedef struct {
     int32_t* error;    /* one word of BITNET_CACHE_ERR_* bits, device       */
     int64_t num_pages; /* 1 .. 2^30                                         */
     int64_t max_seqs;  /* 1 .. 2^24                                         */
-    int64_t max_pages; /* pages a slot can hold; times page_size below 2^31 */
+    int64_t max_pages; /* pages a slot can hold; times page_size <= 2^30    */
     int32_t page_size; /* tokens per page: 8, 16, 32, 64, 128 or 256        */
     int32_t kv_heads;  /* 1 .. 1024; num_pages * kv_heads * page_size < 2^31 */
     int32_t head_dim;  /* 64 or 128                                         */
@@ -517,7 +518,8 @@ bitnet_status bitnet_cache_append(const bitnet_cache* cache, const bitnet_cache_
  * All positions are visible with window = 0; otherwise those with j < sinks or j >= n - window
  * (a sliding window, and the first tokens that stay visible). A sequence of no visible token
  * gives out = 0 and lse = -inf.
- *   q    [in]  (B, heads, head_dim) bf16 bits, 16-byte aligned; heads a multiple of kv_heads.
+ *   q    [in]  (B, heads, head_dim) bf16 bits, 16-byte aligned; B up to 2^20, heads up to 16384 and
+ *        a multiple of kv_heads, B * heads < 2^31.
  *   out  [out] (B, heads, head_dim) bf16 bits, 16-byte aligned.
  *   lse  [out] (B, heads) fp32, 4-byte aligned, or NULL.
  *   Rows of skipped queries (slot negative or out of range) are left as they were.

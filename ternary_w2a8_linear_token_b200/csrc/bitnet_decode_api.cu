@@ -17,7 +17,8 @@ bitnet_status check_cache(const bitnet_cache* c, CacheView* v) {
     int shift = 3;
     while (shift <= 8 && (1 << shift) != c->page_size) ++shift;
     if (shift > 8) return BITNET_ERR_UNSUPPORTED;
-    if (c->max_pages < 1 || c->max_pages >= (int64_t(1) << (31 - shift))) return BITNET_ERR_SHAPE;
+    // (positions, rounded up to a kernel's step, stay in 32 bits)
+    if (c->max_pages < 1 || c->max_pages > (int64_t(1) << (30 - shift))) return BITNET_ERR_SHAPE;
     // Rows of a pool are numbered in 32 bits (2^31 of the smallest would be 137 GB of K alone).
     if ((c->num_pages * c->kv_heads) << shift >= (int64_t(1) << 31)) return BITNET_ERR_UNSUPPORTED;
     if (c->head_dim != 64 && c->head_dim != 128) return BITNET_ERR_UNSUPPORTED;
@@ -61,9 +62,10 @@ size_t upkeep_ws(const CacheView& c, int64_t n) {
     return cache_ws_bytes(c.num_pages, c.max_seqs, n);
 }
 
-// Queries and heads of an attention call: B * heads indexes 32-bit rows.
+// Queries and heads of an attention call: one CTA of the joining kernel each.
 bitnet_status check_heads(int32_t kv_heads, int64_t B, int64_t heads) {
-    if (B < 1 || B > (int64_t(1) << 20) || heads < 1 || heads > 16384 || heads % kv_heads != 0)
+    if (B < 1 || B > (int64_t(1) << 20) || heads < 1 || heads > 16384 || heads % kv_heads != 0 ||
+        B * heads >= (int64_t(1) << 31))
         return BITNET_ERR_SHAPE;
     return BITNET_OK;
 }
@@ -229,8 +231,8 @@ bitnet_status bitnet_paged_attention(const bitnet_cache* cache, const bitnet_cac
     if ((st = check_ws(workspace, workspace_bytes,
                        attn_ws_bytes(p.c.kv_heads, p.c.head_dim, B, heads))) != BITNET_OK)
         return st;
-    // Lengths are below 2^31, so a window or sinks beyond that see everything they can.
-    const int64_t cap = (int64_t(1) << 30) * 2 - 1;
+    // Lengths are at most 2^30, so a window or sinks beyond that see everything they can.
+    const int64_t cap = (int64_t(1) << 31) - 1;
     p.layer = *layer;
     p.q = q;
     p.seqs = seqs;

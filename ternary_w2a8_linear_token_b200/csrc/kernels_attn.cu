@@ -52,8 +52,10 @@ struct Shape {
     static constexpr int kUnit = kTile * kWarps;
     static constexpr int kPool = kTile * kRowBytes;  // K or V of one tile
     static constexpr int kStageBytes = 2 * kPool + (I8 ? 2 * kTile * 4 : 0);
-    static constexpr int kCtas = kRowBytes == 64 ? 3 : 2;  // per SM
-    static constexpr int kStages = 3;
+    // CTAs per SM and stages of the ring. D = 64 has registers for a third CTA, in bf16 with two stages
+    // (64 sequences in a window of 4100 tokens: 96.9 against 100.5 µs with two CTAs of three).
+    static constexpr int kCtas = D == 64 ? 3 : 2;
+    static constexpr int kStages = D == 64 && !I8 ? 2 : 3;
     static constexpr int kSmem = kWarps * kStages * kStageBytes + kJoinBytes;
 };
 

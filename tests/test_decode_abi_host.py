@@ -81,11 +81,12 @@ def test_descriptor_refusals(bn, name):
     for kw in (dict(table=None), dict(lens=None), dict(refs=None), dict(error=None)):
         assert call(_cache(bn, **kw)) == bn.ERR_NULL
     for kw in (dict(num_pages=0), dict(num_pages=(1 << 30) + 1), dict(max_seqs=0),
-               dict(max_seqs=(1 << 24) + 1), dict(max_pages=0), dict(max_pages=1 << 27),
+               dict(max_seqs=(1 << 24) + 1), dict(max_pages=0), dict(max_pages=(1 << 26) + 1),
+              
                dict(kv_heads=0), dict(kv_heads=1025)):
         assert call(_cache(bn, **kw)) == bn.ERR_SHAPE, kw
     for kw in (dict(page_size=0), dict(page_size=4), dict(page_size=24), dict(page_size=512),
-               dict(head_dim=32), dict(head_dim=96), dict(head_dim=256), dict(dtype=2)):
+               dict(head_dim=32), dict(head_dim=96), dict(head_dim=256), dict(dtype=2), dict(num_pages=1 << 27)):
         assert call(_cache(bn, **kw)) == bn.ERR_UNSUPPORTED, kw
     for kw in (dict(table=FAKE + 2), dict(lens=FAKE + 1), dict(refs=FAKE + 2),
                dict(error=FAKE + 2)):
@@ -154,6 +155,7 @@ def test_attention_refusals(bn):
 
     assert call(q=None) == call(out=None) == call(layer=None) == bn.ERR_NULL
     assert call(B=0) == call(B=(1 << 20) + 1) == call(heads=7) == call(heads=0) == bn.ERR_SHAPE
+    assert call(B=1 << 20, heads=2048) == bn.ERR_SHAPE
     assert call(heads=16386) == call(window=-1) == call(sinks=-1) == bn.ERR_SHAPE
     assert call(scale=float("nan")) == call(scale=float("inf")) == bn.ERR_UNSUPPORTED
     assert call(q=FAKE + 8) == call(out=FAKE + 2) == call(lse=FAKE + 2) == bn.ERR_ALIGN

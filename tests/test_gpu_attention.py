@@ -279,3 +279,79 @@ def test_side_stream(bn):
     out, lse = bn.bitnet_paged_attention(q, cache, return_lse=True, stream=side)
     side.synchronize()
     _check(cache, q, out, lse)
+
+
+def test_workspace_contents_do_not_matter(bn):
+    """A workspace of exactly the size asked for, full of ones and of an earlier call's leavings."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    results = []
+    size = 0
+    for kind in range(3):
+        cache = _fill(bn, [700, 0, 33, 5000], 2, 128, 16, torch.bfloat16)
+        q = _q(4, 8, 128)
+        size = cache.attention_workspace_size(4, 8)
+        buf = torch.full((size + 256,), 255, dtype=torch.uint8, device="cuda")
+        ws = buf[:size]
+        if kind == 1:
+            other = _fill(bn, [9000] * 4, 2, 128, 16, torch.bfloat16, seed=4)
+            bn.bitnet_paged_attention(q, other, workspace=ws)
+        elif kind == 2:
+            ws.copy_(torch.randint(0, 256, (size,), generator=g, device="cuda").to(torch.uint8))
+        out, lse = bn.bitnet_paged_attention(q, cache, workspace=ws, return_lse=True)
+        _check(cache, q, out, lse)
+        results.append((out, lse))
+        assert torch.all(buf[size:] == 255)
+    assert all(torch.equal(a, b) for r in results[1:] for a, b in zip(r, results[0]))
+    with pytest.raises(bn.BitnetError) as e:
+        bn.bitnet_paged_attention(q, cache, workspace=ws[:-1].clone())
+    assert e.value.status == bn.ERR_WORKSPACE
+
+
+def test_calls_at_once_on_two_streams(bn):
+    caches = [_fill(bn, [3000, 17, 800], 2, 128, 16, torch.bfloat16, seed=s) for s in (1, 2)]
+    qs = [_q(3, 8, 128, s) for s in (3, 4)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i in range(2):
+            got[i].append(bn.bitnet_paged_attention(qs[i], caches[i], return_lse=True,
+                                                    stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        _check(caches[i], qs[i], *got[i][0])
+        assert all(torch.equal(a, b) for r in got[i] for a, b in zip(r, got[i][0]))
+
+
+def test_more_queries_than_one_look_with_gaps(bn):
+    """Padded entries between and behind the queries of a batch of several hundred."""
+    lens = [(i * 53) % 300 for i in range(90)]
+    cache = _fill(bn, lens, 2, 64, 32, torch.int8)
+    slots = [(i * 7) % 90 if i % 5 else -1 for i in range(400)] + [-1] * 150
+    q = _q(len(slots), 4, 64)
+    out = torch.full_like(q, 3.0)
+    lse = torch.full((len(slots), 4), 3.0, device="cuda")
+    bn.bitnet_paged_attention(q, cache, seqs=_dev(slots), out=out, lse=lse)
+    rows = [b for b, s in enumerate(slots) if s >= 0]
+    _check(cache, q, out, lse, slots, rows=rows)
+    rest = [b for b, s in enumerate(slots) if s < 0]
+    assert torch.all(out[rest] == 3.0) and torch.all(lse[rest] == 3.0)
+    out.fill_(3.0)
+    bn.bitnet_paged_attention(q, cache, seqs=_dev([-1] * len(slots)), out=out)
+    assert torch.all(out == 3.0) and cache.errors() == 0
+
+
+def test_misaligned_and_foreign_tensors_are_refused(bn):
+    cache = _fill(bn, [20], 2, 64, 16, torch.bfloat16)
+    q = _q(1, 4, 64)
+    with pytest.raises(bn.BitnetError) as e:
+        buf = torch.zeros(257, dtype=torch.bfloat16, device="cuda")
+        bn.bitnet_paged_attention(buf[1:].view(1, 4, 64), cache)
+    assert e.value.status == bn.ERR_ALIGN
+    for bad in (q.float(), q.cpu(), q[:, :, :32], q.transpose(1, 2), _q(2, 4, 64)):
+        with pytest.raises((ValueError, bn.BitnetError)):
+            bn.bitnet_paged_attention(bad, cache)
+    with pytest.raises(bn.BitnetError):
+        bn.bitnet_paged_attention(_q(1, 3, 64), cache)  # 3 heads over 2
+    with pytest.raises(IndexError):
+        bn.bitnet_paged_attention(q, cache, 1)

@@ -262,3 +262,69 @@ def test_quantised_ties(bn):
         q, sc = ref.quantise((x * (w + 1))[0])
         assert np.array_equal(cache.layers[0][w][0, :, 0].cpu().numpy(), q)
         assert cache.layers[0][2 + w][0, 0, 0].item() == s == sc[0]
+
+
+def test_more_slots_than_the_bitmap(bn):
+    """Duplicates are found in caches of more slots than one CTA keeps marks for."""
+    cache, m = _make(bn, 50, 200000, 2, 16, kv=1)
+    seqs, add = [199999, 5, 131072, 131071], [3, 20, 1, 32]
+    assert ref.pairs(bn.bitnet_cache_extend(cache, _dev(seqs), _dev(add))) == m.extend(seqs, add)
+    assert cache.lens[torch.tensor(seqs, device="cuda")].tolist() == add
+    for bad in ([5, 199999, 5], [7, 200000]):
+        bn.bitnet_cache_free(cache, _dev(bad))
+        assert cache.errors() == bn.CACHE_ERR_SEQ
+    bn.bitnet_cache_fork(cache, _dev([5, 5]), _dev([6, 199998]))
+    m.fork([5, 5], [6, 199998])
+    bn.bitnet_cache_free(cache, _dev([199999, 5]))
+    m.free([199999, 5])
+    assert ref.pairs(bn.bitnet_cache_compact(cache)) == m.compact()
+    assert cache.refs.tolist() == m.refs and cache.lens.tolist() == m.lens
+    for s in (6, 199998, 131071):
+        assert cache.table[s].tolist()[:m.pages(m.lens[s])] == m.table[s][:m.pages(m.lens[s])]
+    assert cache.errors() == 0
+
+
+def test_upkeep_workspace_contents_do_not_matter(bn):
+    """The same life with scratch of exactly the size asked for, full of ones."""
+    for fill in (0, 255):
+        cache, m = _make(bn, 70, 9, 40, 8, kv=1)
+        n = 6
+        size = cache.workspace_size(n)
+        buf = torch.full((size + 64,), fill, dtype=torch.uint8, device="cuda")
+        ws = buf[:size]
+
+        def again():
+            buf.fill_(fill)
+            return ws
+
+        bn.bitnet_cache_extend(cache, _dev([0, 1]), _dev([100, 61]), workspace=again())
+        m.extend([0, 1], [100, 61])
+        bn.bitnet_cache_fork(cache, _dev([0, 1, 1, 0]), _dev([2, 3, 4, 5]), workspace=again())
+        m.fork([0, 1, 1, 0], [2, 3, 4, 5])
+        seqs, add = [5, 4, 3, 2, 1, 0], [1, 1, 2, 3, 1, 9]
+        got = bn.bitnet_cache_extend(cache, _dev(seqs), _dev(add), workspace=again())
+        assert ref.pairs(got) == m.extend(seqs, add)
+        bn.bitnet_cache_free(cache, _dev([0, 3]), workspace=again())
+        m.free([0, 3])
+        assert ref.pairs(bn.bitnet_cache_compact(cache, workspace=again())) == m.compact()
+        m.check(cache)
+        assert torch.all(buf[size:] == fill) and cache.errors() == 0
+
+
+def test_long_rows(bn):
+    """Slots of many pages: forks, frees and compactions over several chunks of a row."""
+    cache, m = _make(bn, 9000, 6, 3000, 8, kv=1)
+    bn.bitnet_cache_extend(cache, _dev([1, 4]), _dev([20000, 7]))
+    m.extend([1, 4], [20000, 7])
+    bn.bitnet_cache_fork(cache, _dev([1, 1]), _dev([0, 5]))
+    m.fork([1, 1], [0, 5])
+    got = bn.bitnet_cache_extend(cache, _dev([0, 4, 5]), _dev([4000, 20000, 1]))
+    assert ref.pairs(got) == m.extend([0, 4, 5], [4000, 20000, 1])
+    bn.bitnet_cache_free(cache, _dev([1, 5]))
+    m.free([1, 5])
+    bn.bitnet_cache_free(cache, _dev([0]))
+    m.free([0])
+    m.check(cache)
+    assert ref.pairs(bn.bitnet_cache_compact(cache)) == m.compact()
+    m.check(cache)
+    assert cache.errors() == 0
