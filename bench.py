@@ -324,6 +324,72 @@ def run_mlp(bn, torch, dev, name, layers_w, M, steps, warmup, flush, world, peak
             else "tensor"}, launches * steps + layers * (2 if tc else 1) * steps
 
 
+# Attention heads of the stacks: query heads over key/value heads of 128 (the widths of q, k, v).
+STACK_HEADS = {"2B-4T stack": (20, 5), "8B-class stack": (32, 8)}
+DECODE_BATCHES = ((1, 4096), (16, 4096), (64, 2048))  # (sequences, tokens held by each)
+
+
+def run_decode_step(bn, torch, dev, name, stack, B, tokens, kv_dtype, steps, warmup, flush, world):
+    """One decode step of B sequences that hold `tokens` tokens each, every layer back to back with
+    its attention: the cache grown by one token (bitnet_cache_extend, _copy), then per layer q/k/v
+    (bitnet_linear_batch), bitnet_cache_append, bitnet_paged_attention, o, and the MLP's
+    bitnet_linear_swiglu and down with 4-bit weights (bitnet_linear_w4, groups of 128). Synthetic
+    inputs; q, k and v come from the projections. Timed as one CUDA graph that starts from the same
+    lengths on every replay."""
+    layers, hidden, ffn, _, per_row = STACK_SPECS[name]
+    heads, kv = STACK_HEADS[name]
+    page, D = 64, 128
+    need = -(-(tokens + 1) // page)
+    cache = bn.make_cache(B * need, B, need, kv, D, page, layers, kv_dtype, dev)
+    g = torch.Generator(device=dev).manual_seed(0)
+    for layer in cache.layers:
+        for pool in layer[:2]:
+            if kv_dtype == torch.int8:
+                pool.random_(-127, 128, generator=g)
+            else:
+                pool.normal_(generator=g)
+        for scale in layer[2:]:
+            scale.fill_(40.0)
+    seqs = torch.arange(B, dtype=torch.int32, device=dev)
+    bn.bitnet_cache_extend(cache, seqs, torch.full_like(seqs, tokens))
+    start = [t.clone() for t in (cache.table, cache.lens, cache.refs)]
+    one = torch.ones_like(seqs)
+    gen = synth.stack2b_x if name.startswith("2B") else synth.stack8b_x
+    x = torch.from_numpy(gen(B, hidden, which=0).view(np.int16).copy()).to(dev).view(torch.bfloat16)
+    W = torch.empty(hidden, ffn, device=dev).normal_(0.0, 0.02, generator=g)
+    down = bn.bitnet_pack_w4(W, 128)
+    downs = [down] + [tuple(t.clone() for t in down) for _ in range(layers - 1)]
+    mlps = [bn.bitnet_interleave_gate_up(*L["gate"][:2], *L["up"][:2], per_row) for L in stack]
+    tc = B > bn.GEMV_AUTO_M
+    ws = bn.make_workspace(B, hidden, dev) if tc else None
+
+    def step():
+        for t, s in zip((cache.table, cache.lens, cache.refs), start):
+            t.copy_(s)
+        bn.bitnet_cache_copy(cache, bn.bitnet_cache_extend(cache, seqs, one))
+        for i, L in enumerate(stack):
+            q, k, v = bn.bitnet_linear_batch(x, [L[p] for p in ("q", "k", "v")], workspace=ws)
+            bn.bitnet_cache_append(cache, i, k, v, seqs=seqs)
+            a = bn.bitnet_paged_attention(q, cache, i, seqs=seqs)
+            h = bn.bitnet_linear(a, *L["o"], workspace=ws)
+            h = bn.bitnet_linear_swiglu(h, *mlps[i], per_row, workspace=ws)
+            bn.bitnet_linear_w4(h, *downs[i], 128)
+
+    gr = capture(torch, step)
+    ms = timed_steps(torch, gr.replay, steps, warmup, flush, world)
+    assert cache.errors() == 0 and bn.bitnet_check_device_errors() == 0
+    ms_max, _ = reduce_over_ranks(ms, 0.0, world)
+    t = ms_max * 1e-3 / steps
+    kv_bytes = layers * B * tokens * 2 * kv * (D * 2 if kv_dtype == torch.bfloat16 else D + 4)
+    w_bytes = layers * ((heads + 2 * kv) * D * hidden // 4 + hidden * hidden // 4
+                        + 2 * ffn * hidden // 4 + hidden * ffn // 2 + hidden * ffn // 64)
+    del gr
+    return {"decode_step": name, "sequences": B, "tokens_held": tokens,
+            "cache": "bf16" if kv_dtype == torch.bfloat16 else "int8", "us_per_step": t * 1e6,
+            "tokens_per_s": B / t, "cache_MB": kv_bytes / 1e6, "weights_MB": w_bytes / 1e6,
+            "GB_per_s": (kv_bytes + w_bytes) / t / 1e9}
+
+
 def run_calls(bn, calls):
     for c in calls:
         bn.bitnet_linear(c["x"], c["packed"], c["s_w"], False, y=c["y"], workspace=c.get("ws"))
@@ -673,6 +739,20 @@ def run_ours(args):
             del st
             torch.cuda.empty_cache()
 
+    # ---------------- decode steps with attention over a paged cache (only when asked for)
+    decode_steps = []
+    if args.only == "layers":
+        for name in STACK_SPECS:
+            st = build_stack(bn, torch, dev, name)
+            for B, tokens in DECODE_BATCHES:
+                for kv_dtype in (torch.bfloat16, torch.int8):
+                    decode_steps.append(run_decode_step(bn, torch, dev, name, st, B, tokens,
+                                                        kv_dtype, min(args.steps, 5), args.warmup,
+                                                        flush, world))
+                    torch.cuda.empty_cache()
+            del st
+            torch.cuda.empty_cache()
+
     # ---------------- fused MLP gate/up + SwiGLU against the unfused sequence
     mlp = []
     if args.stacks == "all" and args.only in ("all", "mlp"):
@@ -739,6 +819,8 @@ def run_ours(args):
             "stacks": stacks,
             "mlp": mlp,
         }
+        if decode_steps:
+            line["decode_steps"] = decode_steps
         print(json.dumps(line), flush=True)
     del g_dec, g_e2e, g_pre
     if world > 1:
@@ -754,9 +836,10 @@ def main():
     ap.add_argument("--warmup", type=int, default=5)
     ap.add_argument("--impl", choices=["ours", "reference"], default="ours")
     ap.add_argument("--cpu-seconds", type=float, default=10.0)
-    ap.add_argument("--only", choices=["all", "decode", "mlp"], default="all",
+    ap.add_argument("--only", choices=["all", "decode", "mlp", "layers"], default="all",
                     help="decode: skip everything after the decode sweep; mlp: decode sweep "
-                         "and the MLP gate/up + SwiGLU part only (small profiling runs)")
+                         "and the MLP gate/up + SwiGLU part only (small profiling runs); layers: "
+                         "decode sweep and whole decode steps with attention over a paged cache")
     ap.add_argument("--mlp-m", default="",
                     help="comma-separated token counts of the MLP part (default: all listed)")
     ap.add_argument("--replicas", type=int, default=0,
