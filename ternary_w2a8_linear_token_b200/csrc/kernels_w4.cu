@@ -114,19 +114,19 @@ __device__ __forceinline__ void w4_mma_new(float (&d)[4], uint32_t a0, uint32_t 
 }
 
 // Shared memory of a call: the rings, the teams' reduction buffers, two tiles' scales for each team
-// (rows of an odd number of words, those of a last, half block filled up with zeros), and x as
-// (block, quarter, token, 64 bytes), zeros behind K.
+// as (group, row) with one row more, so that neither reads nor writes meet in a bank (those of a
+// last, half block filled up with zeros), and x as (block, pair of tokens, quarter, token, 64 bytes),
+// zeros behind K: what a lane reads of either lies at fixed distances.
 struct W4Layout {
     uint32_t red, scales, x, bytes;  // offsets; the rings come first
 };
-__host__ __device__ inline int w4_scale_pitch(int filled) { return ((filled + 1) / 2 | 1) * 2; }
 __host__ __device__ inline W4Layout w4_layout(int teams, int nt, int ng, int rt, int blocks,
                                               int tokens, bool xs) {
     W4Layout l;
     l.red = teams * kW4Warps * kW4Stages * rt * 1024;
     l.scales = l.red + teams * kW4Warps * nt * 8 * rt * kW4Pad * 4;
-    l.x = l.scales + (teams * 2 * 16 * rt * 2 * w4_scale_pitch(blocks * ng) + 15) / 16 * 16;
-    l.bytes = l.x + (xs ? blocks * 256 * tokens : 0);
+    l.x = l.scales + (teams * 2 * (16 * rt + 1) * 2 * blocks * ng + 15) / 16 * 16;
+    l.bytes = l.x + (xs ? blocks * 512 * ((tokens + 1) / 2) : 0);
     return l;
 }
 
@@ -156,12 +156,14 @@ __global__ void __launch_bounds__(32 * kW4Warps * kW4Teams, 1)
     // This warp's blocks of a tile (a team may be without rows).
     const int mine = tiles ? (p.blocks - warp + kW4Warps - 1) / kW4Warps : 0;
     const int64_t row_bytes = int64_t(p.blocks) * 64;
-    const int filled = p.blocks * NG, pitch = w4_scale_pitch(filled);
+    constexpr int kPitch = kRowsTile + 1;
+    const int filled = p.blocks * NG;
+    const int pair = 512 * ((tokens + 1) / 2);  // bytes of a block of x
     const W4Layout lay = w4_layout(cta_teams, NT, NG, RT, p.blocks, tokens, XS);
     float* const red = reinterpret_cast<float*>(w4_dyn + lay.red) +
                        team * (kW4Warps * NT * 8 * RT * kW4Pad);
     uint16_t* const scales = reinterpret_cast<uint16_t*>(w4_dyn + lay.scales) +
-                             team * (2 * kRowsTile * pitch);
+                             team * (2 * kPitch * filled);
     const uint8_t* const ring = w4_dyn + (team * kW4Warps + warp) * (S * kStage);
     const uint32_t ring_at = smem_addr(ring);
 
@@ -208,12 +210,12 @@ __global__ void __launch_bounds__(32 * kW4Warps * kW4Teams, 1)
     auto store_scales = [&](int tile) {
 #pragma unroll
         for (int r = 0; r < 2 * RT; ++r) {
-            uint16_t* to = scales + ((tile & 1) * kRowsTile + 8 * r + warp) * pitch;
+            uint16_t* to = scales + (tile & 1) * (kPitch * filled) + 8 * r + warp;
 #pragma unroll
             for (int i = 0; i < kHeld; ++i)
-                if (32 * i + lane < filled) to[32 * i + lane] = held[r][i];
+                if (32 * i + lane < filled) to[(32 * i + lane) * kPitch] = held[r][i];
             for (int i = 32 * kHeld + lane; i < filled; i += 32)
-                to[i] = i < p.groups ? __ldg(scale_row(tile, r) + i) : uint16_t(0);
+                to[i * kPitch] = i < p.groups ? __ldg(scale_row(tile, r) + i) : uint16_t(0);
         }
     };
     auto team_sync = [&]() {
@@ -254,9 +256,10 @@ __global__ void __launch_bounds__(32 * kW4Warps * kW4Teams, 1)
                         for (int m = 0; m < V; ++m) {
                             const int i = i0 + u * step;
                             if (m1 + m < tokens && i < places)
-                                *reinterpret_cast<uint4*>(w4_dyn + lay.x +
-                                                          ((i >> 2) * tokens + m1 + m) * 64 +
-                                                          (i & 3) * 16) = v[u][m];
+                                *reinterpret_cast<uint4*>(
+                                    w4_dyn + lay.x + (i >> 4) * pair + (m1 + m >> 1) * 512 +
+                                    (i >> 2 & 3) * 128 + (m1 + m & 1) * 64 + (i & 3) * 16) =
+                                    v[u][m];
                         }
                 }
         };
@@ -274,7 +277,7 @@ __global__ void __launch_bounds__(32 * kW4Warps * kW4Teams, 1)
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         const int m = min(8 * t + g, tokens - 1);
-        xo[t] = w4_dyn + lay.x + (warp * 4 * tokens + m) * 64 + c * 16;
+        xo[t] = w4_dyn + lay.x + warp * pair + (m >> 1) * 512 + (m & 1) * 64 + c * 16;
         xg[t] = p.x + (m0 + m) * p.K + warp * 128 + 8 * c;
     }
     // Without XS the last block's empty half is not read; it falls to one warp.
@@ -298,7 +301,7 @@ __global__ void __launch_bounds__(32 * kW4Warps * kW4Teams, 1)
             for (int t = 0; t < NT; ++t) {
                 xv[t] = make_uint4(0, 0, 0, 0);
                 if (XS)
-                    xv[t] = *reinterpret_cast<const uint4*>(xo[t] + xa + j * tokens * 64);
+                    xv[t] = *reinterpret_cast<const uint4*>(xo[t] + xa + j * 128);
                 else if (j < 2 || !half)
                     xv[t] = __ldg(reinterpret_cast<const uint4*>(xg[t] + xv0 + 32 * j));
             }
@@ -318,9 +321,9 @@ __global__ void __launch_bounds__(32 * kW4Warps * kW4Teams, 1)
                     w4_mma(part[r][t], a2, b2, a3, b3, xv[t].z, xv[t].w);
                 }
                 if (j % kWords == kWords - 1) {  // a group ends
-                    const uint16_t* q = sa + 16 * r * pitch + j / kWords;
+                    const uint16_t* q = sa + 16 * r + j / kWords * kPitch;
                     const float s0 = __uint_as_float(uint32_t(q[0]) << 16);
-                    const float s1 = __uint_as_float(uint32_t(q[8 * pitch]) << 16);
+                    const float s1 = __uint_as_float(uint32_t(q[8]) << 16);
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
                         acc[r][t][0] += s0 * part[r][t][0];
@@ -337,7 +340,7 @@ __global__ void __launch_bounds__(32 * kW4Warps * kW4Teams, 1)
         if (tile + 1 < tiles) fetch_scales(tile + 1);
         const int below = min(rows - tile * kRowsTile, kRowsTile);  // rows of this tile
         float acc[RT][NT][4] = {};
-        const uint16_t* sa = scales + ((tile & 1) * kRowsTile + g) * pitch + warp * NG;
+        const uint16_t* sa = scales + (tile & 1) * (kPitch * filled) + warp * NG * kPitch + g;
         int xa = 0;  // bytes from the warp's first block of x to this one
         int64_t xv0 = 0;
         for (int todo = mine; todo > 0; todo -= S) {
@@ -355,8 +358,8 @@ __global__ void __launch_bounds__(32 * kW4Warps * kW4Teams, 1)
                     __syncwarp();  // all lanes have read the stage
                 }
                 load(i);
-                sa += kW4Warps * NG;
-                xa += kW4Warps * 256 * tokens;
+                sa += kW4Warps * NG * kPitch;
+                xa += kW4Warps * pair;
                 xv0 += kW4Warps * 128;
             }
             advance();
@@ -395,9 +398,9 @@ __global__ void __launch_bounds__(32 * kW4Warps * kW4Teams, 1)
 
 // Without x the longest rows fit in every tile shape, in a CTA of one team.
 static_assert(kW4Warps * kW4Stages * 2048 + kW4Warps * 8 * 2 * kW4Pad * 4 +
-                      2 * 32 * 2 * (BITNET_W4_MAX_GROUPS + 2) + 16 <= kW4Room &&
+                      2 * 33 * 2 * BITNET_W4_MAX_GROUPS + 16 <= kW4Room &&
                   kW4Warps * kW4Stages * 1024 + kW4Warps * 32 * kW4Pad * 4 +
-                          2 * 16 * 2 * (BITNET_W4_MAX_GROUPS + 2) + 16 <= kW4Room,
+                          2 * 17 * 2 * BITNET_W4_MAX_GROUPS + 16 <= kW4Room,
               "the longest rows' scales fit beside the rings");
 
 template <int NT, int NG, int RT, bool XS>
