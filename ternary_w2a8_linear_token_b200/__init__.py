@@ -571,7 +571,7 @@ def _handle(stream: Optional[torch.cuda.Stream], dev: int) -> int:
 
 
 def _keep(stream: Optional[torch.cuda.Stream], *tensors):
-    """The tensors were allocated on the current stream: not to be reused before `stream` is done."""
+    """The tensors, of the current stream, are not to be reused before `stream` is done."""
     if stream is not None:
         for t in tensors:
             if t is not None:
@@ -580,8 +580,8 @@ def _keep(stream: Optional[torch.cuda.Stream], *tensors):
 
 def _on(t: torch.Tensor, dtype: torch.dtype, dev: int, name: str) -> int:
     if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor on cuda:{dev}, got {t.dtype} on "
-                         f"{t.device}" + ("" if t.is_contiguous() else ", not contiguous"))
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on cuda:{dev}, got {t.dtype} "
+                         f"on {t.device}" + ("" if t.is_contiguous() else ", not contiguous"))
     return t.data_ptr()
 
 
@@ -613,8 +613,8 @@ def bitnet_linear_w4(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor
         raise ValueError(f"group must be 32, 64 or 128, got {group}")
     N, row_bytes = packed.shape
     if row_bytes != -(-K // 128) * 64 or scales.shape != (N, -(-K // group)):
-        raise ValueError(f"packed must be (N, {-(-K // 128) * 64}) and scales (N, {-(-K // group)}), "
-                         f"got {tuple(packed.shape)} and {tuple(scales.shape)}")
+        raise ValueError(f"packed must be (N, {-(-K // 128) * 64}) and scales (N, {-(-K // group)})"
+                         f", got {tuple(packed.shape)} and {tuple(scales.shape)}")
     dev = x.get_device()
     if dev < 0 or dev != _current():
         return _elsewhere(dev, bitnet_linear_w4, x, packed, scales, group, out_dtype, y, stream)
@@ -653,7 +653,8 @@ class PagedCache:
         if dev < 0:
             raise ValueError(f"table must be a CUDA tensor, got {table.device}")
         if table.dim() != 2 or lens.shape != table.shape[:1] or refs.dim() != 1:
-            raise ValueError("table must be (max_seqs, max_pages), lens (max_seqs), refs (num_pages)")
+            raise ValueError("table must be (max_seqs, max_pages), lens (max_seqs), refs "
+                             "(num_pages)")
         if not 1 <= len(layers) <= CACHE_MAX_LAYERS:
             raise ValueError(f"1..{CACHE_MAX_LAYERS} layers")
         k0 = layers[0][0]
@@ -678,7 +679,8 @@ class PagedCache:
         for c_layer, layer in zip(self._layers, self.layers):
             pools, scales = layer[:2], [t for t in layer[2:] if t is not None]
             if len(pools) != 2 or len(scales) != (2 if i8 else 0):
-                raise ValueError("a layer is (k, v) in bfloat16, or (k, v, k_scale, v_scale) in int8")
+                raise ValueError("a layer is (k, v) in bfloat16, or (k, v, k_scale, v_scale) in "
+                                 "int8")
             if any(t.shape != k0.shape for t in pools) or \
                     any(t.shape != k0.shape[:3] for t in scales):
                 raise ValueError("all pools must have one shape, scales (num_pages, kv_heads, "
@@ -906,8 +908,8 @@ def bitnet_paged_attention(q: torch.Tensor, cache: PagedCache, layer: int = 0,
     ws, wp, wb = _scratch(cache, workspace, cache.attention_workspace_size(B, heads), stream)
     st = lib.bitnet_paged_attention(
         cache._ref, cache._layer(layer), _on(q, torch.bfloat16, dev, "q"), B, heads,
-        None if seqs is None else _slots(cache, seqs, "seqs", B), D ** -0.5 if scale is None else scale,
-        window, sinks, _on(out, torch.bfloat16, dev, "out"),
+        None if seqs is None else _slots(cache, seqs, "seqs", B),
+        D ** -0.5 if scale is None else scale, window, sinks, _on(out, torch.bfloat16, dev, "out"),
         None if lse is None else _on(lse, torch.float32, dev, "lse"), wp, wb, _handle(stream, dev))
     if st:
         _check(st, "bitnet_paged_attention")

@@ -10,8 +10,8 @@
 
 namespace bitnet {
 
-// Launches under programmatic dependent launch: the kernel starts when its predecessor in the stream
-// lets it or ends, and waits for the end (pdl_wait) before it touches what others may write.
+// Launches under programmatic dependent launch: the kernel starts when its predecessor in the
+// stream lets it or ends, and waits for the end (pdl_wait) before it touches what others may write.
 template <typename... P, typename... A>
 cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem,
                        cudaStream_t stream, const A&... args) {

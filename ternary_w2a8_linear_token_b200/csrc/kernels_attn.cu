@@ -7,15 +7,15 @@
 // and two such states join by the same formula. out = o / l, lse = (m + log2 l) ln 2.
 //
 // Bound by HBM: every K and V byte is read once, for 2 to 32 multiply-adds. The products still run
-// on the tensor cores (mma.sync m16n8k16, up to 16 heads of a group as its rows), which leaves
-// the issue slots to the loads; tcgen05 would need 64 rows and more to pay. p enters the second
+// on the tensor cores (mma.sync m16n8k16, eight heads of a group as its columns), which leaves the
+// issue slots to the loads; tcgen05 would need 64 rows and more to pay. p enters the second
 // product as two bf16 terms (value and remainder), so its error of 2^-16 vanishes beside the
 // output's rounding of 2^-8; one term would add as much again as that rounding.
 //
 // Split. The tokens of all (sequence, key/value head, block of 16 heads) items are cut into units
-// of 64 or 128, and every CTA takes an equal, contiguous share of all units, so that one long sequence
-// among short ones keeps the whole GPU busy. The lengths are on the device, so each CTA finds its
-// share there. A CTA's four warps take a quarter of each unit and load them through a ring of
+// of 64 or 128, and every CTA takes an equal, contiguous share of all units, so that one long
+// sequence among short ones keeps the whole GPU busy. The lengths are on the device, so each CTA
+// finds its share there. A CTA's four warps take a quarter of each unit and load them through a ring of
 // their own (cp.async, 16 bytes a lane, no barrier between warps); at the end of an item, or of
 // the CTA's share, the four states are joined in shared memory, and the result goes out, or into
 // the workspace if other CTAs hold parts of the item. A second kernel joins those, in order.
@@ -52,8 +52,8 @@ struct Shape {
     static constexpr int kUnit = kTile * kWarps;
     static constexpr int kPool = kTile * kRowBytes;  // K or V of one tile
     static constexpr int kStageBytes = 2 * kPool + (I8 ? 2 * kTile * 4 : 0);
-    // CTAs per SM and stages of the ring. D = 64 has registers for a third CTA, in bf16 with two stages
-    // (64 sequences in a window of 4100 tokens: 96.9 against 100.5 µs with two CTAs of three).
+    // CTAs per SM and stages of the ring. D = 64 has registers for a third CTA, in bf16 with two
+    // stages (64 sequences in a window of 4100 tokens: 96.9 against 100.5 µs with two of three).
     static constexpr int kCtas = D == 64 ? 3 : 2;
     static constexpr int kStages = D == 64 && !I8 ? 2 : 3;
     static constexpr int kSmem = kWarps * kStages * kStageBytes + kJoinBytes;
@@ -114,8 +114,8 @@ __device__ __forceinline__ int32_t units_of(const Seen& s) {
     return s.slot < 0 ? 0 : s.n <= UNIT ? 1 : (s.n - 1) / UNIT + 1;
 }
 
-// a / b of non-negative numbers, in 32 bits where they fit: the divisions of 64 bits were a tenth of
-// a small call's time.
+// a / b of non-negative numbers, in 32 bits where they fit: divisions of 64 bits were a tenth of a
+// small call's time.
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
     if (((a | b) >> 32) == 0) return uint32_t(a) / uint32_t(b);
     return a / b;
@@ -203,7 +203,8 @@ __device__ __forceinline__ uint32_t bytes_to_f16(uint32_t turned, bool odd) {
     uint32_t q;
     asm("add.rn.f16x2 %0, %1, %2;"
         : "=r"(q)
-        : "r"(__byte_perm(turned, 0x64646464u, odd ? 0x4341 : 0x4240)), "r"(0xE480E480u));  // - 1152
+        : "r"(__byte_perm(turned, 0x64646464u, odd ? 0x4341 : 0x4240)),
+          "r"(0xE480E480u));  // - 1152
     return q;
 }
 
@@ -327,7 +328,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8>::kCtas)
         b0 += kThreads;
         if (b0 >= p.B || (found && !last_cta)) break;
         // The next sequences; those among which the share begins stay in sh.seen.
-        const Seen s = b0 + threadIdx.x < p.B ? seen_by(p, b0 + threadIdx.x, false) : Seen{-1, 0, 0};
+        const int64_t next = b0 + threadIdx.x;
+        const Seen s = next < p.B ? seen_by(p, next, false) : Seen{-1, 0, 0};
         mine = units_of<UNIT>(s);
         upto = scan(mine);
         __syncthreads();  // sums and seen have been read
@@ -432,8 +434,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8>::kCtas)
     const int g = lane >> 2, cq = lane & 3;
     uint32_t q[NH][D / 16][2];
     // o[h][i][e], m[h][e & 1], l[h][e & 1]: head 8 h + 2 cq + (e & 1), dimension dim_of(i, e >> 1).
-    // m is the maximum that the sums stand on, which may lag behind by kLag (below). qx: in 8 bits the
-    // power of two that q was divided by to fit fp16.
+    // m is the maximum that the sums stand on, which may lag behind by kLag (below). qx: in 8 bits
+    // the power of two that q was divided by to fit fp16.
     float o[NH][D / 16][4], m[NH][2], l[NH][2], qx[NH][2];
     auto dim_of = [&](int i, int half) { return 16 * i + (I8 ? 2 * g + half : g + 8 * half); };
     bool fresh = true;  // an item begins
@@ -521,7 +523,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8>::kCtas)
 #pragma unroll
             for (int h = 0; h < NH; ++h)
 #pragma unroll
-                for (int t = 0; t < MT; ++t) z[h][t][0] = z[h][t][1] = z[h][t][2] = z[h][t][3] = 0.0f;
+                for (int t = 0; t < MT; ++t)
+                    z[h][t][0] = z[h][t][1] = z[h][t][2] = z[h][t][3] = 0.0f;
             const int lrow = lane & 15, lch = lane >> 4;
             if (I8) {
 #pragma unroll
@@ -532,7 +535,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8>::kCtas)
                         ldmatrix4(r, kt + tile_at<RB>(16 * t + lrow, ks + lch));
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            const uint32_t x = r[2 * k] ^ 0x80808080u, y = r[2 * k + 1] ^ 0x80808080u;
+                            const uint32_t x = r[2 * k] ^ 0x80808080u;
+                            const uint32_t y = r[2 * k + 1] ^ 0x80808080u;
                             const uint32_t a[4] = {bytes_to_f16(x, false), bytes_to_f16(y, false),
                                                    bytes_to_f16(x, true), bytes_to_f16(y, true)};
 #pragma unroll
@@ -652,7 +656,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8>::kCtas)
                         for (int k = 0; k < 2; ++k) {
                             const uint32_t a[4] = {
                                 bytes_to_bf16(r[2 * k], false), bytes_to_bf16(r[2 * k], true),
-                                bytes_to_bf16(r[2 * k + 1], false), bytes_to_bf16(r[2 * k + 1], true)};
+                                bytes_to_bf16(r[2 * k + 1], false),
+                                bytes_to_bf16(r[2 * k + 1], true)};
 #pragma unroll
                             for (int h = 0; h < NH; ++h) {
                                 mma_bf16(o[h][i + k], a, hi[h][0], hi[h][1]);
@@ -732,7 +737,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8>::kCtas)
                                                   fmaxf(sh.m[2][r], sh.m[3][r]));
                         b = b == -INFINITY ? 0.0f : b;
 #pragma unroll
-                        for (int w = 0; w < kWarps; ++w) t += sh.l[w][r] * exp2_fast(sh.m[w][r] - b);
+                        for (int w = 0; w < kWarps; ++w)
+                            t += sh.l[w][r] * exp2_fast(sh.m[w][r] - b);
                         p.out[(int64_t(cur.b) * p.heads + head0 + r) * D + d0 + d] =
                             __bfloat16_as_ushort(__float2bfloat16_rn(t > 0.0f ? v / t : 0.0f));
                     } else {
@@ -763,8 +769,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8>::kCtas)
     cp_async_wait<0>();
 }
 
-// Joins the parts of the items that several CTAs worked on: one CTA per (query, head); groups of D / 4
-// threads take every n-th part, and the groups' states join in a fixed order.
+// Joins the parts of the items that several CTAs worked on: one CTA per (query, head); groups of
+// D / 4 threads take every n-th part, and the groups' states join in a fixed order.
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttnParams p) {
     constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes;
@@ -822,7 +828,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     const int64_t at = int64_t(b) * p.heads + h;
     p.out[at * D + threadIdx.x] =
         __bfloat16_as_ushort(__float2bfloat16_rn(total > 0.0f ? out / total : 0.0f));
-    if (p.lse && threadIdx.x == 0) p.lse[at] = total > 0.0f ? (top + log2f(total)) * kLn2 : -INFINITY;
+    if (p.lse && threadIdx.x == 0)
+        p.lse[at] = total > 0.0f ? (top + log2f(total)) * kLn2 : -INFINITY;
 }
 
 // CTAs of the split: as many as the GPU holds at once, whatever the lengths will be.

@@ -166,8 +166,8 @@ __device__ __forceinline__ void free_page(const CacheView& c, const Item& it, in
 
 // Plans a fork (src given) or a free (src null): validates the list, then notes for each entry
 // the slots, pages and length, so that what follows reads no length that it also writes. What
-// follows is the apply grid, or with `alone` the same CTA, a warp per entry: for small tables that
-// saves a launch (fork of 6 slots of up to 39 pages, both in a chain of calls: ... against ... µs).
+// follows is the apply grid, or with `alone` the same CTA, a warp per entry (see
+// applies_alone).
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(CacheView c, Ws w, const int32_t* src,
                                                             const int32_t* dst, int64_t n,
                                                             int alone) {
@@ -212,7 +212,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(CacheView c, Ws w, c
     }
 }
 
-// Applies a planned fork or free: blockIdx.x walks the pages of a row in chunks, blockIdx.y the list.
+// Applies a planned fork or free: blockIdx.x walks the pages of a row in chunks, blockIdx.y the
+// list.
 template <bool FORK>
 __global__ void __launch_bounds__(kApplyThreads) apply_kernel(CacheView c, Ws w, int64_t n) {
     pdl_trigger();
@@ -495,7 +496,8 @@ __global__ void __launch_bounds__(kApplyThreads) compact_apply_kernel(CacheView 
 }
 
 // Copies pages: the work is cut into pieces of 16 KB (256 threads x 4 x 16 bytes) over all pairs,
-// layers and pools, and the grid strides over them. Bound by HBM: every byte read and written once.
+// layers and pools, and the grid strides over them. Bound by HBM: every byte read and written once
+// (about 4000 pages of 64 KB in two layers at 6.3 TB/s).
 constexpr int kCopyPieces = 4;
 constexpr int64_t kCopyUnit = int64_t(kApplyThreads) * kCopyPieces * 16;
 
@@ -548,9 +550,11 @@ __global__ void __launch_bounds__(kApplyThreads) copy_kernel(CacheView c,
 }
 
 // Writes new tokens. A CTA takes about 2048 pieces of 8 values (kv_heads * D / 4 pieces a token),
-// eight per thread on their way at once (four: 52 against 47 µs for 32768 tokens), while some of its threads look up where the tokens go;
-// D / 8 neighbouring lanes hold a row, so its absolute maximum is one warp reduction away. Bound
-// by HBM (K and V read once, pages written once), or by latency for one token per sequence.
+// eight per thread on their way at once (with four 32768 tokens took 52 µs instead of 47), while
+// some of its threads look up where the tokens go; D / 8 neighbouring lanes hold a row, so its
+// absolute maximum is one warp reduction away. Bound by HBM (K and V read once, pages written
+// once: 32768 tokens of 8 heads of 128 in bf16 at 5.7 TB/s), or by latency for one token per
+// sequence.
 constexpr int kAppendPieces = 8;
 constexpr int kAppendTokens = 128;  // tokens of a CTA: 2048 pieces of the smallest
 
@@ -621,15 +625,18 @@ __global__ void __launch_bounds__(kApplyThreads) append_kernel(CacheView c, bitn
             const uint32_t lanes = ((1u << kLanes) - 1) << (threadIdx.x & 31 & ~(kLanes - 1));
             const float amax = bf16_lo(__reduce_max_sync(lanes, absmax8_bits(x[u])));
             const float scale = __fdiv_rn(127.0f, fmaxf(amax, kActEps));
-            reinterpret_cast<uint2*>(is_v ? lay.v : lay.k)[to * kLanes + piece] = quant8(x[u], scale);
+            reinterpret_cast<uint2*>(is_v ? lay.v : lay.k)[to * kLanes + piece] =
+                quant8(x[u], scale);
             if (piece == 0) (is_v ? lay.v_scale : lay.k_scale)[to] = scale;
         }
     }
 }
 
-// Whether one CTA applies a plan itself: up to eight rounds of a warp per row and 32 entries.
+// Whether one CTA applies a plan itself, in rounds of a warp per row and 32 entries: up to three
+// rounds that takes less than a second launch (fork and free of 6 rows of 39 pages 5.5 against 7.9
+// µs, of 32 rows of 64 pages 6.1 against 7.8; eight rounds, 64 rows of 100 pages, 11.4 against 7.8).
 bool applies_alone(const CacheView& c, int64_t rows) {
-    return ((rows + 31) / 32) * ((c.max_pages + 31) / 32) <= 8;
+    return ((rows + 31) / 32) * ((c.max_pages + 31) / 32) <= 3;
 }
 
 dim3 apply_grid(const CacheView& c, int64_t rows) {

@@ -57,10 +57,10 @@ __global__ void __launch_bounds__(kW4Threads) pack_w4_kernel(const float* __rest
 // the same; tcgen05 has no use for 16-row tiles, and its operands would have to be unpacked into
 // shared or tensor memory first).
 //
-// A CTA is one or two teams of eight warps (one where two CTAs fit on an SM, so that the next call's
-// can start as this one's end; two that share x where it takes more room). Rows are dealt out evenly
-// over the teams, by 16 where each has more, and done in tiles of 16 RT; a team's warps take every eighth block of 128 weights of a tile
-// (512 bytes of a row per step of the team) and add their sums in shared memory, in order. Every
+// A CTA is one or two teams of eight warps (one where two CTAs fit on an SM, so that the next
+// call's can start as this one's end; two that share x where it takes more room). Rows are dealt
+// out evenly over the teams, by 16 where each has more, and done in tiles of 16 RT; a team's warps
+// take every eighth block of 128 weights of a tile (512 bytes of a row per step of the team) and add their sums in shared memory, in order. Every
 // warp loads its blocks through a ring of its own (cp.async, no barrier between warps), across
 // tiles, and fills it before the previous kernel of the stream has ended (weights do not depend on
 // it). x and the scales come from shared memory: read by fragments from global memory, the eight
@@ -115,8 +115,8 @@ __device__ __forceinline__ void w4_mma_new(float (&d)[4], uint32_t a0, uint32_t 
 
 // Shared memory of a call: the rings, the teams' reduction buffers, two tiles' scales for each team
 // as (group, row) with one row more, so that neither reads nor writes meet in a bank (those of a
-// last, half block filled up with zeros), and x as (block, pair of tokens, quarter, token, 64 bytes),
-// zeros behind K: what a lane reads of either lies at fixed distances.
+// last, half block filled up with zeros), and x as (block, pair of tokens, quarter, token, 64
+// bytes), zeros behind K: what a lane reads of either lies at fixed distances.
 struct W4Layout {
     uint32_t red, scales, x, bytes;  // offsets; the rings come first
 };
@@ -146,8 +146,8 @@ __global__ void __launch_bounds__(32 * kW4Warps * kW4Teams, 1)
     const int cta_teams = blockDim.x / (32 * kW4Warps);
     const int64_t teams = int64_t(gridDim.x) * cta_teams;
     const int64_t me = int64_t(blockIdx.x) * cta_teams + team;
-    // Where a team has more than 16 rows, they begin at a multiple of 16 (a tile that is begun costs
-    // as much as a full one).
+    // Where a team has more than 16 rows, they begin at a multiple of 16 (a tile that is begun
+    // costs as much as a full one: 14336 x 4096 at one token 10.7 against 11.0 µs).
     const int64_t deal = p.N > 16 * teams ? 16 : 1, deals = (p.N + deal - 1) / deal;
     const int64_t r0 = deals * me / teams * deal, r1 = min(deals * (me + 1) / teams * deal, p.N);
     const int64_t m0 = int64_t(blockIdx.y) * (8 * NT);
@@ -181,7 +181,8 @@ __global__ void __launch_bounds__(32 * kW4Warps * kW4Teams, 1)
         if (i < left) {
 #pragma unroll
             for (int r = 0; r < 2 * RT; ++r)
-                cp_async16(ring_at + i * kStage + (8 * r + g) * 64 + c * 16, from[r] + i * kStep, true);
+                cp_async16(ring_at + i * kStage + (8 * r + g) * 64 + c * 16, from[r] + i * kStep,
+                           true);
         }
         cp_async_commit();
     };
@@ -194,8 +195,8 @@ __global__ void __launch_bounds__(32 * kW4Warps * kW4Teams, 1)
             if (left > 0) aim();
         }
     };
-    // Scales of a tile: a warp brings rows warp, warp + 8, ..., in registers until the tile before it
-    // is done.
+    // Scales of a tile: a warp brings rows warp, warp + 8, ..., in registers until the tile before
+    // it is done.
     uint16_t held[2 * RT][kHeld];
     auto scale_row = [&](int tile, int r) {
         return p.scales + (r0 + min(tile * kRowsTile + 8 * r + warp, rows - 1)) * p.groups;
@@ -205,7 +206,8 @@ __global__ void __launch_bounds__(32 * kW4Warps * kW4Teams, 1)
         for (int r = 0; r < 2 * RT; ++r)
 #pragma unroll
             for (int i = 0; i < kHeld; ++i)
-                held[r][i] = 32 * i + lane < p.groups ? __ldg(scale_row(tile, r) + 32 * i + lane) : 0;
+                held[r][i] =
+                    32 * i + lane < p.groups ? __ldg(scale_row(tile, r) + 32 * i + lane) : 0;
     };
     auto store_scales = [&](int tile) {
 #pragma unroll
@@ -270,8 +272,8 @@ __global__ void __launch_bounds__(32 * kW4Warps * kW4Teams, 1)
     }
     __syncthreads();
 
-    // This lane's x: token 8 t + g of the tile, 8 values of a quarter block. Columns behind the last
-    // token repeat it and are not written.
+    // This lane's x: token 8 t + g of the tile, 8 values of a quarter block. Columns behind the
+    // last token repeat it and are not written.
     const uint8_t* xo[NT];
     const uint16_t* xg[NT];
 #pragma unroll
@@ -376,7 +378,8 @@ __global__ void __launch_bounds__(32 * kW4Warps * kW4Teams, 1)
                         acc[r][t][e];
         if (tile + 1 < tiles) store_scales(tile + 1);
         team_sync();
-        for (int i = threadIdx.x & (32 * kW4Warps - 1); i < NT * 8 * kRowsTile; i += 32 * kW4Warps) {
+        for (int i = threadIdx.x & (32 * kW4Warps - 1); i < NT * 8 * kRowsTile;
+             i += 32 * kW4Warps) {
             const int m = i / kRowsTile, row = i % kRowsTile;
             const int64_t n = r0 + tile * kRowsTile + row;
             float v = 0.0f;
@@ -416,9 +419,9 @@ cudaError_t launch_w4_as(const W4Params& p, int teams, uint32_t smem, cudaStream
                       32 * kW4Warps * teams, smem, stream, p);
 }
 
-// x goes through shared memory where it fits: for one team on half an SM while a copy of x for each
-// is small (one token of 14336 values, 4096 rows: 9.4 against 10.6 µs; 8 tokens of 4096 values, 14336
-// rows: 12.3 against 11.7), for two on all of it otherwise.
+// x goes through shared memory where it fits: for one team on half an SM while a copy of x for
+// each is small (one token of 14336 values, 4096 rows: 9.4 against 10.6 µs; 8 tokens of 4096
+// values, 14336 rows: 12.3 against 11.7), for two on all of it otherwise.
 template <int NT, int NG, int RT>
 cudaError_t launch_w4(const W4Params& p, cudaStream_t stream) {
     const int tokens = static_cast<int>(p.M < 8 * NT ? p.M : 8 * NT);
@@ -434,8 +437,8 @@ cudaError_t launch_w4(const W4Params& p, cudaStream_t stream) {
 
 // The tile shape: 32 tokens a pass for up to 2^25 weights (6912 x 2560, 32 tokens: 11.4 µs against
 // 13.0 in two passes of 16), 16 for more (28672 x 4096: 47 against 58; the second pass finds the
-// weights in L2, and x takes half the reads); for up to eight tokens two row tiles share the reads of
-// x where every team has more than one.
+// weights in L2, and x takes half the reads); for up to eight tokens two row tiles share the reads
+// of x where every team has more than one.
 template <int NG>
 cudaError_t launch_w4_tokens(const W4Params& p, cudaStream_t stream) {
     if (p.M > 16 && p.N * p.K <= int64_t(1) << 25) return launch_w4<4, NG, 1>(p, stream);

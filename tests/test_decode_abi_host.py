@@ -86,7 +86,8 @@ def test_descriptor_refusals(bn, name):
                dict(kv_heads=0), dict(kv_heads=1025)):
         assert call(_cache(bn, **kw)) == bn.ERR_SHAPE, kw
     for kw in (dict(page_size=0), dict(page_size=4), dict(page_size=24), dict(page_size=512),
-               dict(head_dim=32), dict(head_dim=96), dict(head_dim=256), dict(dtype=2), dict(num_pages=1 << 27)):
+               dict(head_dim=32), dict(head_dim=96), dict(head_dim=256), dict(dtype=2),
+               dict(num_pages=1 << 27)):
         assert call(_cache(bn, **kw)) == bn.ERR_UNSUPPORTED, kw
     for kw in (dict(table=FAKE + 2), dict(lens=FAKE + 1), dict(refs=FAKE + 2),
                dict(error=FAKE + 2)):

@@ -71,12 +71,14 @@ def _check(cache, q, out, lse, slots=None, scale=None, window=0, sinks=0, layer=
             j = np.arange(lens[s])
             seen = (j < sinks) | (j >= lens[s] - window)
             k, v = k[seen], v[seen]
-        o, l, to, tl = ref.attention(qd[b], k, v, cache.head_dim ** -0.5 if scale is None else scale)
+        o, l, to, tl = ref.attention(qd[b], k, v,
+                                     cache.head_dim ** -0.5 if scale is None else scale)
         tol = to + ref.BF16_HALF * (np.abs(o) + to)
         err = np.abs(got[b] - o)
         assert np.all(err <= tol), f"query {b} of {lens[s]}: {np.nanmax(err / tol):.2f}"
         if len(k):
-            assert np.all(np.abs(got_lse[b] - l) <= tl), f"lse {b}: {np.max(np.abs(got_lse[b] - l) / tl)}"
+            off = np.abs(got_lse[b] - l)
+            assert np.all(off <= tl), f"lse {b}: {np.max(off / tl)}"
         else:
             assert np.all(got_lse[b] == -np.inf) and not got[b].any()
 
@@ -254,7 +256,8 @@ def test_two_captured_graphs_with_their_own_workspaces(bn):
     """Captured once, replayed after the sequences have grown, two graphs in turn."""
     lens = [60, 1, 200]
     cache = _fill(bn, lens, 2, 128, 16, torch.bfloat16, spare=40)
-    cache.table.copy_(torch.arange(cache.table.numel(), device="cuda").view_as(cache.table) % cache.num_pages)
+    cache.table.copy_(torch.arange(cache.table.numel(), device="cuda").view_as(cache.table)
+                      % cache.num_pages)
     qs = [_q(3, 8, 128, s) for s in (1, 2)]
     graphs = []
     for q in qs:
