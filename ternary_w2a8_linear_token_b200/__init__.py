@@ -623,12 +623,13 @@ def bitnet_linear_w4(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor
             raise ValueError(f"out_dtype must be bfloat16 or float32, got {out_dtype}")
         y = torch.empty((M, N), dtype=out_dtype, device=x.device)
         _keep(stream, y)
+        yp = y.data_ptr()
     else:
         _check_out(y, M, N)
+        yp = _on(y, y.dtype, dev, "y")
     st = lib.bitnet_linear_w4(_on(x, torch.bfloat16, dev, "x"), M, K,
                               _on(packed, torch.uint8, dev, "packed"),
-                              _on(scales, torch.bfloat16, dev, "scales"), group, N,
-                              _on(y, y.dtype, dev, "y"),
+                              _on(scales, torch.bfloat16, dev, "scales"), group, N, yp,
                               OUT_BF16 if y.dtype is torch.bfloat16 else OUT_F32,
                               _handle(stream, dev))
     if st:
@@ -698,6 +699,7 @@ class PagedCache:
                                self.head_dim, CACHE_I8 if i8 else CACHE_BF16)
         self._ref = ctypes.byref(self._c)
         self._sizes = {}  # workspace bytes by call
+        self._scratch = None  # the default stream's workspace (see _scratch)
 
     def _layer(self, i: int):
         if not 0 <= i < len(self.layers):
@@ -752,9 +754,17 @@ def _slots(cache: PagedCache, t: torch.Tensor, name: str, n: int) -> int:
     return _on(t, torch.int32, cache._dev, name)
 
 
-def _scratch(cache: PagedCache, workspace: Optional[torch.Tensor], size: int, stream):
-    """The workspace of a call, its address and its bytes."""
+def _scratch(cache: PagedCache, workspace: Optional[torch.Tensor], size: int, stream, handle: int):
+    """The workspace of a call, its address and its bytes. Calls on the legacy default stream share
+    one that the cache keeps: they run one after the other, and that stream cannot be captured, so
+    no graph holds it. Other streams get a new one each time."""
     if workspace is None:
+        if handle == 0 and stream is None:
+            workspace = cache._scratch
+            if workspace is None or workspace.shape[0] < size:
+                workspace = cache._scratch = torch.empty(size, dtype=torch.uint8,
+                                                         device=cache.device)
+            return workspace, workspace.data_ptr(), size
         workspace = torch.empty(size, dtype=torch.uint8, device=cache.device)
         _keep(stream, workspace)
         return workspace, workspace.data_ptr(), size
@@ -780,9 +790,10 @@ def bitnet_cache_fork(cache: PagedCache, src: torch.Tensor, dst: torch.Tensor,
     dev, n = cache._dev, src.shape[0]
     if dev != _current():
         return _elsewhere(dev, bitnet_cache_fork, cache, src, dst, workspace, stream)
-    ws, wp, wb = _scratch(cache, workspace, cache.workspace_size(n), stream)
+    handle = _handle(stream, dev)
+    ws, wp, wb = _scratch(cache, workspace, cache.workspace_size(n), stream, handle)
     st = lib.bitnet_cache_fork(cache._ref, _slots(cache, src, "src", n),
-                               _slots(cache, dst, "dst", n), n, wp, wb, _handle(stream, dev))
+                               _slots(cache, dst, "dst", n), n, wp, wb, handle)
     if st:
         _check(st, "bitnet_cache_fork")
 
@@ -796,10 +807,10 @@ def bitnet_cache_extend(cache: PagedCache, seqs: torch.Tensor, add: torch.Tensor
     if dev != _current():
         return _elsewhere(dev, bitnet_cache_extend, cache, seqs, add, copies, workspace, stream)
     copies, cp, room = _copies(cache, n, copies, stream)
-    ws, wp, wb = _scratch(cache, workspace, cache.workspace_size(n), stream)
+    handle = _handle(stream, dev)
+    ws, wp, wb = _scratch(cache, workspace, cache.workspace_size(n), stream, handle)
     st = lib.bitnet_cache_extend(cache._ref, _slots(cache, seqs, "seqs", n),
-                                 _slots(cache, add, "add", n), n, cp, room, wp, wb,
-                                 _handle(stream, dev))
+                                 _slots(cache, add, "add", n), n, cp, room, wp, wb, handle)
     if st:
         _check(st, "bitnet_cache_extend")
     return copies
@@ -811,9 +822,9 @@ def bitnet_cache_free(cache: PagedCache, seqs: torch.Tensor,
     dev, n = cache._dev, seqs.shape[0]
     if dev != _current():
         return _elsewhere(dev, bitnet_cache_free, cache, seqs, workspace, stream)
-    ws, wp, wb = _scratch(cache, workspace, cache.workspace_size(n), stream)
-    st = lib.bitnet_cache_free(cache._ref, _slots(cache, seqs, "seqs", n), n, wp, wb,
-                               _handle(stream, dev))
+    handle = _handle(stream, dev)
+    ws, wp, wb = _scratch(cache, workspace, cache.workspace_size(n), stream, handle)
+    st = lib.bitnet_cache_free(cache._ref, _slots(cache, seqs, "seqs", n), n, wp, wb, handle)
     if st:
         _check(st, "bitnet_cache_free")
 
@@ -826,8 +837,9 @@ def bitnet_cache_compact(cache: PagedCache, copies: Optional[torch.Tensor] = Non
     if dev != _current():
         return _elsewhere(dev, bitnet_cache_compact, cache, copies, workspace, stream)
     copies, cp, room = _copies(cache, cache.num_pages // 2, copies, stream)
-    ws, wp, wb = _scratch(cache, workspace, cache.workspace_size(0), stream)
-    st = lib.bitnet_cache_compact(cache._ref, cp, room, wp, wb, _handle(stream, dev))
+    handle = _handle(stream, dev)
+    ws, wp, wb = _scratch(cache, workspace, cache.workspace_size(0), stream, handle)
+    st = lib.bitnet_cache_compact(cache._ref, cp, room, wp, wb, handle)
     if st:
         _check(st, "bitnet_cache_compact")
     return copies
@@ -894,23 +906,30 @@ def bitnet_paged_attention(q: torch.Tensor, cache: PagedCache, layer: int = 0,
         raise ValueError(f"q must be (B, heads, {D}), got {tuple(shape)}")
     if seqs is None and B > cache.max_seqs:
         raise ValueError(f"{B} queries for {cache.max_seqs} slots: give seqs")
+    qp = _on(q, torch.bfloat16, dev, "q")
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
+        out = torch.empty_like(q)
         _keep(stream, out)
-    elif out.shape != shape:
+        op = out.data_ptr()
+    elif out.shape == shape:
+        op = _on(out, torch.bfloat16, dev, "out")
+    else:
         raise ValueError(f"out must be {tuple(shape)}, got {tuple(out.shape)}")
-    if lse is None:
-        if return_lse:
-            lse = torch.empty((B, heads), dtype=torch.float32, device=cache.device)
-            _keep(stream, lse)
-    elif lse.shape != (B, heads):
-        raise ValueError(f"lse must be ({B}, {heads}), got {tuple(lse.shape)}")
-    ws, wp, wb = _scratch(cache, workspace, cache.attention_workspace_size(B, heads), stream)
+    lp = None
+    if lse is not None:
+        if lse.shape != (B, heads):
+            raise ValueError(f"lse must be ({B}, {heads}), got {tuple(lse.shape)}")
+        lp = _on(lse, torch.float32, dev, "lse")
+    elif return_lse:
+        lse = torch.empty((B, heads), dtype=torch.float32, device=cache.device)
+        _keep(stream, lse)
+        lp = lse.data_ptr()
+    handle = _handle(stream, dev)
+    ws, wp, wb = _scratch(cache, workspace, cache.attention_workspace_size(B, heads), stream, handle)
     st = lib.bitnet_paged_attention(
-        cache._ref, cache._layer(layer), _on(q, torch.bfloat16, dev, "q"), B, heads,
+        cache._ref, cache._layer(layer), qp, B, heads,
         None if seqs is None else _slots(cache, seqs, "seqs", B),
-        D ** -0.5 if scale is None else scale, window, sinks, _on(out, torch.bfloat16, dev, "out"),
-        None if lse is None else _on(lse, torch.float32, dev, "lse"), wp, wb, _handle(stream, dev))
+        D ** -0.5 if scale is None else scale, window, sinks, op, lp, wp, wb, handle)
     if st:
         _check(st, "bitnet_paged_attention")
     return out if lse is None else (out, lse)

@@ -358,3 +358,30 @@ def test_misaligned_and_foreign_tensors_are_refused(bn):
         bn.bitnet_paged_attention(_q(1, 3, 64), cache)  # 3 heads over 2
     with pytest.raises(IndexError):
         bn.bitnet_paged_attention(q, cache, 1)
+
+
+def test_default_stream_shares_scratch_and_others_do_not(bn):
+    """Calls on the default stream, on a side stream and in a captured graph, interleaved: the
+    default stream's kept workspace is nobody else's."""
+    cache = _fill(bn, [6000, 40], 2, 128, 16, torch.bfloat16)
+    qs = [_q(2, 8, 128, s) for s in (1, 2, 3)]
+    want = [bn.bitnet_paged_attention(q, cache) for q in qs]
+    small = bn.bitnet_paged_attention(qs[0][:1], cache, seqs=_dev([1]))
+    kept = cache._scratch
+    assert kept is not None
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = bn.bitnet_paged_attention(qs[1], cache)
+    assert cache._scratch is kept
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        with torch.cuda.stream(side):
+            graph.replay()
+        a = bn.bitnet_paged_attention(qs[0], cache)
+        b = bn.bitnet_paged_attention(qs[2], cache, stream=side)
+        c = bn.bitnet_paged_attention(qs[0][:1], cache, seqs=_dev([1]))
+        torch.cuda.synchronize()
+        assert torch.equal(a, want[0]) and torch.equal(b, want[2]) and torch.equal(c, small)
+        assert torch.equal(captured, want[1])
+    assert cache._scratch is kept
