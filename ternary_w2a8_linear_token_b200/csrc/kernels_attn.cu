@@ -36,7 +36,6 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kRows = 16;         // heads per item
-constexpr int kJoinBytes = 8192;  // shared memory in which the warps' states are joined
 constexpr int kMinUnits = 2;      // fewest units that are worth a CTA of their own
 constexpr int kJoinThreads = 512;
 constexpr float kLag = 8.0f;  // powers of two that weights may exceed 1 by
@@ -44,20 +43,24 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // A unit is kTile tokens for each warp: 16 of 256 bytes (a row of K or V), 32 of 128 or 64, so
 // that a ring stage is 8 KB (4 KB for the smallest rows) and the work per tile that does not
-// depend on its bytes weighs less.
-template <int D, bool I8>
+// depend on its bytes weighs less. NH: blocks of eight heads in an item.
+template <int D, bool I8, int NH>
 struct Shape {
     static constexpr int kRowBytes = D * (I8 ? 1 : 2);
     static constexpr int kTile = kRowBytes == 256 ? 16 : 32;
     static constexpr int kUnit = kTile * kWarps;
     static constexpr int kPool = kTile * kRowBytes;  // K or V of one tile
     static constexpr int kStageBytes = 2 * kPool + (I8 ? 2 * kTile * 4 : 0);
-    // CTAs per SM and stages of the ring. D = 64 has registers for a third CTA, in bf16 with two
-    // stages (64 sequences in a window of 4100 tokens: 96.9 against 100.5 µs with two of three).
-    static constexpr int kCtas = D == 64 ? 3 : 2;
-    static constexpr int kStages = D == 64 && !I8 ? 2 : 3;
+    // CTAs per SM and stages of the ring: a third CTA where registers allow, with two stages for rows
+    // of 128 bytes (D = 64 in bf16, 64 sequences in a window of 4100 tokens: 96.9 against 100.5 µs
+    // with two CTAs of three stages; D = 128 in 8 bits, 8 sequences of up to 65536: 122 against 130).
+    static constexpr int kCtas = D == 64 || (I8 && NH == 1) ? 3 : 2;
+    static constexpr int kStages = kCtas == 3 && kRowBytes == 128 ? 2 : 3;
+    // Shared memory in which the warps' states are joined.
+    static constexpr int kJoinBytes = D == 128 && kCtas == 3 ? 4096 : 8192;
     static constexpr int kSmem = kWarps * kStages * kStageBytes + kJoinBytes;
 };
+constexpr int kMostCtas = 3;  // per SM, of any shape
 
 // The workspace: a header, the first unit of each sequence, then two partial states per CTA.
 struct AttnWs {
@@ -254,12 +257,12 @@ __device__ __forceinline__ uint32_t tile_at(int row, int chunk) {
     return uint32_t(row * RB + ((chunk ^ swz) << 4));
 }
 
-// NH: blocks of eight heads in an item. Tokens (scores) and dimensions (output) are the rows of the
+// Tokens (scores) and dimensions (output) are the rows of the
 // products and heads their columns, so that up to eight heads cost one column block.
 template <int D, bool I8, int NH>
-__global__ void __launch_bounds__(kThreads, Shape<D, I8>::kCtas)
+__global__ void __launch_bounds__(kThreads, Shape<D, I8, NH>::kCtas)
     attn_kernel(const __grid_constant__ AttnParams p) {
-    using Sh = Shape<D, I8>;
+    using Sh = Shape<D, I8, NH>;
     constexpr int RB = Sh::kRowBytes, S = Sh::kStages, T = Sh::kTile, UNIT = Sh::kUnit;
     constexpr int MT = T / 16;  // token tiles of sixteen
     constexpr uint32_t kAll = T == 32 ? ~0u : 0xFFFFu;  // mask of a full tile
@@ -713,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8>::kCtas)
             // Columns go through shared memory in pieces that hold all warps' rows.
             float* buf = reinterpret_cast<float*>(smem + kWarps * S * Sh::kStageBytes);
             int piece = D;
-            while (piece * rows * 4 * kWarps > kJoinBytes) piece >>= 1;
+            while (piece * rows * 4 * kWarps > Sh::kJoinBytes) piece >>= 1;
             for (int d0 = 0; d0 < D; d0 += piece) {
                 if (d0) __syncthreads();
 #pragma unroll
@@ -832,20 +835,14 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
         p.lse[at] = total > 0.0f ? (top + log2f(total)) * kLn2 : -INFINITY;
 }
 
-// CTAs of the split: as many as the GPU holds at once, whatever the lengths will be.
-int attn_ctas(int head_dim, bool i8) {
-    const int per = head_dim == 64 ? (i8 ? Shape<64, true>::kCtas : Shape<64, false>::kCtas)
-                                   : (i8 ? Shape<128, true>::kCtas : Shape<128, false>::kCtas);
-    return tc_num_sms() * per;
-}
-
 template <int D, bool I8, int NH>
 cudaError_t launch_one(const AttnParams& p, cudaStream_t stream) {
-    using Sh = Shape<D, I8>;
+    using Sh = Shape<D, I8, NH>;
     static std::atomic<uint64_t> allowed;
     cudaError_t e = allow_smem(attn_kernel<D, I8, NH>, Sh::kSmem, allowed);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(attn_kernel<D, I8, NH>, dim3(attn_ctas(D, I8)), kThreads, Sh::kSmem, stream, p);
+    // CTAs of the split: as many as the GPU holds at once, whatever the lengths will be
+    e = launch_pdl(attn_kernel<D, I8, NH>, dim3(tc_num_sms() * Sh::kCtas), kThreads, Sh::kSmem, stream, p);
     if (e != cudaSuccess) return e;
     return launch_pdl(join_kernel<D>, dim3(static_cast<unsigned>(int64_t(p.B) * p.heads)),
                       kJoinThreads, 0, stream, p);
@@ -862,7 +859,7 @@ cudaError_t launch_groups(const AttnParams& p, cudaStream_t stream) {
 size_t attn_ws_bytes(int32_t, int32_t head_dim, int64_t B, int64_t) {
     const AttnWs w = attn_ws(nullptr, B);
     return reinterpret_cast<size_t>(w.part) +
-           size_t(attn_ctas(head_dim, true)) * 2 * (kRows * head_dim + 2 * kRows) * 4;
+           size_t(tc_num_sms()) * kMostCtas * 2 * (kRows * head_dim + 2 * kRows) * 4;
 }
 
 cudaError_t launch_paged_attention(const AttnParams& p, cudaStream_t stream) {
