@@ -519,7 +519,7 @@ bitnet_status bitnet_cache_append(const bitnet_cache* cache, const bitnet_cache_
  * (a sliding window, and the first tokens that stay visible). A sequence of no visible token
  * gives out = 0 and lse = -inf.
  *   q    [in]  (B, heads, head_dim) bf16 bits, 16-byte aligned; B up to 2^20, heads up to 16384 and
- *        a multiple of kv_heads, B * heads < 2^31.
+ *        a multiple of kv_heads.
  *   out  [out] (B, heads, head_dim) bf16 bits, 16-byte aligned.
  *   lse  [out] (B, heads) fp32, 4-byte aligned, or NULL.
  *   Rows of skipped queries (slot negative or out of range) are left as they were.

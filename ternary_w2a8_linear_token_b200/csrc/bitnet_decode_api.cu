@@ -62,10 +62,9 @@ size_t upkeep_ws(const CacheView& c, int64_t n) {
     return cache_ws_bytes(c.num_pages, c.max_seqs, n);
 }
 
-// Queries and heads of an attention call: one CTA of the joining kernel each.
+// Queries and heads of an attention call.
 bitnet_status check_heads(int32_t kv_heads, int64_t B, int64_t heads) {
-    if (B < 1 || B > (int64_t(1) << 20) || heads < 1 || heads > 16384 || heads % kv_heads != 0 ||
-        B * heads >= (int64_t(1) << 31))
+    if (B < 1 || B > (int64_t(1) << 20) || heads < 1 || heads > 16384 || heads % kv_heads != 0)
         return BITNET_ERR_SHAPE;
     return BITNET_OK;
 }
@@ -209,7 +208,7 @@ size_t bitnet_paged_attention_workspace_size(const bitnet_cache* cache, int64_t 
     CacheView c;
     if (check_cache(cache, &c) != BITNET_OK || check_heads(c.kv_heads, B, heads) != BITNET_OK)
         return 0;
-    return attn_ws_bytes(c.kv_heads, c.head_dim, B, heads);
+    return attn_ws_bytes(c.head_dim);
 }
 
 bitnet_status bitnet_paged_attention(const bitnet_cache* cache, const bitnet_cache_layer* layer,
@@ -228,8 +227,7 @@ bitnet_status bitnet_paged_attention(const bitnet_cache* cache, const bitnet_cac
     if (!aligned(q, 16) || !aligned(out, 16) || (lse && !aligned(lse, 4)) ||
         (seqs && !aligned(seqs, 4)))
         return BITNET_ERR_ALIGN;
-    if ((st = check_ws(workspace, workspace_bytes,
-                       attn_ws_bytes(p.c.kv_heads, p.c.head_dim, B, heads))) != BITNET_OK)
+    if ((st = check_ws(workspace, workspace_bytes, attn_ws_bytes(p.c.head_dim))) != BITNET_OK)
         return st;
     // Lengths are at most 2^30, so a window or sinks beyond that see everything they can.
     const int64_t cap = (int64_t(1) << 31) - 1;

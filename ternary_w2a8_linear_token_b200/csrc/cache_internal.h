@@ -106,7 +106,7 @@ struct AttnParams {
     int32_t window;  // 0: all positions
     int32_t sinks;
 };
-size_t attn_ws_bytes(int32_t kv_heads, int32_t head_dim, int64_t B, int64_t heads);
+size_t attn_ws_bytes(int32_t head_dim);
 cudaError_t launch_paged_attention(const AttnParams& p, cudaStream_t stream);
 
 }  // namespace bitnet

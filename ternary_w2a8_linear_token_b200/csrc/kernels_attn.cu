@@ -37,7 +37,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kRows = 16;         // heads per item
 constexpr int kMinUnits = 2;      // fewest units that are worth a CTA of their own
-constexpr int kJoinThreads = 512;
+constexpr int kJoinThreads = 128;
 constexpr float kLag = 8.0f;  // powers of two that weights may exceed 1 by
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -62,18 +62,26 @@ struct Shape {
 };
 constexpr int kMostCtas = 3;  // per SM, of any shape
 
-// The workspace: a header, the first unit of each sequence, then two partial states per CTA.
+// The workspace: the units and the CTAs that share them, a note of each CTA on the item that goes on
+// behind its share, and two partial states per CTA.
+struct Note {
+    int32_t b;      // query of an item that begins in this share and ends in another, -1: none
+    int32_t head0;  // first head
+    int32_t rows;   // heads
+    int32_t pad;
+    int64_t end;    // last unit
+};
 struct AttnWs {
-    int64_t* head;   // [0] units, [1] CTAs that share them
-    int64_t* first;  // (B + 1) units before each sequence, per item of a sequence
-    float* part;     // [cta][2][kRows * D + 2 * kRows]: o, then m, then l
+    int64_t* head;  // [0] CTAs, [1] units
+    Note* note;   // [cta]
+    float* part;  // [cta][2][kRows * D + 2 * kRows]: o, then m, then l
 };
 
-__host__ __device__ inline AttnWs attn_ws(void* ws, int64_t B) {
+__host__ __device__ inline AttnWs attn_ws(void* ws, int most_ctas) {
     AttnWs w;
     w.head = static_cast<int64_t*>(ws);
-    w.first = w.head + 32;
-    w.part = reinterpret_cast<float*>(w.first + ((B + 1 + 31) & ~int64_t(31)));
+    w.note = reinterpret_cast<Note*>(w.head + 32);
+    w.part = reinterpret_cast<float*>(w.note + ((most_ctas + 15) & ~15));
     return w;
 }
 
@@ -272,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8, NH>::kCtas)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int group = p.heads / c.kv_heads, blocks = head_blocks(p.heads, c.kv_heads);
     const int items = c.kv_heads * blocks;
-    const AttnWs ws = attn_ws(p.ws, p.B);
+    const AttnWs ws = attn_ws(p.ws, gridDim.x);
 
     pdl_wait();
     pdl_trigger();
@@ -309,35 +317,33 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8, NH>::kCtas)
     const int64_t units = (all + rest) * items;
     const int64_t want = (units + kMinUnits - 1) / kMinUnits;
     const int64_t ctas = want < gridDim.x ? want : gridDim.x;
-    const bool last_cta = blockIdx.x == (ctas ? ctas - 1 : 0);
-    if (last_cta && threadIdx.x == 0) {
-        ws.head[0] = units;
-        ws.head[1] = ctas;
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        ws.head[0] = ctas;
+        ws.head[1] = units;
     }
     if (blockIdx.x >= ctas) return;
     const int64_t u0 = share_begin(units, ctas, blockIdx.x);
     const int64_t u1 = share_begin(units, ctas, int64_t(blockIdx.x) + 1);
     int64_t before = 0;
     for (int64_t b0 = 0;;) {
-        const int64_t b = b0 + threadIdx.x;
-        if (last_cta && b < p.B) ws.first[b] = upto - mine;
-        const bool found = u0 < (before + all) * items, here = found && u0 >= before * items;
-        if (here && (upto - mine) * items <= u0 && u0 < upto * items) {
-            sh.before = (upto - mine) * items;
-            sh.base = static_cast<int32_t>(b0);
-            sh.start = static_cast<int32_t>(b);
+        const bool found = u0 < (before + all) * items;
+        if (found) {
+            if ((upto - mine) * items <= u0 && u0 < upto * items) {
+                sh.before = (upto - mine) * items;
+                sh.base = static_cast<int32_t>(b0);
+                sh.start = static_cast<int32_t>(b0 + threadIdx.x);
+            }
+            break;
         }
         before += all;
-        b0 += kThreads;
-        if (b0 >= p.B || (found && !last_cta)) break;
-        // The next sequences; those among which the share begins stay in sh.seen.
+        b0 += kThreads;  // (there is a sequence that holds u0)
         const int64_t next = b0 + threadIdx.x;
         const Seen s = next < p.B ? seen_by(p, next, false) : Seen{-1, 0, 0};
         mine = units_of<UNIT>(s);
         upto = scan(mine);
         __syncthreads();  // sums and seen have been read
         if (lane == 31) sh.sums[warp] = upto;
-        if (!found) sh.seen[threadIdx.x] = s;
+        sh.seen[threadIdx.x] = s;
         __syncthreads();
         all = 0;
         upto += before;
@@ -347,7 +353,6 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8, NH>::kCtas)
             all += sh.sums[w];
         }
     }
-    if (last_cta && threadIdx.x == 0) ws.first[p.B] = before;
     __syncthreads();
 
     Walk ahead;  // the unit whose pages are looked up next
@@ -749,6 +754,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8, NH>::kCtas)
                     }
                 }
             }
+            if (u + 1 == n_units && threadIdx.x == 0)
+                ws.note[blockIdx.x] = {begun && !ended ? cur.b : -1, head0, rows, 0,
+                                       u0 + u + (cur.units - 1 - cur.t)};
             if (threadIdx.x < rows) {
                 const int r = threadIdx.x;
                 const float b = fmaxf(fmaxf(sh.m[0][r], sh.m[1][r]), fmaxf(sh.m[2][r], sh.m[3][r]));
@@ -772,67 +780,88 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8, NH>::kCtas)
     cp_async_wait<0>();
 }
 
-// Joins the parts of the items that several CTAs worked on: one CTA per (query, head); groups of
-// D / 4 threads take every n-th part, and the groups' states join in a fixed order.
+// Joins the parts of the items that several CTAs worked on: blockIdx.x stands for a CTA of the split
+// and takes head blockIdx.y of the item that goes on behind its share, if one does. A thread has four
+// dimensions; groups of D / 4 threads take every n-th part, and their states join in a fixed order.
+// Few CTAs have something to do, so they are small (64 sequences in a window of 4100 tokens: 84 µs
+// for both kernels, 87 with 256 threads, 97 with a CTA of 512 per query and head).
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttnParams p) {
-    constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes;
-    __shared__ float acc[kGroups][D], tops[kGroups], sums[kGroups];
+    constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes, kAtOnce = 4;
+    __shared__ float4 acc[kGroups][kLanes];
+    __shared__ float tops[kGroups], sums[kGroups];
     pdl_wait();
-    const AttnWs ws = attn_ws(p.ws, p.B);
-    const int b = static_cast<int>(blockIdx.x / uint32_t(p.heads));
-    const int h = static_cast<int>(blockIdx.x - uint32_t(b) * uint32_t(p.heads));
-    const int64_t units = ws.head[0], ctas = ws.head[1];
-    if (units == 0) return;  // no query at all
-    const int64_t first = ws.first[b], mine = ws.first[b + 1] - first;
-    if (mine == 0) return;
-    const int group = p.heads / p.c.kv_heads, blocks = head_blocks(p.heads, p.c.kv_heads);
-    const int r = h % group % kRows;
-    const int64_t u0 = first * (p.c.kv_heads * blocks) +
-                       (int64_t(h / group) * blocks + h % group / kRows) * mine;
-    const int64_t c0 = share_owner(units, ctas, u0), c1 = share_owner(units, ctas, u0 + mine - 1);
-    if (c0 == c1) return;  // whole in one CTA, which has written it
-    const int d = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
+    const AttnWs ws = attn_ws(p.ws, gridDim.x);
+    const int c0 = blockIdx.x, r = blockIdx.y;
+    const int64_t ctas = ws.head[0], units = ws.head[1];
+    const Note note = ws.note[c0];  // (of a CTA without a share it says nothing)
+    if (c0 >= ctas || note.b < 0 || r >= note.rows) return;
+    const int last = static_cast<int>(share_owner(units, ctas, note.end));
+    const int grp = threadIdx.x / kLanes, d = threadIdx.x % kLanes;
     float top = -INFINITY, sum = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (int64_t c = c0 + grp; c <= c1; c += kGroups) {
-        // the item begins in c0's share and goes on in the others'
-        const float* part = ws.part + (c * 2 + (c == c0)) * (kRows * D + 2 * kRows);
-        const float m = part[kRows * D + r], l = part[kRows * D + kRows + r];
-        const float4 v = *reinterpret_cast<const float4*>(part + r * D + 4 * d);
-        const float next = fmaxf(top, m), base = next == -INFINITY ? 0.0f : next;
-        const float a = exp2_fast(top - base), f = exp2_fast(m - base);
-        sum = sum * a + l * f;
-        o.x = o.x * a + v.x * f;
-        o.y = o.y * a + v.y * f;
-        o.z = o.z * a + v.z * f;
-        o.w = o.w * a + v.w * f;
+    for (int c1 = c0 + grp; c1 <= last; c1 += kAtOnce * kGroups) {
+        float m[kAtOnce], l[kAtOnce];
+        float4 v[kAtOnce];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int c = c1 + i * kGroups;
+            m[i] = -INFINITY;
+            l[i] = 0.0f;
+            v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (c > last) continue;
+            // the item begins in c0's share and goes on in the others'
+            const float* part = ws.part + (int64_t(c) * 2 + (c == c0)) * (kRows * D + 2 * kRows);
+            m[i] = part[kRows * D + r];
+            l[i] = part[kRows * D + kRows + r];
+            v[i] = *reinterpret_cast<const float4*>(part + r * D + 4 * d);
+        }
+        float next = top;
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) next = fmaxf(next, m[i]);
+        const float base = next == -INFINITY ? 0.0f : next, a = exp2_fast(top - base);
+        sum *= a;
+        o = make_float4(o.x * a, o.y * a, o.z * a, o.w * a);
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const float f = exp2_fast(m[i] - base);
+            sum += l[i] * f;
+            o.x += v[i].x * f;
+            o.y += v[i].y * f;
+            o.z += v[i].z * f;
+            o.w += v[i].w * f;
+        }
         top = next;
     }
-    *reinterpret_cast<float4*>(&acc[grp][4 * d]) = o;
+    acc[grp][d] = o;
     if (d == 0) {
         tops[grp] = top;
         sums[grp] = sum;
     }
     __syncthreads();
-    if (threadIdx.x >= D) return;
-    top = tops[0];
+    if (grp) return;
 #pragma unroll
     for (int i = 1; i < kGroups; ++i) top = fmaxf(top, tops[i]);
     const float base = top == -INFINITY ? 0.0f : top;
-    float total = 0.0f, out = 0.0f;
+    float total = 0.0f;
+    o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) {
         const float f = exp2_fast(tops[i] - base);
+        const float4 v = acc[i][d];
         total += sums[i] * f;
-        out += acc[i][threadIdx.x] * f;
+        o.x += v.x * f;
+        o.y += v.y * f;
+        o.z += v.z * f;
+        o.w += v.w * f;
     }
-    const int64_t at = int64_t(b) * p.heads + h;
-    p.out[at * D + threadIdx.x] =
-        __bfloat16_as_ushort(__float2bfloat16_rn(total > 0.0f ? out / total : 0.0f));
-    if (p.lse && threadIdx.x == 0)
-        p.lse[at] = total > 0.0f ? (top + log2f(total)) * kLn2 : -INFINITY;
+    const float scale = total > 0.0f ? 1.0f / total : 0.0f;
+    const int64_t row = int64_t(note.b) * p.heads + note.head0 + r;
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * scale, o.y * scale);
+    const __nv_bfloat162 hi = __floats2bfloat162_rn(o.z * scale, o.w * scale);
+    *reinterpret_cast<uint2*>(p.out + row * D + 4 * d) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+    if (p.lse && d == 0) p.lse[row] = total > 0.0f ? (top + log2f(total)) * kLn2 : -INFINITY;
 }
 
 template <int D, bool I8, int NH>
@@ -844,7 +873,8 @@ cudaError_t launch_one(const AttnParams& p, cudaStream_t stream) {
     // CTAs of the split: as many as the GPU holds at once, whatever the lengths will be
     e = launch_pdl(attn_kernel<D, I8, NH>, dim3(tc_num_sms() * Sh::kCtas), kThreads, Sh::kSmem, stream, p);
     if (e != cudaSuccess) return e;
-    return launch_pdl(join_kernel<D>, dim3(static_cast<unsigned>(int64_t(p.B) * p.heads)),
+    const int group = p.heads / p.c.kv_heads;
+    return launch_pdl(join_kernel<D>, dim3(tc_num_sms() * Sh::kCtas, group < kRows ? group : kRows),
                       kJoinThreads, 0, stream, p);
 }
 
@@ -856,10 +886,10 @@ cudaError_t launch_groups(const AttnParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-size_t attn_ws_bytes(int32_t, int32_t head_dim, int64_t B, int64_t) {
-    const AttnWs w = attn_ws(nullptr, B);
-    return reinterpret_cast<size_t>(w.part) +
-           size_t(tc_num_sms()) * kMostCtas * 2 * (kRows * head_dim + 2 * kRows) * 4;
+size_t attn_ws_bytes(int32_t head_dim) {
+    const int most = tc_num_sms() * kMostCtas;
+    return reinterpret_cast<size_t>(attn_ws(nullptr, most).part) +
+           size_t(most) * 2 * (kRows * head_dim + 2 * kRows) * 4;
 }
 
 cudaError_t launch_paged_attention(const AttnParams& p, cudaStream_t stream) {
