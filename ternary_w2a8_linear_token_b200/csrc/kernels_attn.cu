@@ -52,8 +52,8 @@ struct Shape {
     static constexpr int kPool = kTile * kRowBytes;  // K or V of one tile
     static constexpr int kStageBytes = 2 * kPool + (I8 ? 2 * kTile * 4 : 0);
     // CTAs per SM and stages of the ring: a third CTA where registers allow, with two stages for rows
-    // of 128 bytes (D = 64 in bf16, 64 sequences in a window of 4100 tokens: 96.9 against 100.5 µs
-    // with two CTAs of three stages; D = 128 in 8 bits, 8 sequences of up to 65536: 122 against 130).
+    // of 128 bytes (D = 64 in bf16, 64 sequences in a window of 4100 tokens: 3.5 µs less than with
+    // two CTAs of three stages; D = 128 in 8 bits, 8 sequences of up to 65536: 8 µs less).
     static constexpr int kCtas = D == 64 || (I8 && NH == 1) ? 3 : 2;
     static constexpr int kStages = kCtas == 3 && kRowBytes == 128 ? 2 : 3;
     // Shared memory in which the warps' states are joined.
@@ -219,20 +219,17 @@ __device__ __forceinline__ uint32_t bytes_to_f16(uint32_t turned, bool odd) {
     return q;
 }
 
-// Signed bytes 0 and 2 of w (odd: 1 and 3) as a bf16 pair, exactly. The byte with its sign bit
-// turned, under the exponent of 128, reads f = 256 + q for q < 0 and 256 + 2q for q >= 0 (its top
-// bit is the exponent's lowest), so q = (f - 256) - max(f / 2 - 128, 0). One logic and three
-// half-precision instructions for two values: the logic pipe is the kernel's bound in 8 bits (two
-// and one instead: 170 against ... µs).
+// Signed bytes 0 and 2 of w (odd: 1 and 3) as a bf16 pair, exactly: 128 + the low seven bits, less
+// 128, or 256 for a negative byte (its sign bit is then the exponent's lowest). Two logic and one
+// half-precision instruction for two values, the logic written out, since from C the compiler makes
+// two of each; a form with one and three took 120 µs where this takes 115 (8 sequences of up to
+// 65536 tokens, 32 heads over 8).
 __device__ __forceinline__ uint32_t bytes_to_bf16(uint32_t w, bool odd) {
     if (odd) w >>= 8;
-    uint32_t f, t, r, q;
-    asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(f) : "r"(w), "n"(0x00FF00FF), "r"(0x43804380));
-    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(t) : "r"(f), "r"(0xC380C380u));  // - 256
-    asm("fma.rn.relu.bf16x2 %0, %1, %2, %3;"
-        : "=r"(r)
-        : "r"(f), "r"(0x3F003F00u), "r"(0xC300C300u));  // f / 2 - 128
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(q) : "r"(t), "r"(r));
+    uint32_t v, o, q;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(w), "n"(0x007F007F), "r"(0x43004300));
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(o) : "r"(w), "n"(0x00800080), "r"(0x43004300));
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(q) : "r"(v), "r"(o));
     return q;
 }
 
