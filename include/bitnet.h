@@ -12,6 +12,10 @@
  * items 2 and 3; "BitNet 1-bit LLM推理优化：内存布局、量化策略与硬件加速", section 3.2
  * "激活量化策略"), and an int32 accumulator ("BitNet 深度实战" section 4.4 "查找表加速").
  *
+ * Beside it the library has what else a decode step needs: linear layers with 4-bit weights, a paged
+ * key/value cache and the attention of one new token over it (below, before the tensor-parallel
+ * steps).
+ *
  * Conventions shared by every call:
  *  - Data pointers are DEVICE pointers in the current CUDA context, owned by the
  *    caller. The library keeps no pointer after a call returns.
