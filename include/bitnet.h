@@ -535,7 +535,9 @@ bitnet_status bitnet_cache_append(const bitnet_cache* cache, const bitnet_cache_
  * cut over (sequence, key/value head, tokens) by the lengths that the kernel finds on the device,
  * and joined in a fixed order: the same inputs give the same bits on the same GPU model. Tokens
  * of a page outside the pool count as not visible (BITNET_CACHE_ERR_PAGE); a length outside the
- * table is cut at its end (BITNET_CACHE_ERR_LEN). Inf or NaN in a hidden token has no effect.
+ * table is cut at its end (BITNET_CACHE_ERR_LEN). Inf or NaN in a hidden token has no effect; in a
+ * visible one or in q it gives NaN where the formula gives Inf or NaN, and nothing elsewhere.
+ * |scale| < 2e38.
  */
 size_t bitnet_paged_attention_workspace_size(const bitnet_cache* cache, int64_t B,
                                              int64_t heads);

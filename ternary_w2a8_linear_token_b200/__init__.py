@@ -27,6 +27,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import threading
 from typing import Optional, Sequence
 
 import torch
@@ -545,8 +546,10 @@ def bitnet_linear_b3(x: torch.Tensor, packed_b3: torch.Tensor, s_w: torch.Tensor
 
 # ----------------------------------------------------------------------------- decode step
 # The operators of a decode step beside the ternary projections. They run on the device of their
-# tensors, whichever is current; what a call allocates is kept from reuse until `stream` is done
-# with it. A call's host time is that of a decode step's, so the checks are few and flat.
+# tensors, whichever is current. With `stream` given, what a call allocates belongs to that stream (no
+# pending work of the current one can still be using it), and no tensor of a call is reused before
+# both streams are done with it. A call's host time is that of a decode step's, so the checks are
+# few and flat.
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(
     torch._C, "_cuda_getCurrentRawStream") else (
     lambda i: torch.cuda.current_stream(i).cuda_stream)
@@ -570,12 +573,22 @@ def _handle(stream: Optional[torch.cuda.Stream], dev: int) -> int:
     return stream.cuda_stream
 
 
-def _keep(stream: Optional[torch.cuda.Stream], *tensors):
-    """The tensors, of the current stream, are not to be reused before `stream` is done."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+def _new(shape, dtype: torch.dtype, dev: torch.device, stream) -> torch.Tensor:
+    """A tensor for a call on `stream` (None: the current one)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    here = torch.cuda.current_stream(dev)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    t.record_stream(here)
+    return t
+
+
+def _keep(stream: torch.cuda.Stream, *tensors):
+    """The caller's tensors are not to be reused before `stream` is done with them."""
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
 
 
 def _on(t: torch.Tensor, dtype: torch.dtype, dev: int, name: str) -> int:
@@ -596,11 +609,13 @@ def bitnet_pack_w4(W: torch.Tensor, group: int = 128, stream=None):
     if dev < 0 or dev != _current():
         return _elsewhere(dev, bitnet_pack_w4, W, group, stream)
     N, K = W.shape
-    packed = W.new_empty((N, -(-K // 128) * 64), dtype=torch.uint8)
-    scales = W.new_empty((N, -(-K // group)), dtype=torch.bfloat16)
+    handle = _handle(stream, dev)
+    packed = _new((N, -(-K // 128) * 64), torch.uint8, W.device, stream)
+    scales = _new((N, -(-K // group)), torch.bfloat16, W.device, stream)
     _check(lib.bitnet_pack_w4(_on(W, torch.float32, dev, "W"), N, K, group, packed.data_ptr(),
-                              scales.data_ptr(), _handle(stream, dev)), "bitnet_pack_w4")
-    _keep(stream, packed, scales)
+                              scales.data_ptr(), handle), "bitnet_pack_w4")
+    if stream is not None:
+        _keep(stream, W)
     return packed, scales
 
 
@@ -618,11 +633,11 @@ def bitnet_linear_w4(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor
     dev = x.get_device()
     if dev < 0 or dev != _current():
         return _elsewhere(dev, bitnet_linear_w4, x, packed, scales, group, out_dtype, y, stream)
+    handle = _handle(stream, dev)
     if y is None:
         if out_dtype not in (torch.bfloat16, torch.float32):
             raise ValueError(f"out_dtype must be bfloat16 or float32, got {out_dtype}")
-        y = torch.empty((M, N), dtype=out_dtype, device=x.device)
-        _keep(stream, y)
+        y = _new((M, N), out_dtype, x.device, stream)
         yp = y.data_ptr()
     else:
         _check_out(y, M, N)
@@ -630,10 +645,11 @@ def bitnet_linear_w4(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor
     st = lib.bitnet_linear_w4(_on(x, torch.bfloat16, dev, "x"), M, K,
                               _on(packed, torch.uint8, dev, "packed"),
                               _on(scales, torch.bfloat16, dev, "scales"), group, N, yp,
-                              OUT_BF16 if y.dtype is torch.bfloat16 else OUT_F32,
-                              _handle(stream, dev))
+                              OUT_BF16 if y.dtype is torch.bfloat16 else OUT_F32, handle)
     if st:
         _check(st, "bitnet_linear_w4")
+    if stream is not None:
+        _keep(stream, x, packed, scales, y)
     return y
 
 
@@ -699,7 +715,7 @@ class PagedCache:
                                self.head_dim, CACHE_I8 if i8 else CACHE_BF16)
         self._ref = ctypes.byref(self._c)
         self._sizes = {}  # workspace bytes by call
-        self._scratch = None  # the default stream's workspace (see _scratch)
+        self._kept = threading.local()  # .ws: the default stream's workspace (see _scratch)
 
     def _layer(self, i: int):
         if not 0 <= i < len(self.layers):
@@ -755,18 +771,17 @@ def _slots(cache: PagedCache, t: torch.Tensor, name: str, n: int) -> int:
 
 
 def _scratch(cache: PagedCache, workspace: Optional[torch.Tensor], size: int, stream, handle: int):
-    """The workspace of a call, its address and its bytes. Calls on the legacy default stream share
-    one that the cache keeps: they run one after the other, and that stream cannot be captured, so
-    no graph holds it. Other streams get a new one each time."""
+    """The workspace of a call, its address and its bytes. A thread's calls on the legacy default
+    stream share one that the cache keeps: they run one after the other (those of two threads may
+    mix their kernels), and that stream cannot be captured, so no graph holds it. Other streams get
+    a new one each time."""
     if workspace is None:
         if handle == 0 and stream is None:
-            workspace = cache._scratch
+            workspace = getattr(cache._kept, "ws", None)
             if workspace is None or workspace.shape[0] < size:
-                workspace = cache._scratch = torch.empty(size, dtype=torch.uint8,
-                                                         device=cache.device)
-            return workspace, workspace.data_ptr(), size
-        workspace = torch.empty(size, dtype=torch.uint8, device=cache.device)
-        _keep(stream, workspace)
+                workspace = cache._kept.ws = _new(size, torch.uint8, cache.device, None)
+        else:
+            workspace = _new(size, torch.uint8, cache.device, stream)
         return workspace, workspace.data_ptr(), size
     if workspace.get_device() != cache._dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous on {cache.device}")
@@ -776,8 +791,7 @@ def _scratch(cache: PagedCache, workspace: Optional[torch.Tensor], size: int, st
 def _copies(cache: PagedCache, room: int, copies: Optional[torch.Tensor], stream):
     """A list of page copies with room for `room` pairs: int32 [count, 0, from, to, from, ...]."""
     if copies is None:
-        copies = torch.empty(2 + 2 * room, dtype=torch.int32, device=cache.device)
-        _keep(stream, copies)
+        copies = _new(2 + 2 * room, torch.int32, cache.device, stream)
         return copies, copies.data_ptr(), room
     if copies.dim() != 1 or copies.shape[0] < 2 + 2 * room:
         raise ValueError(f"copies must be one list of at least {2 + 2 * room}")
@@ -796,6 +810,8 @@ def bitnet_cache_fork(cache: PagedCache, src: torch.Tensor, dst: torch.Tensor,
                                _slots(cache, dst, "dst", n), n, wp, wb, handle)
     if st:
         _check(st, "bitnet_cache_fork")
+    if stream is not None:
+        _keep(stream, src, dst, ws)
 
 
 def bitnet_cache_extend(cache: PagedCache, seqs: torch.Tensor, add: torch.Tensor,
@@ -806,13 +822,15 @@ def bitnet_cache_extend(cache: PagedCache, seqs: torch.Tensor, add: torch.Tensor
     dev, n = cache._dev, seqs.shape[0]
     if dev != _current():
         return _elsewhere(dev, bitnet_cache_extend, cache, seqs, add, copies, workspace, stream)
-    copies, cp, room = _copies(cache, n, copies, stream)
     handle = _handle(stream, dev)
+    copies, cp, room = _copies(cache, n, copies, stream)
     ws, wp, wb = _scratch(cache, workspace, cache.workspace_size(n), stream, handle)
     st = lib.bitnet_cache_extend(cache._ref, _slots(cache, seqs, "seqs", n),
                                  _slots(cache, add, "add", n), n, cp, room, wp, wb, handle)
     if st:
         _check(st, "bitnet_cache_extend")
+    if stream is not None:
+        _keep(stream, seqs, add, copies, ws)
     return copies
 
 
@@ -827,6 +845,8 @@ def bitnet_cache_free(cache: PagedCache, seqs: torch.Tensor,
     st = lib.bitnet_cache_free(cache._ref, _slots(cache, seqs, "seqs", n), n, wp, wb, handle)
     if st:
         _check(st, "bitnet_cache_free")
+    if stream is not None:
+        _keep(stream, seqs, ws)
 
 
 def bitnet_cache_compact(cache: PagedCache, copies: Optional[torch.Tensor] = None,
@@ -836,12 +856,14 @@ def bitnet_cache_compact(cache: PagedCache, copies: Optional[torch.Tensor] = Non
     dev = cache._dev
     if dev != _current():
         return _elsewhere(dev, bitnet_cache_compact, cache, copies, workspace, stream)
-    copies, cp, room = _copies(cache, cache.num_pages // 2, copies, stream)
     handle = _handle(stream, dev)
+    copies, cp, room = _copies(cache, cache.num_pages // 2, copies, stream)
     ws, wp, wb = _scratch(cache, workspace, cache.workspace_size(0), stream, handle)
     st = lib.bitnet_cache_compact(cache._ref, cp, room, wp, wb, handle)
     if st:
         _check(st, "bitnet_cache_compact")
+    if stream is not None:
+        _keep(stream, copies, ws)
     return copies
 
 
@@ -858,6 +880,8 @@ def bitnet_cache_copy(cache: PagedCache, copies: torch.Tensor, stream=None) -> N
                                (copies.shape[0] - 2) // 2, _handle(stream, dev))
     if st:
         _check(st, "bitnet_cache_copy")
+    if stream is not None:
+        _keep(stream, copies)
 
 
 def bitnet_cache_append(cache: PagedCache, layer: int, k: torch.Tensor, v: torch.Tensor,
@@ -881,6 +905,8 @@ def bitnet_cache_append(cache: PagedCache, layer: int, k: torch.Tensor, v: torch
         None if pos is None else _slots(cache, pos, "pos", T), _handle(stream, dev))
     if st:
         _check(st, "bitnet_cache_append")
+    if stream is not None:
+        _keep(stream, k, v, seqs, pos)
 
 
 def bitnet_paged_attention(q: torch.Tensor, cache: PagedCache, layer: int = 0,
@@ -906,10 +932,10 @@ def bitnet_paged_attention(q: torch.Tensor, cache: PagedCache, layer: int = 0,
         raise ValueError(f"q must be (B, heads, {D}), got {tuple(shape)}")
     if seqs is None and B > cache.max_seqs:
         raise ValueError(f"{B} queries for {cache.max_seqs} slots: give seqs")
+    handle = _handle(stream, dev)
     qp = _on(q, torch.bfloat16, dev, "q")
     if out is None:
-        out = torch.empty_like(q)
-        _keep(stream, out)
+        out = torch.empty_like(q) if stream is None else _new(shape, q.dtype, q.device, stream)
         op = out.data_ptr()
     elif out.shape == shape:
         op = _on(out, torch.bfloat16, dev, "out")
@@ -921,10 +947,8 @@ def bitnet_paged_attention(q: torch.Tensor, cache: PagedCache, layer: int = 0,
             raise ValueError(f"lse must be ({B}, {heads}), got {tuple(lse.shape)}")
         lp = _on(lse, torch.float32, dev, "lse")
     elif return_lse:
-        lse = torch.empty((B, heads), dtype=torch.float32, device=cache.device)
-        _keep(stream, lse)
+        lse = _new((B, heads), torch.float32, cache.device, stream)
         lp = lse.data_ptr()
-    handle = _handle(stream, dev)
     ws, wp, wb = _scratch(cache, workspace, cache.attention_workspace_size(B, heads), stream, handle)
     st = lib.bitnet_paged_attention(
         cache._ref, cache._layer(layer), qp, B, heads,
@@ -932,6 +956,8 @@ def bitnet_paged_attention(q: torch.Tensor, cache: PagedCache, layer: int = 0,
         D ** -0.5 if scale is None else scale, window, sinks, op, lp, wp, wb, handle)
     if st:
         _check(st, "bitnet_paged_attention")
+    if stream is not None:
+        _keep(stream, q, seqs, out, lse, ws)
     return out if lse is None else (out, lse)
 
 

@@ -222,7 +222,8 @@ bitnet_status bitnet_paged_attention(const bitnet_cache* cache, const bitnet_cac
     if (!layer || !q || !out) return BITNET_ERR_NULL;
     if ((st = check_heads(p.c.kv_heads, B, heads)) != BITNET_OK) return st;
     if (window < 0 || sinks < 0) return BITNET_ERR_SHAPE;
-    if (!(scale > -3.0e38f && scale < 3.0e38f)) return BITNET_ERR_UNSUPPORTED;
+    // (times log2 e it stays finite)
+    if (!(scale > -2.0e38f && scale < 2.0e38f)) return BITNET_ERR_UNSUPPORTED;
     if ((st = check_layer(p.c, *layer)) != BITNET_OK) return st;
     if (!aligned(q, 16) || !aligned(out, 16) || (lse && !aligned(lse, 4)) ||
         (seqs && !aligned(seqs, 4)))

@@ -15,8 +15,8 @@
 // Split. The tokens of all (sequence, key/value head, block of 16 heads) items are cut into units
 // of 64 or 128, and every CTA takes an equal, contiguous share of all units, so that one long
 // sequence among short ones keeps the whole GPU busy. The lengths are on the device, so each CTA
-// finds its share there. A CTA's four warps take a quarter of each unit and load them through a ring of
-// their own (cp.async, 16 bytes a lane, no barrier between warps); at the end of an item, or of
+// finds its share there. A CTA's four warps take a quarter of each unit and load them through a ring
+// of their own (cp.async, 16 bytes a lane, no barrier between warps); at the end of an item, or of
 // the CTA's share, the four states are joined in shared memory, and the result goes out, or into
 // the workspace if other CTAs hold parts of the item. A second kernel joins those, in order.
 #include <cuda_bf16.h>
@@ -51,9 +51,9 @@ struct Shape {
     static constexpr int kUnit = kTile * kWarps;
     static constexpr int kPool = kTile * kRowBytes;  // K or V of one tile
     static constexpr int kStageBytes = 2 * kPool + (I8 ? 2 * kTile * 4 : 0);
-    // CTAs per SM and stages of the ring: a third CTA where registers allow, with two stages for rows
-    // of 128 bytes (D = 64 in bf16, 64 sequences in a window of 4100 tokens: 3.5 µs less than with
-    // two CTAs of three stages; D = 128 in 8 bits, 8 sequences of up to 65536: 8 µs less).
+    // CTAs per SM and stages of the ring: a third CTA where registers allow, with two stages for
+    // rows of 128 bytes (D = 64 in bf16, 64 sequences in a window of 4100 tokens: 3.5 µs less than
+    // with two CTAs of three stages; D = 128 in 8 bits, 8 sequences of up to 65536: 8 µs less).
     static constexpr int kCtas = D == 64 || (I8 && NH == 1) ? 3 : 2;
     static constexpr int kStages = kCtas == 3 && kRowBytes == 128 ? 2 : 3;
     // Shared memory in which the warps' states are joined.
@@ -73,8 +73,8 @@ struct Note {
 };
 struct AttnWs {
     int64_t* head;  // [0] CTAs, [1] units
-    Note* note;   // [cta]
-    float* part;  // [cta][2][kRows * D + 2 * kRows]: o, then m, then l
+    Note* note;     // [cta]
+    float* part;    // [cta][2][kRows * D + 2 * kRows]: o, then m, then l
 };
 
 __host__ __device__ inline AttnWs attn_ws(void* ws, int most_ctas) {
@@ -262,8 +262,8 @@ __device__ __forceinline__ uint32_t tile_at(int row, int chunk) {
     return uint32_t(row * RB + ((chunk ^ swz) << 4));
 }
 
-// Tokens (scores) and dimensions (output) are the rows of the
-// products and heads their columns, so that up to eight heads cost one column block.
+// Tokens (scores) and dimensions (output) are the rows of the products and heads their columns, so
+// that up to eight heads cost one column block.
 template <int D, bool I8, int NH>
 __global__ void __launch_bounds__(kThreads, Shape<D, I8, NH>::kCtas)
     attn_kernel(const __grid_constant__ AttnParams p) {
@@ -745,7 +745,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8, NH>::kCtas)
                         for (int w = 0; w < kWarps; ++w)
                             t += sh.l[w][r] * exp2_fast(sh.m[w][r] - b);
                         p.out[(int64_t(cur.b) * p.heads + head0 + r) * D + d0 + d] =
-                            __bfloat16_as_ushort(__float2bfloat16_rn(t > 0.0f ? v / t : 0.0f));
+                            __bfloat16_as_ushort(__float2bfloat16_rn(t == 0.0f ? 0.0f : v / t));
                     } else {
                         part[r * D + d0 + d] = v;
                     }
@@ -766,7 +766,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8, NH>::kCtas)
                     part[kRows * D + kRows + r] = t;
                 } else if (p.lse) {
                     p.lse[int64_t(cur.b) * p.heads + head0 + r] =
-                        t > 0.0f ? (b + log2f(t)) * kLn2 : -INFINITY;
+                        t == 0.0f ? -INFINITY : (b + log2f(t)) * kLn2;
                 }
             }
             __syncthreads();
@@ -777,11 +777,11 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8, NH>::kCtas)
     cp_async_wait<0>();
 }
 
-// Joins the parts of the items that several CTAs worked on: blockIdx.x stands for a CTA of the split
-// and takes head blockIdx.y of the item that goes on behind its share, if one does. A thread has four
-// dimensions; groups of D / 4 threads take every n-th part, and their states join in a fixed order.
-// Few CTAs have something to do, so they are small (64 sequences in a window of 4100 tokens: 84 µs
-// for both kernels, 87 with 256 threads, 97 with a CTA of 512 per query and head).
+// Joins the parts of the items that several CTAs worked on: blockIdx.x stands for a CTA of the
+// split and takes head blockIdx.y of the item that goes on behind its share, if one does. A thread
+// has four dimensions; groups of D / 4 threads take every n-th part, and their states join in a
+// fixed order. Few CTAs have something to do, so they are small (64 sequences in a window of 4100
+// tokens: 84 µs for both kernels, 87 with 256 threads, 97 with a CTA of 512 per query and head).
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttnParams p) {
     constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes, kAtOnce = 4;
@@ -852,13 +852,13 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
         o.z += v.z * f;
         o.w += v.w * f;
     }
-    const float scale = total > 0.0f ? 1.0f / total : 0.0f;
+    const float scale = total == 0.0f ? 0.0f : 1.0f / total;  // (a NaN stays one)
     const int64_t row = int64_t(note.b) * p.heads + note.head0 + r;
     const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * scale, o.y * scale);
     const __nv_bfloat162 hi = __floats2bfloat162_rn(o.z * scale, o.w * scale);
     *reinterpret_cast<uint2*>(p.out + row * D + 4 * d) =
         make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-    if (p.lse && d == 0) p.lse[row] = total > 0.0f ? (top + log2f(total)) * kLn2 : -INFINITY;
+    if (p.lse && d == 0) p.lse[row] = total == 0.0f ? -INFINITY : (top + log2f(total)) * kLn2;
 }
 
 template <int D, bool I8, int NH>
@@ -868,7 +868,8 @@ cudaError_t launch_one(const AttnParams& p, cudaStream_t stream) {
     cudaError_t e = allow_smem(attn_kernel<D, I8, NH>, Sh::kSmem, allowed);
     if (e != cudaSuccess) return e;
     // CTAs of the split: as many as the GPU holds at once, whatever the lengths will be
-    e = launch_pdl(attn_kernel<D, I8, NH>, dim3(tc_num_sms() * Sh::kCtas), kThreads, Sh::kSmem, stream, p);
+    e = launch_pdl(attn_kernel<D, I8, NH>, dim3(tc_num_sms() * Sh::kCtas), kThreads, Sh::kSmem,
+                   stream, p);
     if (e != cudaSuccess) return e;
     const int group = p.heads / p.c.kv_heads;
     return launch_pdl(join_kernel<D>, dim3(tc_num_sms() * Sh::kCtas, group < kRows ? group : kRows),

@@ -60,11 +60,12 @@ __global__ void __launch_bounds__(kW4Threads) pack_w4_kernel(const float* __rest
 // A CTA is one or two teams of eight warps (one where two CTAs fit on an SM, so that the next
 // call's can start as this one's end; two that share x where it takes more room). Rows are dealt
 // out evenly over the teams, by 16 where each has more, and done in tiles of 16 RT; a team's warps
-// take every eighth block of 128 weights of a tile (512 bytes of a row per step of the team) and add their sums in shared memory, in order. Every
-// warp loads its blocks through a ring of its own (cp.async, no barrier between warps), across
-// tiles, and fills it before the previous kernel of the stream has ended (weights do not depend on
-// it). x and the scales come from shared memory: read by fragments from global memory, the eight
-// rows of an instruction cost the L1 a tag lookup each.
+// take every eighth block of 128 weights of a tile (512 bytes of a row per step of the team) and
+// add their sums in shared memory, in order. Every warp loads its blocks through a ring of its own
+// (cp.async, no barrier between warps), across tiles, and fills it before the previous kernel of
+// the stream has ended (weights do not depend on it). x and the scales come from shared memory:
+// read by fragments from global memory, the eight rows of an instruction cost the L1 a tag lookup
+// each.
 constexpr int kW4Warps = 8;  // of a team
 constexpr int kW4Teams = 2;  // most of a CTA, and of an SM
 constexpr int kW4Stages = 4;

@@ -158,6 +158,7 @@ def test_attention_refusals(bn):
     assert call(B=0) == call(B=(1 << 20) + 1) == call(heads=7) == call(heads=0) == bn.ERR_SHAPE
     assert call(heads=16386) == call(window=-1) == call(sinks=-1) == bn.ERR_SHAPE
     assert call(scale=float("nan")) == call(scale=float("inf")) == bn.ERR_UNSUPPORTED
+    assert call(scale=2.5e38) == call(scale=-2.5e38) == bn.ERR_UNSUPPORTED
     assert call(q=FAKE + 8) == call(out=FAKE + 2) == call(lse=FAKE + 2) == bn.ERR_ALIGN
     assert call(seqs=FAKE + 2) == call(ws=FAKE + 128) == bn.ERR_ALIGN
     size = bn.lib.bitnet_paged_attention_workspace_size

@@ -1,5 +1,7 @@
 """bitnet_paged_attention against 64-bit attention over the same tokens. The tolerances are those
 that decode_ref.attention derives from binary32 arithmetic, plus one rounding to bf16."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -165,6 +167,37 @@ def test_hidden_tokens_may_hold_anything(bn):
         out, lse = bn.bitnet_paged_attention(q, cache, window=40, sinks=2, return_lse=True)
         assert torch.equal(out, want) and torch.equal(lse, want_lse)
         assert cache.errors() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.int8])
+def test_nan_in_sight_shows(bn, dtype):
+    """A NaN in q, or in a visible token, comes out where the formula has one and nowhere else: in
+    items of one CTA and in ones that several CTAs share."""
+    cache = _fill(bn, [21, 4000], 2, 64, 16, dtype)
+    q = _q(2, 8, 64)
+    for b in range(2):  # one dimension of one query head
+        bad = q.clone()
+        bad[b, 3, 5] = float("nan")
+        out, lse = bn.bitnet_paged_attention(bad, cache, return_lse=True)
+        assert out[b, 3].isnan().all() and lse[b, 3].isnan()
+        clean, clean_lse = bn.bitnet_paged_attention(q, cache, return_lse=True)
+        out[b, 3], lse[b, 3] = clean[b, 3], clean_lse[b, 3]
+        _check(cache, q, out, lse)
+    for w in range(2):  # a token of key/value head 1 (query heads 4 to 7), of K or of V
+        for s, j in ((0, 20), (1, 2345)):
+            at = (int(cache.table[s, j // 16]), 1, j % 16)
+            pool, i = (cache.layers[0][w], at + (7,)) if dtype == torch.bfloat16 else \
+                (cache.layers[0][2 + w], at)
+            keep = pool[i].item()
+            pool[i] = float("nan")
+            out, lse = bn.bitnet_paged_attention(q, cache, return_lse=True)
+            pool[i] = keep
+            want = torch.zeros_like(out, dtype=torch.bool)
+            want[s, 4:, slice(7, 8) if w and dtype == torch.bfloat16 else slice(None)] = True
+            assert torch.equal(out.isnan(), want)
+            want = torch.zeros_like(lse, dtype=torch.bool)
+            want[s, 4:] = w == 0
+            assert torch.equal(lse.isnan(), want)
 
 
 def test_bad_pages_and_slots_are_skipped_and_reported(bn):
@@ -367,12 +400,12 @@ def test_default_stream_shares_scratch_and_others_do_not(bn):
     qs = [_q(2, 8, 128, s) for s in (1, 2, 3)]
     want = [bn.bitnet_paged_attention(q, cache) for q in qs]
     small = bn.bitnet_paged_attention(qs[0][:1], cache, seqs=_dev([1]))
-    kept = cache._scratch
+    kept = cache._kept.ws
     assert kept is not None
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         captured = bn.bitnet_paged_attention(qs[1], cache)
-    assert cache._scratch is kept
+    assert cache._kept.ws is kept
     side = torch.cuda.Stream()
     torch.cuda.synchronize()
     for _ in range(10):
@@ -384,4 +417,54 @@ def test_default_stream_shares_scratch_and_others_do_not(bn):
         torch.cuda.synchronize()
         assert torch.equal(a, want[0]) and torch.equal(b, want[2]) and torch.equal(c, small)
         assert torch.equal(captured, want[1])
-    assert cache._scratch is kept
+    assert cache._kept.ws is kept
+
+
+def test_two_threads_on_the_default_stream(bn):
+    """Their calls may mix on the stream; each thread has a workspace of its own."""
+    cache = _fill(bn, [9000, 700], 2, 128, 16, torch.bfloat16)
+    qs = [_q(2, 8, 128, s) for s in (1, 2)]
+    want = [bn.bitnet_paged_attention(q, cache, return_lse=True) for q in qs]
+    wrong = []
+
+    def work(i):
+        for _ in range(200):
+            got = bn.bitnet_paged_attention(qs[i], cache, return_lse=True)
+            if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
+                wrong.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
+def test_tensors_of_a_call_on_another_stream_live_long_enough(bn):
+    """With stream given: what the caller drops after the call, and what the call allocates while
+    the current stream still works on memory that it has given back."""
+    cache = _fill(bn, [300, 77], 2, 64, 16, torch.int8)
+    q = _q(2, 8, 64)
+    want = bn.bitnet_paged_attention(q, cache)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        early = q.clone()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+        out = bn.bitnet_paged_attention(early, cache, stream=side)
+        del early
+        junk = [torch.full_like(q, 9.0) for _ in range(8)]  # the dropped query's memory, if free
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        del junk, out
+        late = torch.empty_like(q)
+        torch.cuda._sleep(20_000_000)
+        late.fill_(9.0)
+        del late  # free for the current stream, which has yet to write it
+        out = bn.bitnet_paged_attention(q, cache, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        del out
