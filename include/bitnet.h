@@ -374,9 +374,11 @@ bitnet_status bitnet_linear_b3(const uint16_t* x, int64_t M, int64_t K, const ui
  *   ties to even; the clamp to -8 never acts).
  * bitnet_linear_w4 — the forward for any M >= 1, 16 or 32 tokens per pass over the weights: made
  *   for decode, where the time is that of reading the weights once; a prompt of M tokens reads
- *   them M / 32 to M / 16 times. Codes are exact in bf16; products and sums run in
- *   binary32 (sums within a group, times the scale, added over the groups in a fixed order, so
- *   results are the same on every run), and y is rounded once at the end.
+ *   them M / 32 to M / 16 times. Products are exact; sums run in binary32 (within a group, times
+ *   the scale, added over the groups in a fixed order, so results are the same on every run), and y
+ *   is rounded once at the end. For up to four tokens of large layers x is rounded to 2^-28 times
+ *   the power of two below the largest value of each 128 of a row, and sums within a group are
+ *   exact.
  *   A row of x that holds an Inf or NaN gives unspecified values in that row of y only.
  *   Rows of up to BITNET_W4_MAX_GROUPS groups (BITNET_ERR_UNSUPPORTED beyond). Under programmatic
  *   dependent launch the weights are read before the previous kernel of the stream has ended: a

@@ -66,6 +66,13 @@ __global__ void __launch_bounds__(kW4Threads) pack_w4_kernel(const float* __rest
 // the stream has ended (weights do not depend on it). x and the scales come from shared memory:
 // read by fragments from global memory, the eight rows of an instruction cost the L1 a tag lookup
 // each.
+//
+// In bf16 a word's eight weights cost eleven instructions to unpack, and instructions, not HBM, bound
+// large layers (131071 x 4096 at 68 % of the copy rate). Few tokens therefore go in bytes: x as
+// integers in units of 2^-28 of the largest value of a block (what smaller values lose is less than
+// binary32 sums of the block would), cut into four signed bytes, which take four of a product's
+// columns; eight weights are then three instructions, the sums of a group are exact in 32-bit
+// integers, and one subtraction makes a float of each (96 % there at one token).
 constexpr int kW4Warps = 8;  // of a team
 constexpr int kW4Teams = 2;  // most of a CTA, and of an SM
 constexpr int kW4Stages = 4;
@@ -114,26 +121,98 @@ __device__ __forceinline__ void w4_mma_new(float (&d)[4], uint32_t a0, uint32_t 
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
+// Four of a word's eight weights as signed bytes 16 t: the high nibbles (words shifted left by 4:
+// the low ones), in the order 2 6 3 7 (0 4 1 5). One mask and one change of the sign bit, in one
+// logic instruction.
+__device__ __forceinline__ uint32_t w4_bytes(uint32_t word) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(r) : "r"(word), "n"(0xF0F0F0F0), "r"(0x80808080));
+    return r;
+}
+
+__device__ __forceinline__ void w4_mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same on kW4Zero, whose bits are those of the float 1.5 * 2^23: sums v of less than 2^22 make
+// it the float 1.5 * 2^23 + v, so that one subtraction turns them into floats.
+constexpr int kW4Zero = 0x4B400000;
+__device__ __forceinline__ void w4_mma_s8_new(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%10,%10,%10};"
+        : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(kW4Zero));
+}
+
+// Eight values of x as 30-bit integers in units of 2^(E - 155) (E: the biased exponent of the
+// largest of their block, at least 13), cut into four signed bytes each, of weights 1, 2^8, 2^15 and
+// 2^23: to[128 d + half] (of odd d: to[128 d + 64 - half]) gets byte d of the values in the order of
+// w4_bytes, low nibbles first.
+__device__ __forceinline__ void w4_digits(const uint4& v, int E, uint8_t* to, int half) {
+    // Adding 1.5 * 2^23 rounds to an integer and leaves it in the low bits; the 128 more carry what
+    // makes the low byte signed, up to its sign bit.
+    constexpr float kRound = 12582912.0f + 128.0f;
+    const float scale = __uint_as_float(uint32_t(267 - E) << 23);
+    uint32_t y[2][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t w = (&v.x)[i >> 1];
+        const float h = (i & 1 ? bf16_hi(w) : bf16_lo(w)) * scale;  // below 2^14, exactly
+        const float a = h + kRound;
+        const float b = fmaf(h - (a - kRound), 32768.0f, kRound);  // of at most 2^14
+        y[0][i] = __float_as_uint(b);
+        y[1][i] = __float_as_uint(a);
+    }
+#pragma unroll
+    for (int d = 0; d < 2; ++d) {
+        const uint32_t a = __byte_perm(y[d][0], y[d][4], 0x5140);
+        const uint32_t b = __byte_perm(y[d][1], y[d][5], 0x5140);
+        const uint32_t e = __byte_perm(y[d][2], y[d][6], 0x5140);
+        const uint32_t f = __byte_perm(y[d][3], y[d][7], 0x5140);
+        *reinterpret_cast<uint2*>(to + d * 256 + half) =
+            make_uint2(__byte_perm(a, b, 0x5410) ^ 0x80808080u,
+                       __byte_perm(e, f, 0x5410) ^ 0x80808080u);
+        *reinterpret_cast<uint2*>(to + d * 256 + 128 + 64 - half) =
+            make_uint2(__byte_perm(a, b, 0x7632), __byte_perm(e, f, 0x7632));
+    }
+}
+
+// Where x comes from: global memory through L1, shared memory, or shared memory as signed bytes
+// (four columns of a product for each token, its four bytes).
+enum W4X { kGlobal, kShared, kBytes };
+__host__ __device__ constexpr int w4_tokens(W4X xm) { return xm == kBytes ? 2 : 8; }  // of a product
+
 // Shared memory of a call: the rings, the teams' reduction buffers, two tiles' scales for each team
 // as (group, row) with one row more, so that neither reads nor writes meet in a bank (those of a
-// last, half block filled up with zeros), and x as (block, pair of tokens, quarter, token, 64
-// bytes), zeros behind K: what a lane reads of either lies at fixed distances.
+// last, half block filled up with zeros), and x, zeros behind K, as (block, pair of tokens, quarter,
+// token, 64 bytes), or in bytes as (block, token, half, byte, c of a quarter, quarter, 8 bytes) and
+// the units (block, token): what a lane reads of any lies at fixed distances.
 struct W4Layout {
-    uint32_t red, scales, x, bytes;  // offsets; the rings come first
+    uint32_t red, scales, x, units, bytes;  // offsets; the rings come first
 };
 __host__ __device__ inline W4Layout w4_layout(int teams, int nt, int ng, int rt, int blocks,
-                                              int tokens, bool xs) {
+                                              int tokens, W4X xm) {
     W4Layout l;
     l.red = teams * kW4Warps * kW4Stages * rt * 1024;
-    l.scales = l.red + teams * kW4Warps * nt * 8 * rt * kW4Pad * 4;
+    l.scales = l.red + teams * kW4Warps * nt * w4_tokens(xm) * rt * kW4Pad * 4;
     l.x = l.scales + (teams * 2 * (16 * rt + 1) * 2 * blocks * ng + 15) / 16 * 16;
-    l.bytes = l.x + (xs ? blocks * 512 * ((tokens + 1) / 2) : 0);
+    l.units = l.x + (xm == kBytes    ? blocks * 512 * tokens
+                     : xm == kShared ? blocks * 512 * ((tokens + 1) / 2)
+                                     : 0);
+    l.bytes = l.units + (xm == kBytes ? blocks * tokens * 4 : 0);
     return l;
 }
 
-// NT: tiles of 8 tokens; NG: groups per block (1, 2 or 4); RT: tiles of 16 rows that share a load
-// of x; XS: x is in shared memory (otherwise read through L1).
-template <int NT, int NG, int RT, bool XS>
+// NT: column tiles, of 8 tokens or of 2 in bytes; NG: groups per block (1, 2 or 4); RT: tiles of 16
+// rows that share a load of x; XM: where x comes from.
+template <int NT, int NG, int RT, W4X XM>
 __global__ void __launch_bounds__(32 * kW4Warps * kW4Teams, 1)
     linear_w4_kernel(const __grid_constant__ W4Params p) {
     constexpr int S = kW4Stages;
@@ -141,6 +220,7 @@ __global__ void __launch_bounds__(32 * kW4Warps * kW4Teams, 1)
     constexpr int kStage = RT * 1024;      // bytes of a block of a tile
     constexpr int kStep = kW4Warps * 64;   // bytes from one block of a warp to its next
     constexpr int kHeld = 4;               // scales per lane and row that are prefetched
+    constexpr int kTok = NT * w4_tokens(XM);
     extern __shared__ __align__(128) uint8_t w4_dyn[];
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const int team = threadIdx.x >> 8, warp = threadIdx.x >> 5 & (kW4Warps - 1);
@@ -151,18 +231,18 @@ __global__ void __launch_bounds__(32 * kW4Warps * kW4Teams, 1)
     // costs as much as a full one: 14336 x 4096 at one token 10.7 against 11.0 µs).
     const int64_t deal = p.N > 16 * teams ? 16 : 1, deals = (p.N + deal - 1) / deal;
     const int64_t r0 = deals * me / teams * deal, r1 = min(deals * (me + 1) / teams * deal, p.N);
-    const int64_t m0 = int64_t(blockIdx.y) * (8 * NT);
-    const int tokens = static_cast<int>(p.M - m0 < 8 * NT ? p.M - m0 : 8 * NT);
+    const int64_t m0 = int64_t(blockIdx.y) * kTok;
+    const int tokens = static_cast<int>(p.M - m0 < kTok ? p.M - m0 : kTok);
     const int rows = static_cast<int>(r1 - r0), tiles = (rows + kRowsTile - 1) / kRowsTile;
     // This warp's blocks of a tile (a team may be without rows).
     const int mine = tiles ? (p.blocks - warp + kW4Warps - 1) / kW4Warps : 0;
     const int64_t row_bytes = int64_t(p.blocks) * 64;
     constexpr int kPitch = kRowsTile + 1;
     const int filled = p.blocks * NG;
-    const int pair = 512 * ((tokens + 1) / 2);  // bytes of a block of x
-    const W4Layout lay = w4_layout(cta_teams, NT, NG, RT, p.blocks, tokens, XS);
+    const int pair = 512 * (XM == kBytes ? tokens : (tokens + 1) / 2);  // bytes of a block of x
+    const W4Layout lay = w4_layout(cta_teams, NT, NG, RT, p.blocks, tokens, XM);
     float* const red = reinterpret_cast<float*>(w4_dyn + lay.red) +
-                       team * (kW4Warps * NT * 8 * RT * kW4Pad);
+                       team * (kW4Warps * kTok * RT * kW4Pad);
     uint16_t* const scales = reinterpret_cast<uint16_t*>(w4_dyn + lay.scales) +
                              team * (2 * kPitch * filled);
     const uint8_t* const ring = w4_dyn + (team * kW4Warps + warp) * (S * kStage);
@@ -235,7 +315,7 @@ __global__ void __launch_bounds__(32 * kW4Warps * kW4Teams, 1)
         store_scales(0);
     }
     pdl_wait();
-    if (XS) {
+    if (XM != kGlobal) {
         // Pieces of 8 values, U places of V tokens per thread on their way at once.
         auto bring = [&](auto u_, auto v_) {
             constexpr int U = decltype(u_)::value, V = decltype(v_)::value;
@@ -258,43 +338,117 @@ __global__ void __launch_bounds__(32 * kW4Warps * kW4Teams, 1)
 #pragma unroll
                         for (int m = 0; m < V; ++m) {
                             const int i = i0 + u * step;
-                            if (m1 + m < tokens && i < places)
+                            if (m1 + m >= tokens || i >= places) continue;
+                            if (XM == kBytes) {
+                                // 16 neighbours, alike in the conditions above, hold a block
+                                const uint32_t top = __reduce_max_sync(
+                                    0xFFFFu << (threadIdx.x & 16), absmax8_bits(v[u][m]));
+                                const int E = max(int(top >> 7), 13);
+                                const int at = (i >> 4) * tokens + m1 + m;
+                                w4_digits(v[u][m], E,
+                                          w4_dyn + lay.x + at * 512 + (i & 3) * 16 +
+                                              (i >> 2 & 1) * 8,
+                                          (i >> 3 & 1) * 64);
+                                // 2^(E - 136), 2^23 / 16 of the unit (see the joining of the
+                                // bytes' sums); NaN for a block with an Inf or NaN
+                                if ((i & 15) == 0)
+                                    reinterpret_cast<uint32_t*>(w4_dyn + lay.units)[at] =
+                                        E == 255 ? 0x7FC00000u : uint32_t(E - 9) << 23;
+                            } else {
                                 *reinterpret_cast<uint4*>(
                                     w4_dyn + lay.x + (i >> 4) * pair + (m1 + m >> 1) * 512 +
                                     (i >> 2 & 3) * 128 + (m1 + m & 1) * 64 + (i & 3) * 16) =
                                     v[u][m];
+                            }
                         }
                 }
         };
         if (tokens == 1)
             bring(std::integral_constant<int, 4>(), std::integral_constant<int, 1>());
+        else if (XM == kBytes && NT == 1)
+            bring(std::integral_constant<int, 4>(), std::integral_constant<int, 2>());
+        else if (XM == kBytes)
+            bring(std::integral_constant<int, 2>(), std::integral_constant<int, 4>());
         else
             bring(std::integral_constant<int, 1>(), std::integral_constant<int, 8>());
     }
     __syncthreads();
 
-    // This lane's x: token 8 t + g of the tile, 8 values of a quarter block. Columns behind the
-    // last token repeat it and are not written.
+    // This lane's x: token 8 t + g of the tile, 8 values of a quarter block, or byte g % 4 of token
+    // 2 t + g / 4, and the units of the columns that it holds sums of. Columns behind the last token
+    // repeat it and are not written.
     const uint8_t* xo[NT];
     const uint16_t* xg[NT];
+    const float* units[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
+        if (XM == kBytes) {
+            xo[t] = w4_dyn + lay.x + warp * pair + min(2 * t + (g >> 2), tokens - 1) * 512 +
+                    (g & 3) * 128 + (g & 1) * 64 + c * 16;
+            units[t] = reinterpret_cast<const float*>(w4_dyn + lay.units) + warp * tokens +
+                       min(2 * t + (c >> 1), tokens - 1);
+            continue;
+        }
         const int m = min(8 * t + g, tokens - 1);
         xo[t] = w4_dyn + lay.x + warp * pair + (m >> 1) * 512 + (m & 1) * 64 + c * 16;
         xg[t] = p.x + (m0 + m) * p.K + warp * 128 + 8 * c;
     }
-    // Without XS the last block's empty half is not read; it falls to one warp.
-    const bool cut = !XS && p.K % 128 != 0 && (p.blocks - 1) % kW4Warps == warp;
+    const int x_half = g & 1 ? -64 : 64;
+    // In global memory the last block's empty half is not read; it falls to one warp.
+    const bool cut = XM == kGlobal && p.K % 128 != 0 && (p.blocks - 1) % kW4Warps == warp;
 
     // One block of 128 weights by the tile's first R row tiles (the others have no rows).
     auto block = [&](auto R, const uint8_t* at, const uint16_t* sa, int xa, int64_t xv0, bool half,
-                     float (&acc)[RT][NT][4]) {
+                     int ua, float (&acc)[RT][NT][4]) {
         constexpr int kR = decltype(R)::value, kWords = 4 / NG;
         uint4 wa[kR], wb[kR];
 #pragma unroll
         for (int r = 0; r < kR; ++r) {
             wa[r] = *reinterpret_cast<const uint4*>(at + r * 1024);
             wb[r] = *reinterpret_cast<const uint4*>(at + r * 1024 + 512);
+        }
+        if constexpr (XM == kBytes) {
+            int part[kR][NT][4];
+            uint4 xv[NT][2];
+            float unit[NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                xv[t][0] = *reinterpret_cast<const uint4*>(xo[t] + xa);
+                xv[t][1] = *reinterpret_cast<const uint4*>(xo[t] + xa + x_half);
+                unit[t] = units[t][ua];
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int r = 0; r < kR; ++r) {
+                    const uint32_t a = (&wa[r].x)[j], b = (&wb[r].x)[j];
+                    const uint32_t a0 = w4_bytes(a << 4), a1 = w4_bytes(b << 4),
+                                   a2 = w4_bytes(a), a3 = w4_bytes(b);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        const uint4& x = xv[t][j >> 1];
+                        const uint32_t b0 = j & 1 ? x.z : x.x, b1 = j & 1 ? x.w : x.y;
+                        if (j % kWords == 0)
+                            w4_mma_s8_new(part[r][t], a0, a1, a2, a3, b0, b1);
+                        else
+                            w4_mma_s8(part[r][t], a0, a1, a2, a3, b0, b1);
+                    }
+                    if (j % kWords == kWords - 1) {  // a group ends
+                        const uint16_t* q = sa + 16 * r + j / kWords * kPitch;
+                        const float s0 = __uint_as_float(uint32_t(q[0]) << 16);
+                        const float s1 = __uint_as_float(uint32_t(q[8]) << 16);
+                        const float zero = __int_as_float(kW4Zero);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            const float q0 = s0 * unit[t], q1 = s1 * unit[t];
+                            acc[r][t][0] += q0 * (__int_as_float(part[r][t][0]) - zero);
+                            acc[r][t][1] += q0 * (__int_as_float(part[r][t][1]) - zero);
+                            acc[r][t][2] += q1 * (__int_as_float(part[r][t][2]) - zero);
+                            acc[r][t][3] += q1 * (__int_as_float(part[r][t][3]) - zero);
+                        }
+                    }
+                }
+            return;
         }
         float part[kR][NT][4];
 #pragma unroll
@@ -303,7 +457,7 @@ __global__ void __launch_bounds__(32 * kW4Warps * kW4Teams, 1)
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 xv[t] = make_uint4(0, 0, 0, 0);
-                if (XS)
+                if (XM == kShared)
                     xv[t] = *reinterpret_cast<const uint4*>(xo[t] + xa + j * 128);
                 else if (j < 2 || !half)
                     xv[t] = __ldg(reinterpret_cast<const uint4*>(xg[t] + xv0 + 32 * j));
@@ -346,6 +500,7 @@ __global__ void __launch_bounds__(32 * kW4Warps * kW4Teams, 1)
         const uint16_t* sa = scales + (tile & 1) * (kPitch * filled) + warp * NG * kPitch + g;
         int xa = 0;  // bytes from the warp's first block of x to this one
         int64_t xv0 = 0;
+        int ua = 0;
         for (int todo = mine; todo > 0; todo -= S) {
 #pragma unroll
             for (int i = 0; i < S; ++i) {
@@ -355,38 +510,54 @@ __global__ void __launch_bounds__(32 * kW4Warps * kW4Teams, 1)
                     const uint8_t* at = ring + i * kStage + g * 64 + c * 16;
                     const bool half = cut && i == todo - 1;
                     if (RT == 1 || below > 16)
-                        block(std::integral_constant<int, RT>(), at, sa, xa, xv0, half, acc);
+                        block(std::integral_constant<int, RT>(), at, sa, xa, xv0, half, ua,
+                              acc);
                     else
-                        block(std::integral_constant<int, 1>(), at, sa, xa, xv0, half, acc);
+                        block(std::integral_constant<int, 1>(), at, sa, xa, xv0, half, ua, acc);
                     __syncwarp();  // all lanes have read the stage
                 }
                 load(i);
                 sa += kW4Warps * NG * kPitch;
                 xa += kW4Warps * pair;
                 xv0 += kW4Warps * 128;
+                ua += kW4Warps * tokens;
             }
             advance();
         }
         // A tile is done: the warps' sums, in order.
-        float* own = red + warp * (NT * 8 * RT * kW4Pad);
+        float* own = red + warp * (kTok * RT * kW4Pad);
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll
             for (int t = 0; t < NT; ++t)
+                if (XM == kBytes) {
+                    // Lanes of even c hold the sums of the bytes of weights 1 and 2^8, those of odd c
+                    // of 2^15 and 2^23, all times 2^23: the largest is as large as the result.
+                    const float f = c & 1 ? 0x1p-8f : 0x1p-23f;
+                    float u0 = acc[r][t][0] * f + acc[r][t][1] * (256.0f * f);
+                    float u1 = acc[r][t][2] * f + acc[r][t][3] * (256.0f * f);
+                    u0 += __shfl_xor_sync(0xFFFFFFFFu, u0, 1);
+                    u1 += __shfl_xor_sync(0xFFFFFFFFu, u1, 1);
+                    float* to = own + ((2 * t + (c >> 1)) * RT + r) * kW4Pad + g;
+                    if (!(c & 1)) {
+                        to[0] = u0;
+                        to[8] = u1;
+                    }
+                } else
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     own[((8 * t + 2 * c + (e & 1)) * RT + r) * kW4Pad + g + 8 * (e >> 1)] =
                         acc[r][t][e];
         if (tile + 1 < tiles) store_scales(tile + 1);
         team_sync();
-        for (int i = threadIdx.x & (32 * kW4Warps - 1); i < NT * 8 * kRowsTile;
+        for (int i = threadIdx.x & (32 * kW4Warps - 1); i < kTok * kRowsTile;
              i += 32 * kW4Warps) {
             const int m = i / kRowsTile, row = i % kRowsTile;
             const int64_t n = r0 + tile * kRowsTile + row;
             float v = 0.0f;
 #pragma unroll
             for (int w = 0; w < kW4Warps; ++w)
-                v += red[(w * (NT * 8) + m) * (RT * kW4Pad) + (row >> 4) * kW4Pad + (row & 15)];
+                v += red[(w * kTok + m) * (RT * kW4Pad) + (row >> 4) * kW4Pad + (row & 15)];
             if (m < tokens && n < r1) {
                 const int64_t to = (m0 + m) * p.N + n;
                 if (p.out_f32)
@@ -407,45 +578,75 @@ static_assert(kW4Warps * kW4Stages * 2048 + kW4Warps * 8 * 2 * kW4Pad * 4 +
                           2 * 17 * 2 * BITNET_W4_MAX_GROUPS + 16 <= kW4Room,
               "the longest rows' scales fit beside the rings");
 
-template <int NT, int NG, int RT, bool XS>
+template <int NT, int NG, int RT, W4X XM>
 cudaError_t launch_w4_as(const W4Params& p, int teams, uint32_t smem, cudaStream_t stream) {
-    auto kern = linear_w4_kernel<NT, NG, RT, XS>;
+    constexpr int kTok = NT * w4_tokens(XM);
+    auto kern = linear_w4_kernel<NT, NG, RT, XM>;
     static std::atomic<uint64_t> allowed;
     const cudaError_t e = allow_smem(kern, kW4Room, allowed);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (p.N + 15) / 16, ctas = int64_t(tc_num_sms()) * kW4Teams / teams;
     return launch_pdl(kern,
                       dim3(static_cast<unsigned>(tiles < ctas ? tiles : ctas),
-                           static_cast<unsigned>((p.M + 8 * NT - 1) / (8 * NT))),
+                           static_cast<unsigned>((p.M + kTok - 1) / kTok)),
                       32 * kW4Warps * teams, smem, stream, p);
 }
 
-// x goes through shared memory where it fits: for one team on half an SM while a copy of x for
+// x goes through shared memory where it fits (*fits): for one team on half an SM while a copy of x for
 // each is small (one token of 14336 values, 4096 rows: 9.4 against 10.6 µs; 8 tokens of 4096
 // values, 14336 rows: 12.3 against 11.7), for two on all of it otherwise.
-template <int NT, int NG, int RT>
-cudaError_t launch_w4(const W4Params& p, cudaStream_t stream) {
-    const int tokens = static_cast<int>(p.M < 8 * NT ? p.M : 8 * NT);
+template <int NT, int NG, int RT, W4X XM>
+cudaError_t launch_w4(const W4Params& p, bool* fits, cudaStream_t stream) {
+    constexpr int kTok = NT * w4_tokens(XM);
+    const int tokens = static_cast<int>(p.M < kTok ? p.M : kTok);
     constexpr uint32_t kHalf = 113 * 1024, kCopy = 32 * 1024;
-    const uint32_t one = w4_layout(1, NT, NG, RT, p.blocks, tokens, true).bytes;
-    if (one <= kHalf && uint32_t(p.blocks) * 256 * tokens <= kCopy)
-        return launch_w4_as<NT, NG, RT, true>(p, 1, one, stream);
-    const uint32_t two = w4_layout(2, NT, NG, RT, p.blocks, tokens, true).bytes;
-    if (two <= kW4Room) return launch_w4_as<NT, NG, RT, true>(p, 2, two, stream);
-    return launch_w4_as<NT, NG, RT, false>(
-        p, 1, w4_layout(1, NT, NG, RT, p.blocks, tokens, false).bytes, stream);
+    const W4Layout one = w4_layout(1, NT, NG, RT, p.blocks, tokens, XM);
+    const uint32_t two = w4_layout(2, NT, NG, RT, p.blocks, tokens, XM).bytes;
+    *fits = true;
+    if (one.bytes <= kHalf && one.bytes - one.x <= kCopy)
+        return launch_w4_as<NT, NG, RT, XM>(p, 1, one.bytes, stream);
+    if (two <= kW4Room) return launch_w4_as<NT, NG, RT, XM>(p, 2, two, stream);
+    *fits = false;
+    return cudaSuccess;
 }
 
 // The tile shape: 32 tokens a pass for up to 2^25 weights (6912 x 2560, 32 tokens: 11.4 µs against
 // 13.0 in two passes of 16), 16 for more (28672 x 4096: 47 against 58; the second pass finds the
 // weights in L2, and x takes half the reads); for up to eight tokens two row tiles share the reads
 // of x where every team has more than one.
+template <int NT, int NG, int RT>
+cudaError_t launch_w4_bf16(const W4Params& p, cudaStream_t stream) {
+    bool fits;
+    const cudaError_t e = launch_w4<NT, NG, RT, kShared>(p, &fits, stream);
+    if (fits) return e;
+    return launch_w4_as<NT, NG, RT, kGlobal>(
+        p, 1, w4_layout(1, NT, NG, RT, p.blocks, 0, kGlobal).bytes, stream);
+}
+
+// Few tokens go in bytes where the weights are many enough to pay for cutting x up (in bytes and in
+// bf16): one token 2560 x 2560 3.3 and 3.0 µs, 2560 x 6912 4.7 and 4.9, 28672 x 4096 14.0 and 18.2,
+// 131071 x 4096 45 and 63; two tokens 6912 x 2560 5.4 and 5.0, 14336 x 4096 9.2 and 10.8; three
+// tokens, which take two column tiles, 14336 x 4096 11.2 and 10.9, 28672 x 4096 17.4 and 18.9,
+// 131071 x 4096 55 and 64, but with groups of 64, and so more sums to turn into floats, 64 and 61.
+template <int NG, int RT>
+cudaError_t launch_w4_few(const W4Params& p, cudaStream_t stream) {
+    const int64_t weights = p.N * p.K;
+    bool fits = false;
+    cudaError_t e = cudaSuccess;
+    if (p.M <= 2 && weights >= int64_t(1) << (p.M == 1 ? 24 : 25))
+        e = launch_w4<1, NG, RT, kBytes>(p, &fits, stream);
+    else if constexpr (NG == 1)
+        if (p.M > 2 && p.M <= 4 && weights >= int64_t(1) << 26)
+            e = launch_w4<2, NG, RT, kBytes>(p, &fits, stream);
+    return fits ? e : launch_w4_bf16<1, NG, RT>(p, stream);
+}
+
 template <int NG>
 cudaError_t launch_w4_tokens(const W4Params& p, cudaStream_t stream) {
-    if (p.M > 16 && p.N * p.K <= int64_t(1) << 25) return launch_w4<4, NG, 1>(p, stream);
-    if (p.M > 8) return launch_w4<2, NG, 1>(p, stream);
-    if (p.N > 16 * kW4Teams * int64_t(tc_num_sms())) return launch_w4<1, NG, 2>(p, stream);
-    return launch_w4<1, NG, 1>(p, stream);
+    if (p.M > 16 && p.N * p.K <= int64_t(1) << 25) return launch_w4_bf16<4, NG, 1>(p, stream);
+    if (p.M > 8) return launch_w4_bf16<2, NG, 1>(p, stream);
+    if (p.N > 16 * kW4Teams * int64_t(tc_num_sms())) return launch_w4_few<NG, 2>(p, stream);
+    return launch_w4_few<NG, 1>(p, stream);
 }
 
 }  // namespace

@@ -128,3 +128,101 @@ def test_streams_and_graph(bn):
     g.replay()
     torch.cuda.synchronize()
     _check(yg, x2, t, scales, 64)
+
+
+def _large(N, K, group, seed):
+    """Random packed weights, their values and scales, on the GPU."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    blocks = -(-K // 128)
+    packed = torch.randint(0, 256, (N, blocks * 64), generator=g, device="cuda",
+                           dtype=torch.int32).to(torch.uint8)
+    words = packed.view(torch.int32).view(N, blocks, 4, 4)  # c, j
+    t = torch.stack([(words >> (2 * i + 14 if i & 1 else 2 * i) & 15) - 8 for i in range(8)], -1)
+    t = t.permute(0, 1, 3, 2, 4).reshape(N, blocks * 128)[:, :K]
+    if K % 128:  # weights past K have code 8
+        half = words[:, -1, :, 2:]
+        half.fill_(-0x77777778)
+    scales = torch.rand(N, -(-K // group), generator=g, device="cuda") * 0.02 + 0.001
+    return packed, t, scales.to(torch.bfloat16)
+
+
+def _check_large(y, x, t, scales, group):
+    """As _check, and every value of x may be off by 2^-29 of the largest of its block of 128: it is
+    taken in units of 2^-28 times the power of two below that, rounded once. (Sums of hundreds of
+    values at the end of binary32's range are off by a step of 2^-149 each at most.)"""
+    K = t.shape[1]
+    w = t.double() * scales.double().repeat_interleave(group, 1)[:, :K]
+    xd = x.double()
+    want, size = xd @ w.T, xd.abs() @ w.abs().T
+    pad = torch.nn.functional.pad(xd.abs(), (0, -K % 128)).view(x.shape[0], -1, 128)
+    off = (pad.amax(2, keepdim=True) * 2.0 ** -29).expand_as(pad).reshape(x.shape[0], -1)[:, :K]
+    tol = (K + 2) * ref.F32_STEP * size + off @ w.abs().T + 2.0 ** -140
+    if y.dtype == torch.bfloat16:
+        tol = tol + ref.BF16_HALF * (want.abs() + tol)
+    err = (y.double() - want).abs()
+    assert torch.all(err <= tol), f"{(err / tol).max().item():.2f} of the tolerance"
+
+
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,N,K,group", [(1, 2560, 6912, 128), (1, 8001, 2112, 64),
+                                         (1, 601, 28160, 32), (2, 17001, 1984, 128),
+                                         (2, 14336, 2560, 32), (2, 700, 48000, 64),
+                                         (3, 35001, 1984, 128), (4, 28672, 2560, 128),
+                                         (4, 1600, 42048, 128), (4, 28672, 2560, 64)])
+def test_large_layers_at_few_tokens(bn, M, N, K, group, out):
+    packed, t, scales = _large(N, K, group, N)
+    g = torch.Generator(device="cuda").manual_seed(M)
+    x = torch.randn(M, K, generator=g, device="cuda").to(torch.bfloat16)
+    y = bn.bitnet_linear_w4(x, packed, scales, group, out_dtype=out)
+    _check_large(y, x, t, scales, group)
+    assert torch.equal(y, bn.bitnet_linear_w4(x, packed, scales, group, out_dtype=out))
+
+
+@pytest.mark.parametrize("M", [1, 2, 4])
+def test_large_layers_wide_ranges_of_x(bn, M):
+    """Values of one row from 2^-130 to 2^100: outliers in their blocks, blocks of zeros, of the
+    type's largest and smallest values, of one magnitude each, all ones and all signs."""
+    N, K = 28672, 2560
+    packed, t, scales = _large(N, K, 128, 9)
+    g = torch.Generator(device="cuda").manual_seed(M)
+    x = torch.randn(M, K, generator=g, device="cuda")
+    x[:, 3] = 3e4
+    x[:, 128:256] *= 2.0 ** -torch.randint(0, 40, (M, 128), generator=g, device="cuda")
+    x[:, 256:384] = 0.0
+    x[:, 384:512] *= 1e-37
+    x[:, 512:640] = 2.0 ** -130
+    x[:, 640:768] = 1.9921875  # all bits of the mantissa
+    x[:, 768:896] = -1.9921875
+    x[:, 900] = 1.0 / 3
+    x = x.to(torch.bfloat16)
+    for rows in (x, x * 2.0 ** 60, x * 2.0 ** 110, x * 2.0 ** -100):
+        y = bn.bitnet_linear_w4(rows, packed, scales, 128, out_dtype=torch.float32)
+        _check_large(y, rows, t, scales, 128)
+    tiny = torch.full((M, K), 2.0 ** -126, dtype=torch.bfloat16, device="cuda")
+    y = bn.bitnet_linear_w4(tiny, packed, torch.full_like(scales, 1024.0), 128,
+                            out_dtype=torch.float32)
+    _check_large(y, tiny, t, torch.full_like(scales, 1024.0), 128)
+    ends = (packed & 0) + 0x0F  # codes 15 and 0: 7 and -8
+    te = torch.where(((ends.view(torch.int32).view(N, -1, 4, 4)[..., None] >> torch.tensor(
+        [2 * i + 14 if i & 1 else 2 * i for i in range(8)], device="cuda")) & 15) == 15, 7, -8)
+    te = te.permute(0, 1, 3, 2, 4).reshape(N, K)
+    big = torch.full((M, K), 2.0 ** 64 * 1.9921875, dtype=torch.bfloat16, device="cuda")
+    for sign in (1, -1):
+        y = bn.bitnet_linear_w4(big * sign, ends, scales, 128, out_dtype=torch.float32)
+        _check_large(y, big * sign, te, scales, 128)
+
+
+def test_large_layers_nan_stays_in_its_row(bn):
+    N, K = 28672, 2560
+    packed, t, scales = _large(N, K, 128, 10)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for M in (2, 4):
+        x = torch.randn(M, K, generator=g, device="cuda").to(torch.bfloat16)
+        y = bn.bitnet_linear_w4(x, packed, scales, 128)
+        for value in (float("nan"), float("inf")):
+            bad = x.clone()
+            bad[1, 777] = value
+            z = bn.bitnet_linear_w4(bad, packed, scales, 128)
+            assert z[1].isnan().all()
+            keep = [m for m in range(M) if m != 1]
+            assert torch.equal(z[keep], y[keep])
