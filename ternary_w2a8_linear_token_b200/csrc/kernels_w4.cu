@@ -190,8 +190,8 @@ enum W4X { kGlobal, kShared, kBytes };
 __host__ __device__ constexpr int w4_tokens(W4X xm) { return xm == kBytes ? 2 : 8; }  // of a product
 
 // Shared memory of a call: the rings, the teams' reduction buffers, two tiles' scales for each team
-// as (group, row) with one row more, so that neither reads nor writes meet in a bank (those of a
-// last, half block filled up with zeros), and x, zeros behind K, as (block, pair of tokens, quarter,
+// as (group, row) with two rows more, so that neither reads nor writes meet in a bank, rows g and
+// g + 8 of 16 next to each other (those of a last, half block filled up with zeros), and x, zeros behind K, as (block, pair of tokens, quarter,
 // token, 64 bytes), or in bytes as (block, token, half, byte, c of a quarter, quarter, 8 bytes) and
 // the units (block, token): what a lane reads of any lies at fixed distances.
 struct W4Layout {
@@ -202,7 +202,7 @@ __host__ __device__ inline W4Layout w4_layout(int teams, int nt, int ng, int rt,
     W4Layout l;
     l.red = teams * kW4Warps * kW4Stages * rt * 1024;
     l.scales = l.red + teams * kW4Warps * nt * w4_tokens(xm) * rt * kW4Pad * 4;
-    l.x = l.scales + (teams * 2 * (16 * rt + 1) * 2 * blocks * ng + 15) / 16 * 16;
+    l.x = l.scales + (teams * 2 * (16 * rt + 2) * 2 * blocks * ng + 15) / 16 * 16;
     l.units = l.x + (xm == kBytes    ? blocks * 512 * tokens
                      : xm == kShared ? blocks * 512 * ((tokens + 1) / 2)
                                      : 0);
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(32 * kW4Warps * kW4Teams, 1)
     // This warp's blocks of a tile (a team may be without rows).
     const int mine = tiles ? (p.blocks - warp + kW4Warps - 1) / kW4Warps : 0;
     const int64_t row_bytes = int64_t(p.blocks) * 64;
-    constexpr int kPitch = kRowsTile + 1;
+    constexpr int kPitch = kRowsTile + 2;
     const int filled = p.blocks * NG;
     const int pair = 512 * (XM == kBytes ? tokens : (tokens + 1) / 2);  // bytes of a block of x
     const W4Layout lay = w4_layout(cta_teams, NT, NG, RT, p.blocks, tokens, XM);
@@ -293,7 +293,8 @@ __global__ void __launch_bounds__(32 * kW4Warps * kW4Teams, 1)
     auto store_scales = [&](int tile) {
 #pragma unroll
         for (int r = 0; r < 2 * RT; ++r) {
-            uint16_t* to = scales + (tile & 1) * (kPitch * filled) + 8 * r + warp;
+            uint16_t* to =
+                scales + (tile & 1) * (kPitch * filled) + 16 * (r >> 1) + 2 * warp + (r & 1);
 #pragma unroll
             for (int i = 0; i < kHeld; ++i)
                 if (32 * i + lane < filled) to[(32 * i + lane) * kPitch] = held[r][i];
@@ -434,9 +435,9 @@ __global__ void __launch_bounds__(32 * kW4Warps * kW4Teams, 1)
                             w4_mma_s8(part[r][t], a0, a1, a2, a3, b0, b1);
                     }
                     if (j % kWords == kWords - 1) {  // a group ends
-                        const uint16_t* q = sa + 16 * r + j / kWords * kPitch;
-                        const float s0 = __uint_as_float(uint32_t(q[0]) << 16);
-                        const float s1 = __uint_as_float(uint32_t(q[8]) << 16);
+                        const uint32_t q = *reinterpret_cast<const uint32_t*>(
+                            sa + 16 * r + j / kWords * kPitch);
+                        const float s0 = bf16_lo(q), s1 = bf16_hi(q);
                         const float zero = __int_as_float(kW4Zero);
 #pragma unroll
                         for (int t = 0; t < NT; ++t) {
@@ -478,9 +479,9 @@ __global__ void __launch_bounds__(32 * kW4Warps * kW4Teams, 1)
                     w4_mma(part[r][t], a2, b2, a3, b3, xv[t].z, xv[t].w);
                 }
                 if (j % kWords == kWords - 1) {  // a group ends
-                    const uint16_t* q = sa + 16 * r + j / kWords * kPitch;
-                    const float s0 = __uint_as_float(uint32_t(q[0]) << 16);
-                    const float s1 = __uint_as_float(uint32_t(q[8]) << 16);
+                    const uint32_t q = *reinterpret_cast<const uint32_t*>(
+                        sa + 16 * r + j / kWords * kPitch);
+                    const float s0 = bf16_lo(q), s1 = bf16_hi(q);
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
                         acc[r][t][0] += s0 * part[r][t][0];
@@ -497,7 +498,7 @@ __global__ void __launch_bounds__(32 * kW4Warps * kW4Teams, 1)
         if (tile + 1 < tiles) fetch_scales(tile + 1);
         const int below = min(rows - tile * kRowsTile, kRowsTile);  // rows of this tile
         float acc[RT][NT][4] = {};
-        const uint16_t* sa = scales + (tile & 1) * (kPitch * filled) + warp * NG * kPitch + g;
+        const uint16_t* sa = scales + (tile & 1) * (kPitch * filled) + warp * NG * kPitch + 2 * g;
         int xa = 0;  // bytes from the warp's first block of x to this one
         int64_t xv0 = 0;
         int ua = 0;
@@ -573,9 +574,9 @@ __global__ void __launch_bounds__(32 * kW4Warps * kW4Teams, 1)
 
 // Without x the longest rows fit in every tile shape, in a CTA of one team.
 static_assert(kW4Warps * kW4Stages * 2048 + kW4Warps * 8 * 2 * kW4Pad * 4 +
-                      2 * 33 * 2 * BITNET_W4_MAX_GROUPS + 16 <= kW4Room &&
+                      2 * 34 * 2 * BITNET_W4_MAX_GROUPS + 16 <= kW4Room &&
                   kW4Warps * kW4Stages * 1024 + kW4Warps * 32 * kW4Pad * 4 +
-                          2 * 17 * 2 * BITNET_W4_MAX_GROUPS + 16 <= kW4Room,
+                          2 * 18 * 2 * BITNET_W4_MAX_GROUPS + 16 <= kW4Room,
               "the longest rows' scales fit beside the rings");
 
 template <int NT, int NG, int RT, W4X XM>
@@ -614,10 +615,14 @@ cudaError_t launch_w4(const W4Params& p, bool* fits, cudaStream_t stream) {
 // 13.0 in two passes of 16), 16 for more (28672 x 4096: 47 against 58; the second pass finds the
 // weights in L2, and x takes half the reads); for up to eight tokens two row tiles share the reads
 // of x where every team has more than one.
+// Where x does not fit beside two row tiles, one leaves it room (28672 x 4096, groups of 32, 8 tokens:
+// 20.0 µs, and 24.6 with two tiles and x through L1).
 template <int NT, int NG, int RT>
 cudaError_t launch_w4_bf16(const W4Params& p, cudaStream_t stream) {
     bool fits;
-    const cudaError_t e = launch_w4<NT, NG, RT, kShared>(p, &fits, stream);
+    cudaError_t e = launch_w4<NT, NG, RT, kShared>(p, &fits, stream);
+    if constexpr (RT > 1)
+        if (!fits) e = launch_w4<NT, NG, 1, kShared>(p, &fits, stream);
     if (fits) return e;
     return launch_w4_as<NT, NG, RT, kGlobal>(
         p, 1, w4_layout(1, NT, NG, RT, p.blocks, 0, kGlobal).bytes, stream);
