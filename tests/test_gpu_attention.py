@@ -468,3 +468,32 @@ def test_tensors_of_a_call_on_another_stream_live_long_enough(bn):
         torch.cuda.synchronize()
         assert torch.equal(out, want)
         del out
+
+
+def test_captured_with_a_stream_given(bn):
+    """A captured step whose calls name their stream: the capture's own, and one forked off it."""
+    cache = _fill(bn, [40, 700], 2, 64, 16, torch.bfloat16, spare=20)
+    seqs, one = _dev([0, 1]), _dev([1, 1])
+    q, k, v = _q(2, 8, 64), _q(2, 2, 64, 2), _q(2, 2, 64, 3)
+    packed, scales = bn.bitnet_pack_w4(torch.randn(96, 512, device="cuda"))
+    flat = q.view(2, 512)
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    lens = cache.lens.tolist()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        here = torch.cuda.current_stream()
+        copies = bn.bitnet_cache_extend(cache, seqs, one, stream=here)
+        bn.bitnet_cache_copy(cache, copies, stream=here)
+        bn.bitnet_cache_append(cache, 0, k, v, seqs, stream=here)
+        side.wait_stream(here)
+        y = bn.bitnet_linear_w4(flat, packed, scales, 128, stream=side)
+        out, lse = bn.bitnet_paged_attention(q, cache, seqs=seqs, return_lse=True, stream=side)
+        here.wait_stream(side)
+    assert cache.lens.tolist() == lens
+    for _ in range(5):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert cache.errors() == 0 and cache.lens.tolist() == [n + 5 for n in lens]
+    _check(cache, q, out, lse)
+    assert torch.equal(y, bn.bitnet_linear_w4(flat, packed, scales, 128))
