@@ -57,15 +57,14 @@ __global__ void __launch_bounds__(kW4Threads) pack_w4_kernel(const float* __rest
 // the same; tcgen05 has no use for 16-row tiles, and its operands would have to be unpacked into
 // shared or tensor memory first).
 //
-// A CTA is one or two teams of eight warps (one where two CTAs fit on an SM, so that the next
-// call's can start as this one's end; two that share x where it takes more room). Rows are dealt
-// out evenly over the teams, by 16 where each has more, and done in tiles of 16 RT; a team's warps
-// take every eighth block of 128 weights of a tile (512 bytes of a row per step of the team) and
-// add their sums in shared memory, in order. Every warp loads its blocks through a ring of its own
-// (cp.async, no barrier between warps), across tiles, and fills it before the previous kernel of
-// the stream has ended (weights do not depend on it). x and the scales come from shared memory:
-// read by fragments from global memory, the eight rows of an instruction cost the L1 a tag lookup
-// each.
+// A CTA is eight warps where two CTAs fit on an SM, so that the next call's can start as this one's
+// end, or sixteen that share x where it takes more room, in teams of W. Rows are dealt out evenly
+// over the teams, by 16 where each has more, and done in tiles of 16 RT; a team's warps take every
+// W-th block of 128 weights of a tile and add their sums in shared memory, in order. Every warp loads
+// its blocks through a ring of its own (cp.async, no barrier between warps), across tiles, and fills
+// it before the previous kernel of the stream has ended (weights do not depend on it). x and the
+// scales come from shared memory: read by fragments from global memory, the eight rows of an
+// instruction cost the L1 a tag lookup each.
 //
 // In bf16 a word's eight weights cost eleven instructions to unpack, and instructions, not HBM, bound
 // large layers (131071 x 4096 at 68 % of the copy rate). Few tokens therefore go in bytes: x as
@@ -73,8 +72,7 @@ __global__ void __launch_bounds__(kW4Threads) pack_w4_kernel(const float* __rest
 // binary32 sums of the block would), cut into four signed bytes, which take four of a product's
 // columns; eight weights are then three instructions, the sums of a group are exact in 32-bit
 // integers, and one subtraction makes a float of each (96 % there at one token).
-constexpr int kW4Warps = 8;  // of a team
-constexpr int kW4Teams = 2;  // most of a CTA, and of an SM
+constexpr int kW4Most = 16;  // warps of a CTA, and of an SM
 constexpr int kW4Stages = 4;
 constexpr uint32_t kW4Room = 227 * 1024;  // shared memory of a CTA
 constexpr int kW4Pad = 20;  // floats per token in the reduction buffer: no bank conflicts
@@ -191,17 +189,18 @@ __host__ __device__ constexpr int w4_tokens(W4X xm) { return xm == kBytes ? 2 : 
 
 // Shared memory of a call: the rings, the teams' reduction buffers, two tiles' scales for each team
 // as (group, row) with two rows more, so that neither reads nor writes meet in a bank, rows g and
-// g + 8 of 16 next to each other (those of a last, half block filled up with zeros), and x, zeros behind K, as (block, pair of tokens, quarter,
-// token, 64 bytes), or in bytes as (block, token, half, byte, c of a quarter, quarter, 8 bytes) and
-// the units (block, token): what a lane reads of any lies at fixed distances.
+// g + 8 of 16 next to each other (those of a last, half block filled up with zeros), and x, zeros
+// behind K, as (block, pair of tokens, quarter, token, 64 bytes), or in bytes as (block, token, byte,
+// half, c of a quarter, quarter, 8 bytes; of the odd bytes the second half first, against conflicts)
+// and the units (block, token): what a lane reads of any lies at fixed distances.
 struct W4Layout {
     uint32_t red, scales, x, units, bytes;  // offsets; the rings come first
 };
-__host__ __device__ inline W4Layout w4_layout(int teams, int nt, int ng, int rt, int blocks,
-                                              int tokens, W4X xm) {
+__host__ __device__ inline W4Layout w4_layout(int warps, int teams, int nt, int ng, int rt,
+                                              int blocks, int tokens, W4X xm) {
     W4Layout l;
-    l.red = teams * kW4Warps * kW4Stages * rt * 1024;
-    l.scales = l.red + teams * kW4Warps * nt * w4_tokens(xm) * rt * kW4Pad * 4;
+    l.red = teams * warps * kW4Stages * rt * 1024;
+    l.scales = l.red + teams * warps * nt * w4_tokens(xm) * rt * kW4Pad * 4;
     l.x = l.scales + (teams * 2 * (16 * rt + 2) * 2 * blocks * ng + 15) / 16 * 16;
     l.units = l.x + (xm == kBytes    ? blocks * 512 * tokens
                      : xm == kShared ? blocks * 512 * ((tokens + 1) / 2)
@@ -211,20 +210,21 @@ __host__ __device__ inline W4Layout w4_layout(int teams, int nt, int ng, int rt,
 }
 
 // NT: column tiles, of 8 tokens or of 2 in bytes; NG: groups per block (1, 2 or 4); RT: tiles of 16
-// rows that share a load of x; XM: where x comes from.
-template <int NT, int NG, int RT, W4X XM>
-__global__ void __launch_bounds__(32 * kW4Warps * kW4Teams, 1)
+// rows that share a load of x; XM: where x comes from; W: warps of a team.
+template <int NT, int NG, int RT, W4X XM, int W>
+__global__ void __launch_bounds__(32 * kW4Most, 1)
     linear_w4_kernel(const __grid_constant__ W4Params p) {
     constexpr int S = kW4Stages;
     constexpr int kRowsTile = 16 * RT;
     constexpr int kStage = RT * 1024;      // bytes of a block of a tile
-    constexpr int kStep = kW4Warps * 64;   // bytes from one block of a warp to its next
-    constexpr int kHeld = 4;               // scales per lane and row that are prefetched
+    constexpr int kStep = W * 64;   // bytes from one block of a warp to its next
+    constexpr int kMine = kRowsTile / W;   // rows whose scales a warp brings
+    constexpr int kHeld = kMine < 4 ? 4 : 16 / kMine;  // per lane and row, prefetched
     constexpr int kTok = NT * w4_tokens(XM);
     extern __shared__ __align__(128) uint8_t w4_dyn[];
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const int team = threadIdx.x >> 8, warp = threadIdx.x >> 5 & (kW4Warps - 1);
-    const int cta_teams = blockDim.x / (32 * kW4Warps);
+    const int team = threadIdx.x / (32 * W), warp = threadIdx.x >> 5 & (W - 1);
+    const int cta_teams = blockDim.x / (32 * W);
     const int64_t teams = int64_t(gridDim.x) * cta_teams;
     const int64_t me = int64_t(blockIdx.x) * cta_teams + team;
     // Where a team has more than 16 rows, they begin at a multiple of 16 (a tile that is begun
@@ -235,17 +235,17 @@ __global__ void __launch_bounds__(32 * kW4Warps * kW4Teams, 1)
     const int tokens = static_cast<int>(p.M - m0 < kTok ? p.M - m0 : kTok);
     const int rows = static_cast<int>(r1 - r0), tiles = (rows + kRowsTile - 1) / kRowsTile;
     // This warp's blocks of a tile (a team may be without rows).
-    const int mine = tiles ? (p.blocks - warp + kW4Warps - 1) / kW4Warps : 0;
+    const int mine = tiles ? (p.blocks - warp + W - 1) / W : 0;
     const int64_t row_bytes = int64_t(p.blocks) * 64;
     constexpr int kPitch = kRowsTile + 2;
     const int filled = p.blocks * NG;
     const int pair = 512 * (XM == kBytes ? tokens : (tokens + 1) / 2);  // bytes of a block of x
-    const W4Layout lay = w4_layout(cta_teams, NT, NG, RT, p.blocks, tokens, XM);
+    const W4Layout lay = w4_layout(W, cta_teams, NT, NG, RT, p.blocks, tokens, XM);
     float* const red = reinterpret_cast<float*>(w4_dyn + lay.red) +
-                       team * (kW4Warps * kTok * RT * kW4Pad);
+                       team * (W * kTok * RT * kW4Pad);
     uint16_t* const scales = reinterpret_cast<uint16_t*>(w4_dyn + lay.scales) +
                              team * (2 * kPitch * filled);
-    const uint8_t* const ring = w4_dyn + (team * kW4Warps + warp) * (S * kStage);
+    const uint8_t* const ring = w4_dyn + (team * W + warp) * (S * kStage);
     const uint32_t ring_at = smem_addr(ring);
 
     // The blocks to load: tile, how many of it are left, and where this lane's 16 bytes of rows g,
@@ -276,15 +276,15 @@ __global__ void __launch_bounds__(32 * kW4Warps * kW4Teams, 1)
             if (left > 0) aim();
         }
     };
-    // Scales of a tile: a warp brings rows warp, warp + 8, ..., in registers until the tile before
+    // Scales of a tile: a warp brings rows warp, warp + W, ..., in registers until the tile before
     // it is done.
-    uint16_t held[2 * RT][kHeld];
+    uint16_t held[kMine][kHeld];
     auto scale_row = [&](int tile, int r) {
-        return p.scales + (r0 + min(tile * kRowsTile + 8 * r + warp, rows - 1)) * p.groups;
+        return p.scales + (r0 + min(tile * kRowsTile + W * r + warp, rows - 1)) * p.groups;
     };
     auto fetch_scales = [&](int tile) {
 #pragma unroll
-        for (int r = 0; r < 2 * RT; ++r)
+        for (int r = 0; r < kMine; ++r)
 #pragma unroll
             for (int i = 0; i < kHeld; ++i)
                 held[r][i] =
@@ -292,9 +292,10 @@ __global__ void __launch_bounds__(32 * kW4Warps * kW4Teams, 1)
     };
     auto store_scales = [&](int tile) {
 #pragma unroll
-        for (int r = 0; r < 2 * RT; ++r) {
-            uint16_t* to =
-                scales + (tile & 1) * (kPitch * filled) + 16 * (r >> 1) + 2 * warp + (r & 1);
+        for (int r = 0; r < kMine; ++r) {
+            const int row = W * r + warp;
+            uint16_t* to = scales + (tile & 1) * (kPitch * filled) + (row & 16) + 2 * (row & 7) +
+                           (row >> 3 & 1);
 #pragma unroll
             for (int i = 0; i < kHeld; ++i)
                 if (32 * i + lane < filled) to[(32 * i + lane) * kPitch] = held[r][i];
@@ -303,7 +304,7 @@ __global__ void __launch_bounds__(32 * kW4Warps * kW4Teams, 1)
         }
     };
     auto team_sync = [&]() {
-        asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(32 * kW4Warps) : "memory");
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(32 * W) : "memory");
     };
 
     pdl_trigger();
@@ -396,7 +397,7 @@ __global__ void __launch_bounds__(32 * kW4Warps * kW4Teams, 1)
     }
     const int x_half = g & 1 ? -64 : 64;
     // In global memory the last block's empty half is not read; it falls to one warp.
-    const bool cut = XM == kGlobal && p.K % 128 != 0 && (p.blocks - 1) % kW4Warps == warp;
+    const bool cut = XM == kGlobal && p.K % 128 != 0 && (p.blocks - 1) % W == warp;
 
     // One block of 128 weights by the tile's first R row tiles (the others have no rows).
     auto block = [&](auto R, const uint8_t* at, const uint16_t* sa, int xa, int64_t xv0, bool half,
@@ -518,10 +519,10 @@ __global__ void __launch_bounds__(32 * kW4Warps * kW4Teams, 1)
                     __syncwarp();  // all lanes have read the stage
                 }
                 load(i);
-                sa += kW4Warps * NG * kPitch;
-                xa += kW4Warps * pair;
-                xv0 += kW4Warps * 128;
-                ua += kW4Warps * tokens;
+                sa += W * NG * kPitch;
+                xa += W * pair;
+                xv0 += W * 128;
+                ua += W * tokens;
             }
             advance();
         }
@@ -551,13 +552,13 @@ __global__ void __launch_bounds__(32 * kW4Warps * kW4Teams, 1)
                         acc[r][t][e];
         if (tile + 1 < tiles) store_scales(tile + 1);
         team_sync();
-        for (int i = threadIdx.x & (32 * kW4Warps - 1); i < kTok * kRowsTile;
-             i += 32 * kW4Warps) {
+        for (int i = threadIdx.x & (32 * W - 1); i < kTok * kRowsTile;
+             i += 32 * W) {
             const int m = i / kRowsTile, row = i % kRowsTile;
             const int64_t n = r0 + tile * kRowsTile + row;
             float v = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kW4Warps; ++w)
+            for (int w = 0; w < W; ++w)
                 v += red[(w * kTok + m) * (RT * kW4Pad) + (row >> 4) * kW4Pad + (row & 15)];
             if (m < tokens && n < r1) {
                 const int64_t to = (m0 + m) * p.N + n;
@@ -573,85 +574,95 @@ __global__ void __launch_bounds__(32 * kW4Warps * kW4Teams, 1)
 }
 
 // Without x the longest rows fit in every tile shape, in a CTA of one team.
-static_assert(kW4Warps * kW4Stages * 2048 + kW4Warps * 8 * 2 * kW4Pad * 4 +
+static_assert(8 * kW4Stages * 2048 + 8 * 8 * 2 * kW4Pad * 4 +
                       2 * 34 * 2 * BITNET_W4_MAX_GROUPS + 16 <= kW4Room &&
-                  kW4Warps * kW4Stages * 1024 + kW4Warps * 32 * kW4Pad * 4 +
+                  8 * kW4Stages * 1024 + 8 * 32 * kW4Pad * 4 +
                           2 * 18 * 2 * BITNET_W4_MAX_GROUPS + 16 <= kW4Room,
               "the longest rows' scales fit beside the rings");
 
-template <int NT, int NG, int RT, W4X XM>
+template <int NT, int NG, int RT, W4X XM, int W>
 cudaError_t launch_w4_as(const W4Params& p, int teams, uint32_t smem, cudaStream_t stream) {
     constexpr int kTok = NT * w4_tokens(XM);
-    auto kern = linear_w4_kernel<NT, NG, RT, XM>;
+    auto kern = linear_w4_kernel<NT, NG, RT, XM, W>;
     static std::atomic<uint64_t> allowed;
     const cudaError_t e = allow_smem(kern, kW4Room, allowed);
     if (e != cudaSuccess) return e;
-    const int64_t tiles = (p.N + 15) / 16, ctas = int64_t(tc_num_sms()) * kW4Teams / teams;
+    const int64_t tiles = (p.N + 15) / 16, ctas = int64_t(tc_num_sms()) * (kW4Most / W) / teams;
     return launch_pdl(kern,
                       dim3(static_cast<unsigned>(tiles < ctas ? tiles : ctas),
                            static_cast<unsigned>((p.M + kTok - 1) / kTok)),
-                      32 * kW4Warps * teams, smem, stream, p);
+                      32 * W * teams, smem, stream, p);
 }
 
-// x goes through shared memory where it fits (*fits): for one team on half an SM while a copy of x for
-// each is small (one token of 14336 values, 4096 rows: 9.4 against 10.6 µs; 8 tokens of 4096
-// values, 14336 rows: 12.3 against 11.7), for two on all of it otherwise.
-template <int NT, int NG, int RT, W4X XM>
+// x goes through shared memory where it fits (*fits): for eight warps on half an SM while a copy of
+// x for each half is small (one token of 14336 values, 4096 rows: 9.4 against 10.6 µs; 8 tokens of
+// 4096 values, 14336 rows: 12.3 against 11.7), for sixteen on all of it otherwise.
+template <int NT, int NG, int RT, W4X XM, int W>
 cudaError_t launch_w4(const W4Params& p, bool* fits, cudaStream_t stream) {
-    constexpr int kTok = NT * w4_tokens(XM);
+    constexpr int kTok = NT * w4_tokens(XM), kTeams = kW4Most / W;
     const int tokens = static_cast<int>(p.M < kTok ? p.M : kTok);
     constexpr uint32_t kHalf = 113 * 1024, kCopy = 32 * 1024;
-    const W4Layout one = w4_layout(1, NT, NG, RT, p.blocks, tokens, XM);
-    const uint32_t two = w4_layout(2, NT, NG, RT, p.blocks, tokens, XM).bytes;
+    const W4Layout half = w4_layout(W, kTeams / 2, NT, NG, RT, p.blocks, tokens, XM);
+    const W4Layout whole = w4_layout(W, kTeams, NT, NG, RT, p.blocks, tokens, XM);
     *fits = true;
-    if (one.bytes <= kHalf && one.bytes - one.x <= kCopy)
-        return launch_w4_as<NT, NG, RT, XM>(p, 1, one.bytes, stream);
-    if (two <= kW4Room) return launch_w4_as<NT, NG, RT, XM>(p, 2, two, stream);
+    if (half.bytes <= kHalf && half.bytes - half.x <= kCopy)
+        return launch_w4_as<NT, NG, RT, XM, W>(p, kTeams / 2, half.bytes, stream);
+    if (whole.bytes <= kW4Room)
+        return launch_w4_as<NT, NG, RT, XM, W>(p, kTeams, whole.bytes, stream);
     *fits = false;
     return cudaSuccess;
+}
+
+// Where x does not fit beside two row tiles, one leaves it room (28672 x 4096, groups of 32, 8 tokens:
+// 20.0 µs, and 24.6 with two tiles and x through L1).
+template <int NT, int NG, int RT, int W>
+cudaError_t launch_w4_bf16(const W4Params& p, cudaStream_t stream) {
+    bool fits;
+    cudaError_t e = launch_w4<NT, NG, RT, kShared, W>(p, &fits, stream);
+    if constexpr (RT > 1)
+        if (!fits) e = launch_w4<NT, NG, 1, kShared, W>(p, &fits, stream);
+    if (fits) return e;
+    return launch_w4_as<NT, NG, RT, kGlobal, 8>(
+        p, 1, w4_layout(8, 1, NT, NG, RT, p.blocks, 0, kGlobal).bytes, stream);
+}
+
+// Few tokens go in bytes where the weights are many enough to pay for cutting x up (in bytes and in
+// bf16, teams of eight): one token 2560 x 2560 3.3 and 3.0 µs, 2560 x 6912 4.7 and 4.9, 28672 x 4096
+// 14.0 and 18.2, 131071 x 4096 45 and 63; two tokens 6912 x 2560 5.4 and 5.0, 14336 x 4096 9.2 and
+// 10.8; three tokens, which take two column tiles, 14336 x 4096 11.2 and 10.9, 28672 x 4096 17.4 and
+// 18.9, 131071 x 4096 55 and 64, but with groups of 64, and so more sums to turn into floats, 64 and
+// 61.
+template <int NG, int RT, int W>
+cudaError_t launch_w4_few(const W4Params& p, cudaStream_t stream) {
+    const int64_t weights = p.N * p.K;
+    bool fits = false;
+    cudaError_t e = cudaSuccess;
+    if (p.M <= 2 && weights >= int64_t(1) << (p.M == 1 ? 24 : 25)) {
+        e = launch_w4<1, NG, RT, kBytes, W>(p, &fits, stream);
+        if (W < 8 && !fits) e = launch_w4<1, NG, RT, kBytes, 8>(p, &fits, stream);
+    } else if constexpr (NG == 1) {
+        if (p.M > 2 && p.M <= 4 && weights >= int64_t(1) << 26)
+            e = launch_w4<2, NG, RT, kBytes, W>(p, &fits, stream);
+    }
+    return fits ? e : launch_w4_bf16<1, NG, RT, W>(p, stream);
 }
 
 // The tile shape: 32 tokens a pass for up to 2^25 weights (6912 x 2560, 32 tokens: 11.4 µs against
 // 13.0 in two passes of 16), 16 for more (28672 x 4096: 47 against 58; the second pass finds the
 // weights in L2, and x takes half the reads); for up to eight tokens two row tiles share the reads
-// of x where every team has more than one.
-// Where x does not fit beside two row tiles, one leaves it room (28672 x 4096, groups of 32, 8 tokens:
-// 20.0 µs, and 24.6 with two tiles and x through L1).
-template <int NT, int NG, int RT>
-cudaError_t launch_w4_bf16(const W4Params& p, cudaStream_t stream) {
-    bool fits;
-    cudaError_t e = launch_w4<NT, NG, RT, kShared>(p, &fits, stream);
-    if constexpr (RT > 1)
-        if (!fits) e = launch_w4<NT, NG, 1, kShared>(p, &fits, stream);
-    if (fits) return e;
-    return launch_w4_as<NT, NG, RT, kGlobal>(
-        p, 1, w4_layout(1, NT, NG, RT, p.blocks, 0, kGlobal).bytes, stream);
-}
-
-// Few tokens go in bytes where the weights are many enough to pay for cutting x up (in bytes and in
-// bf16): one token 2560 x 2560 3.3 and 3.0 µs, 2560 x 6912 4.7 and 4.9, 28672 x 4096 14.0 and 18.2,
-// 131071 x 4096 45 and 63; two tokens 6912 x 2560 5.4 and 5.0, 14336 x 4096 9.2 and 10.8; three
-// tokens, which take two column tiles, 14336 x 4096 11.2 and 10.9, 28672 x 4096 17.4 and 18.9,
-// 131071 x 4096 55 and 64, but with groups of 64, and so more sums to turn into floats, 64 and 61.
-template <int NG, int RT>
-cudaError_t launch_w4_few(const W4Params& p, cudaStream_t stream) {
-    const int64_t weights = p.N * p.K;
-    bool fits = false;
-    cudaError_t e = cudaSuccess;
-    if (p.M <= 2 && weights >= int64_t(1) << (p.M == 1 ? 24 : 25))
-        e = launch_w4<1, NG, RT, kBytes>(p, &fits, stream);
-    else if constexpr (NG == 1)
-        if (p.M > 2 && p.M <= 4 && weights >= int64_t(1) << 26)
-            e = launch_w4<2, NG, RT, kBytes>(p, &fits, stream);
-    return fits ? e : launch_w4_bf16<1, NG, RT>(p, stream);
-}
-
+// of x where every team has more than one. Teams of four warps where each has more than one tile
+// and a tile's scales fit in registers: what a tile costs beside its blocks (scales, sums, barriers)
+// then weighs half (teams of four and of eight: 10000 x 1024 4.1 and 4.7 µs, 131071 x 512 13.5 and
+// 18.7, 14336 x 4096 at 8 tokens 10.5 and 11.7, 131071 x 4096 at 8 58 and 62; with too few rows
+// 6912 x 2560 5.0 and 4.3).
 template <int NG>
 cudaError_t launch_w4_tokens(const W4Params& p, cudaStream_t stream) {
-    if (p.M > 16 && p.N * p.K <= int64_t(1) << 25) return launch_w4_bf16<4, NG, 1>(p, stream);
-    if (p.M > 8) return launch_w4_bf16<2, NG, 1>(p, stream);
-    if (p.N > 16 * kW4Teams * int64_t(tc_num_sms())) return launch_w4_few<NG, 2>(p, stream);
-    return launch_w4_few<NG, 1>(p, stream);
+    if (p.M > 16 && p.N * p.K <= int64_t(1) << 25) return launch_w4_bf16<4, NG, 1, 8>(p, stream);
+    if (p.M > 8) return launch_w4_bf16<2, NG, 1, 8>(p, stream);
+    if (p.groups <= 64 && p.N > 64 * int64_t(tc_num_sms()))
+        return launch_w4_few<NG, 2, 4>(p, stream);
+    if (p.N > 32 * int64_t(tc_num_sms())) return launch_w4_few<NG, 2, 8>(p, stream);
+    return launch_w4_few<NG, 1, 8>(p, stream);
 }
 
 }  // namespace

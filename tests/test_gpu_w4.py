@@ -168,7 +168,11 @@ def _check_large(y, x, t, scales, group):
                                          (1, 601, 28160, 32), (2, 17001, 1984, 128),
                                          (2, 14336, 2560, 32), (2, 700, 48000, 64),
                                          (3, 35001, 1984, 128), (4, 28672, 2560, 128),
-                                         (4, 1600, 42048, 128), (4, 28672, 2560, 64)])
+                                         (4, 1600, 42048, 128), (4, 28672, 2560, 64),
+                                         (1, 9601, 192, 32), (5, 10007, 2048, 32),
+                                         (8, 9999, 4160, 128), (2, 9473, 8192, 128),
+                                         (7, 9500, 8192, 128), (1, 40000, 64, 64),
+                                         (8, 14336, 4096, 64), (3, 10240, 4096, 32)])
 def test_large_layers_at_few_tokens(bn, M, N, K, group, out):
     packed, t, scales = _large(N, K, group, N)
     g = torch.Generator(device="cuda").manual_seed(M)
