@@ -653,14 +653,16 @@ cudaError_t launch_w4_few(const W4Params& p, cudaStream_t stream) {
 // of x where every team has more than one. Teams of four warps where each has more than one tile
 // and a tile's scales fit in registers: what a tile costs beside its blocks (scales, sums, barriers)
 // then weighs half (teams of four and of eight: 10000 x 1024 4.1 and 4.7 µs, 131071 x 512 13.5 and
-// 18.7, 14336 x 4096 at 8 tokens 10.5 and 11.7, 131071 x 4096 at 8 58 and 62; with too few rows
-// 6912 x 2560 5.0 and 4.3).
+// 18.7, 14336 x 4096 at 8 tokens 10.5 and 11.7, at 16 13.2 and 14.3, 131071 x 4096 at 8 58 and 62;
+// with too few rows 6912 x 2560 5.0 and 4.3).
 template <int NG>
 cudaError_t launch_w4_tokens(const W4Params& p, cudaStream_t stream) {
     if (p.M > 16 && p.N * p.K <= int64_t(1) << 25) return launch_w4_bf16<4, NG, 1, 8>(p, stream);
-    if (p.M > 8) return launch_w4_bf16<2, NG, 1, 8>(p, stream);
-    if (p.groups <= 64 && p.N > 64 * int64_t(tc_num_sms()))
-        return launch_w4_few<NG, 2, 4>(p, stream);
+    const bool four = p.groups <= 64 && p.N > 64 * int64_t(tc_num_sms());
+    if (p.M > 8)
+        return four ? launch_w4_bf16<2, NG, 1, 4>(p, stream)
+                    : launch_w4_bf16<2, NG, 1, 8>(p, stream);
+    if (four) return launch_w4_few<NG, 2, 4>(p, stream);
     if (p.N > 32 * int64_t(tc_num_sms())) return launch_w4_few<NG, 2, 8>(p, stream);
     return launch_w4_few<NG, 1, 8>(p, stream);
 }

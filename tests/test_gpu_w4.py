@@ -172,7 +172,8 @@ def _check_large(y, x, t, scales, group):
                                          (1, 9601, 192, 32), (5, 10007, 2048, 32),
                                          (8, 9999, 4160, 128), (2, 9473, 8192, 128),
                                          (7, 9500, 8192, 128), (1, 40000, 64, 64),
-                                         (8, 14336, 4096, 64), (3, 10240, 4096, 32)])
+                                         (8, 14336, 4096, 64), (3, 10240, 4096, 32),
+                                         (9, 9601, 2112, 64), (33, 9480, 1088, 32)])
 def test_large_layers_at_few_tokens(bn, M, N, K, group, out):
     packed, t, scales = _large(N, K, group, N)
     g = torch.Generator(device="cuda").manual_seed(M)
