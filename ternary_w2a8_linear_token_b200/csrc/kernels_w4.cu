@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(32 * kW4Most, 1)
     constexpr int S = kW4Stages;
     constexpr int kRowsTile = 16 * RT;
     constexpr int kStage = RT * 1024;      // bytes of a block of a tile
-    constexpr int kStep = W * 64;   // bytes from one block of a warp to its next
+    constexpr int kStep = W * 64;          // bytes from one block of a warp to its next
     constexpr int kMine = kRowsTile / W;   // rows whose scales a warp brings
     constexpr int kHeld = kMine < 4 ? 4 : 16 / kMine;  // per lane and row, prefetched
     constexpr int kTok = NT * w4_tokens(XM);
