@@ -532,8 +532,8 @@ bitnet_status bitnet_cache_append(const bitnet_cache* cache, const bitnet_cache_
  *   workspace: bitnet_paged_attention_workspace_size(cache, B, heads) bytes, 256-byte aligned;
  *   contents on entry are ignored; not to be shared by calls that may overlap. The size does not
  *   depend on the lengths.
- * Scores, the softmax's maximum and sum, and the weighted sum are held in binary32; weights enter
- * the second product as two bf16 terms (relative error 2^-16), out is rounded once. The work is
+ * Scores, the softmax's weights, maximum and sum, and the weighted sum are held in binary32 (weights
+ * enter the second product as three bf16 terms, all of their bits), out is rounded once. The work is
  * cut over (sequence, key/value head, tokens) by the lengths that the kernel finds on the device,
  * and joined in a fixed order: the same inputs give the same bits on the same GPU model. Tokens
  * of a page outside the pool count as not visible (BITNET_CACHE_ERR_PAGE); a length outside the

@@ -9,8 +9,12 @@
 // Bound by HBM: every K and V byte is read once, for 2 to 32 multiply-adds. The products still run
 // on the tensor cores (mma.sync m16n8k16, eight heads of a group as its columns), which leaves the
 // issue slots to the loads; tcgen05 would need 64 rows and more to pay. p enters the second
-// product as two bf16 terms (value and remainder), so its error of 2^-16 vanishes beside the
-// output's rounding of 2^-8; one term would add as much again as that rounding.
+// product as three bf16 terms, which hold all of its 24 bits, and a tile's products are summed from
+// zero and added to o by rounded additions, since the tensor cores cut their sums off. Of 32768
+// outputs (8 sequences of up to 65536 tokens, 8 bits) 8 then lie on the wrong side of a bf16 step,
+// 22 in a plain binary32 form; with two terms and o as the products' accumulator it was 88, for 10 %
+// less time in 8 bits (115 and 127 µs there) and 1 % in bf16 (137.0 and 138.5 µs, 48 sequences of up
+// to 8192).
 //
 // Split. The tokens of all (sequence, key/value head, block of 16 heads) items are cut into units
 // of 64 or 128, and every CTA takes an equal, contiguous share of all units, so that one long
@@ -38,6 +42,7 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kRows = 16;         // heads per item
 constexpr int kMinUnits = 2;      // fewest units that are worth a CTA of their own
 constexpr int kJoinThreads = 128;
+constexpr int kTerms = 3;     // bf16 terms of a weight: 24 bits, all that binary32 has
 constexpr float kLag = 8.0f;  // powers of two that weights may exceed 1 by
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -246,11 +251,12 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return r;
 }
 
-// a, b -> their bf16 pair (a low), and the pair of what the rounding lost.
-__device__ __forceinline__ uint32_t split_bf16(float a, float b, uint32_t& rest) {
+// a, b -> their bf16 pair (a low), and what the rounding lost, exactly.
+__device__ __forceinline__ uint32_t split_bf16(float& a, float& b) {
     uint32_t hi;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(b), "f"(a));
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(rest) : "f"(b - bf16_hi(hi)), "f"(a - bf16_lo(hi)));
+    a -= bf16_lo(hi);
+    b -= bf16_hi(hi);
     return hi;
 }
 
@@ -636,53 +642,56 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8, NH>::kCtas)
                             l[h][e] += w[h][t][x];
                         }
                 }
+            // Weights with tokens along the lanes' pairs, as the second product takes them.
+            uint32_t term[MT][NH][kTerms][2];
 #pragma unroll
-            for (int t = 0; t < MT; ++t) {  // 16 tokens at a time
-                // Weights with tokens along the lanes' pairs, as the second product takes them.
-                uint32_t hi[NH][2], lo[NH][2];
+            for (int t = 0; t < MT; ++t)
 #pragma unroll
                 for (int h = 0; h < NH; ++h)
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        uint32_t rest;
-                        hi[h][half] = transpose8(
-                            split_bf16(I8 ? w[h][t][2 * half] * vs[t][half] : w[h][t][2 * half],
-                                       I8 ? w[h][t][2 * half + 1] * vs[t][half]
-                                          : w[h][t][2 * half + 1],
-                                       rest));
-                        lo[h][half] = transpose8(rest);
-                    }
-                if (I8) {
-#pragma unroll
-                    for (int i = 0; i < D / 16; i += 2) {
-                        uint32_t r[4];
-                        ldmatrix4_trans(r, vt + tile_at<RB>(16 * t + lrow, i + lch));
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const uint32_t a[4] = {
-                                bytes_to_bf16(r[2 * k], false), bytes_to_bf16(r[2 * k], true),
-                                bytes_to_bf16(r[2 * k + 1], false),
-                                bytes_to_bf16(r[2 * k + 1], true)};
-#pragma unroll
-                            for (int h = 0; h < NH; ++h) {
-                                mma_bf16(o[h][i + k], a, hi[h][0], hi[h][1]);
-                                mma_bf16(o[h][i + k], a, lo[h][0], lo[h][1]);
-                            }
+                        float a = w[h][t][2 * half], b = w[h][t][2 * half + 1];
+                        if (I8) {
+                            a *= vs[t][half];
+                            b *= vs[t][half];
                         }
-                    }
-                } else {
 #pragma unroll
-                    for (int i = 0; i < D / 16; ++i) {
-                        uint32_t a[4];
-                        ldmatrix4_trans(a, vt + tile_at<RB>(16 * t + (lane & 7) + (lane >> 4 << 3),
+                        for (int e = 0; e < kTerms; ++e)
+                            term[t][h][e][half] = transpose8(split_bf16(a, b));
+                    }
+#pragma unroll
+            for (int i = 0; i < D / 16; i += I8 ? 2 : 1) {
+                float d[I8 ? 2 : 1][NH][4] = {};
+#pragma unroll
+                for (int t = 0; t < MT; ++t) {
+                    uint32_t r[4];
+                    if (I8)
+                        ldmatrix4_trans(r, vt + tile_at<RB>(16 * t + lrow, i + lch));
+                    else
+                        ldmatrix4_trans(r, vt + tile_at<RB>(16 * t + (lane & 7) + (lane >> 4 << 3),
                                                             2 * i + (lane >> 3 & 1)));
 #pragma unroll
-                        for (int h = 0; h < NH; ++h) {
-                            mma_bf16(o[h][i], a, hi[h][0], hi[h][1]);
-                            mma_bf16(o[h][i], a, lo[h][0], lo[h][1]);
+                    for (int k = 0; k < (I8 ? 2 : 1); ++k) {
+                        uint32_t a[4] = {r[0], r[1], r[2], r[3]};
+                        if (I8) {
+                            a[0] = bytes_to_bf16(r[2 * k], false);
+                            a[1] = bytes_to_bf16(r[2 * k], true);
+                            a[2] = bytes_to_bf16(r[2 * k + 1], false);
+                            a[3] = bytes_to_bf16(r[2 * k + 1], true);
                         }
+#pragma unroll
+                        for (int h = 0; h < NH; ++h)
+#pragma unroll
+                            for (int e = kTerms - 1; e >= 0; --e)
+                                mma_bf16(d[k][h], a, term[t][h][e][0], term[t][h][e][1]);
                     }
                 }
+#pragma unroll
+                for (int k = 0; k < (I8 ? 2 : 1); ++k)
+#pragma unroll
+                    for (int h = 0; h < NH; ++h)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) o[h][i + k][x] += d[k][h][x];
             }
         }
         stage = stage + 1 == S ? 0 : stage + 1;

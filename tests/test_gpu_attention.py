@@ -497,3 +497,43 @@ def test_captured_with_a_stream_given(bn):
     assert cache.errors() == 0 and cache.lens.tolist() == [n + 5 for n in lens]
     _check(cache, q, out, lse)
     assert torch.equal(y, bn.bitnet_linear_w4(flat, packed, scales, 128))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.int8])
+def test_weights_keep_all_their_bits(bn, dtype):
+    """Weights 1, 1 and w of three tokens whose values cancel all but w's last bits: v = -p1, -p2 and
+    1, where p1 + p2 are the first 14 bits of w (8-bit codes times powers of two, exact in either
+    type), so out = (w - p1 - p2) / (2 + w), about 2^-16. Against the formula in 64 bits: the score
+    and its exponential are off by (4 |z| + 6) binary32 steps of w, as decode_ref derives them, the
+    six terms and two joins of the sum by eight steps of its largest part; then one rounding."""
+    B, kv, D = 64, 8, 64
+    cache = _fill(bn, [3] * B, kv, D, 16, dtype)
+    layer = cache.layers[0]
+    g = np.random.default_rng(12)
+    z = -ref.bf16(g.uniform(0.02, 0.68, (B, kv))).double().numpy()
+    w = np.exp(z)
+    p1 = np.floor(w * 128) / 128
+    p2 = np.floor((w - p1) * 2.0 ** 14) / 2.0 ** 14
+    k, v = np.zeros((B, kv, 3, D)), np.zeros((B, kv, 3, D))
+    k[:, :, 2, 0] = 1.0
+    v[:, :, 0], v[:, :, 1], v[:, :, 2] = -p1[..., None], -p2[..., None], 1.0
+    for pool, x in zip(range(2), (k, v)):
+        page = cache.table[:, 0].long()
+        x = torch.from_numpy(x).cuda()
+        if dtype == torch.int8:
+            scale = torch.tensor([2.0 ** 7, 2.0 ** 14, 1.0] if pool else [1.0] * 3, device="cuda",
+                                 dtype=torch.float64)
+            layer[pool][page, :, :3] = (x * scale[:, None]).to(torch.int8)
+            layer[2 + pool][page, :, :3] = scale.float().expand(B, kv, 3)
+        else:
+            layer[pool][page, :, :3] = x.to(torch.bfloat16)
+            assert torch.equal(layer[pool][page, :, :3].double(), x)
+    q = torch.zeros(B, kv, D, dtype=torch.bfloat16, device="cuda")
+    q[:, :, 0] = torch.from_numpy(z).cuda()
+    out = bn.bitnet_paged_attention(q, cache, scale=1.0).double().cpu().numpy()
+    want = ((w - p1 - p2) / (2 + w))[..., None]
+    tol = (((4 * np.abs(z) + 6) * w + 8) * ref.F32_STEP / (2 + w))[..., None]
+    tol = tol + ref.BF16_HALF * (np.abs(want) + tol)
+    err = np.abs(out - want)
+    assert np.all(err <= tol), f"{np.max(err / tol):.2f} of the tolerance"
+    assert np.median(np.abs(want) / tol) > 4  # (what cancels is large beside it)
