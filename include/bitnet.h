@@ -539,7 +539,8 @@ bitnet_status bitnet_cache_append(const bitnet_cache* cache, const bitnet_cache_
  * of a page outside the pool count as not visible (BITNET_CACHE_ERR_PAGE); a length outside the
  * table is cut at its end (BITNET_CACHE_ERR_LEN). Inf or NaN in a hidden token has no effect; in a
  * visible one or in q it gives NaN where the formula gives Inf or NaN, and nothing elsewhere.
- * |scale| < 2e38.
+ * |scale| < 2e38. Over an int8 cache the sum over d is one of q with codes, divided by k's scale after
+ * it, so that |q| of 2^114 and more may overflow.
  */
 size_t bitnet_paged_attention_workspace_size(const bitnet_cache* cache, int64_t B,
                                              int64_t heads);

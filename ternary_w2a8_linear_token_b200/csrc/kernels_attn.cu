@@ -24,7 +24,6 @@
 // the CTA's share, the four states are joined in shared memory, and the result goes out, or into
 // the workspace if other CTAs hold parts of the item. A second kernel joins those, in order.
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <type_traits>
@@ -204,31 +203,13 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                        uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// Signed bytes 0 and 2 of w (odd: 1 and 3), sign bits turned before, as an fp16 pair, exactly: the
-// byte under the exponent of 1024 reads 1024 + 128 + q.
-__device__ __forceinline__ uint32_t bytes_to_f16(uint32_t turned, bool odd) {
-    uint32_t q;
-    asm("add.rn.f16x2 %0, %1, %2;"
-        : "=r"(q)
-        : "r"(__byte_perm(turned, 0x64646464u, odd ? 0x4341 : 0x4240)),
-          "r"(0xE480E480u));  // - 1152
-    return q;
-}
-
 // Signed bytes 0 and 2 of w (odd: 1 and 3) as a bf16 pair, exactly: 128 + the low seven bits, less
 // 128, or 256 for a negative byte (its sign bit is then the exponent's lowest). Two logic and one
 // half-precision instruction for two values, the logic written out, since from C the compiler makes
-// two of each; a form with one and three took 120 µs where this takes 115 (8 sequences of up to
-// 65536 tokens, 32 heads over 8).
+// two of each; for V a form with one and three took 5 µs more (8 sequences of up to 65536 tokens, 32
+// heads over 8). bf16 takes q as it is; K in fp16, with one permutation and one addition a pair, needs
+// q scaled into fp16's range, where a head's small values lose bits, and took 127 µs where this takes
+// 132 (16 sequences of 30000 over 2 heads: 93 and 91).
 __device__ __forceinline__ uint32_t bytes_to_bf16(uint32_t w, bool odd) {
     if (odd) w >>= 8;
     uint32_t v, o, q;
@@ -445,9 +426,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8, NH>::kCtas)
     const int g = lane >> 2, cq = lane & 3;
     uint32_t q[NH][D / 16][2];
     // o[h][i][e], m[h][e & 1], l[h][e & 1]: head 8 h + 2 cq + (e & 1), dimension dim_of(i, e >> 1).
-    // m is the maximum that the sums stand on, which may lag behind by kLag (below). qx: in 8 bits
-    // the power of two that q was divided by to fit fp16.
-    float o[NH][D / 16][4], m[NH][2], l[NH][2], qx[NH][2];
+    // m is the maximum that the sums stand on, which may lag behind by kLag (below).
+    float o[NH][D / 16][4], m[NH][2], l[NH][2];
     auto dim_of = [&](int i, int half) { return 16 * i + (I8 ? 2 * g + half : g + 8 * half); };
     bool fresh = true;  // an item begins
     int stage = 0, rows = 0, head0 = 0;
@@ -462,7 +442,6 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8, NH>::kCtas)
 #pragma unroll
             for (int h = 0; h < NH; ++h) {
                 const int r = 8 * h + g;
-                float amax = 0.0f;
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
                     uint2 w = make_uint2(0, 0);
@@ -474,31 +453,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8, NH>::kCtas)
                             w = make_uint2(*reinterpret_cast<const uint32_t*>(at + 2 * cq),
                                            *reinterpret_cast<const uint32_t*>(at + 8 + 2 * cq));
                     }
-                    q[h][ks][0] = w.x;
-                    q[h][ks][1] = w.y;
-                    if (I8)
-                        amax = fmaxf(amax, fmaxf(fmaxf(fabsf(bf16_lo(w.x)), fabsf(bf16_hi(w.x))),
-                                                 fmaxf(fabsf(bf16_lo(w.y)), fabsf(bf16_hi(w.y)))));
-                }
-                if (I8) {
-                    // fp16 holds q exactly once its largest value is in [1, 2): smaller ones lose
-                    // bits only below 2^-24 of it. Pairs go in the order of the unpacked bytes.
-                    amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-                    amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-                    const int ex = min(max(int(__float_as_uint(amax) >> 23), 1), 253);
-                    const float down = __uint_as_float(uint32_t(254 - ex) << 23);
-                    const float up = __uint_as_float(uint32_t(ex) << 23);
-#pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks) {
-                        const uint32_t x = q[h][ks][0], y = q[h][ks][1];
-                        const __half2 a = __floats2half2_rn(bf16_lo(x) * down, bf16_lo(y) * down);
-                        const __half2 b = __floats2half2_rn(bf16_hi(x) * down, bf16_hi(y) * down);
-                        q[h][ks][0] = *reinterpret_cast<const uint32_t*>(&a);
-                        q[h][ks][1] = *reinterpret_cast<const uint32_t*>(&b);
-                    }
-                    // this lane's columns are heads 2 cq and 2 cq + 1, held by lanes 8 cq and + 4
-                    qx[h][0] = __shfl_sync(0xFFFFFFFFu, up, 8 * cq);
-                    qx[h][1] = __shfl_sync(0xFFFFFFFFu, up, 8 * cq + 4);
+                    // in 8 bits pairs go in the order of the unpacked bytes
+                    q[h][ks][0] = I8 ? __byte_perm(w.x, w.y, 0x5410) : w.x;
+                    q[h][ks][1] = I8 ? __byte_perm(w.x, w.y, 0x7632) : w.y;
                 }
                 m[h][0] = m[h][1] = -INFINITY;
                 l[h][0] = l[h][1] = 0.0f;
@@ -546,13 +503,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8, NH>::kCtas)
                         ldmatrix4(r, kt + tile_at<RB>(16 * t + lrow, ks + lch));
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            const uint32_t x = r[2 * k] ^ 0x80808080u;
-                            const uint32_t y = r[2 * k + 1] ^ 0x80808080u;
-                            const uint32_t a[4] = {bytes_to_f16(x, false), bytes_to_f16(y, false),
-                                                   bytes_to_f16(x, true), bytes_to_f16(y, true)};
+                            const uint32_t x = r[2 * k], y = r[2 * k + 1];
+                            const uint32_t a[4] = {bytes_to_bf16(x, false), bytes_to_bf16(y, false),
+                                                   bytes_to_bf16(x, true), bytes_to_bf16(y, true)};
 #pragma unroll
                             for (int h = 0; h < NH; ++h)
-                                mma_f16(z[h][t], a, q[h][ks + k][0], q[h][ks + k][1]);
+                                mma_bf16(z[h][t], a, q[h][ks + k][0], q[h][ks + k][1]);
                         }
                     }
             } else {
@@ -576,15 +532,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8, NH>::kCtas)
                     f[t][half] = I8 ? scales[16 * t + 8 * half + g] : sc;
                     if (I8) vs[t][half] = scales[T + 16 * t + 8 * half + g];
                 }
-            auto score = [&](int h, int t, int x) {
-                return I8 ? z[h][t][x] * (f[t][x >> 1] * qx[h][x & 1]) : z[h][t][x] * sc;
-            };
 #pragma unroll
             for (int h = 0; h < NH; ++h)
 #pragma unroll
                 for (int t = 0; t < MT; ++t)
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) w[h][t][x] = score(h, t, x);
+                    for (int x = 0; x < 4; ++x) w[h][t][x] = z[h][t][x] * f[t][x >> 1];
             if (mask != kAll) {
 #pragma unroll
                 for (int t = 0; t < MT; ++t)

@@ -537,3 +537,23 @@ def test_weights_keep_all_their_bits(bn, dtype):
     err = np.abs(out - want)
     assert np.all(err <= tol), f"{np.max(err / tol):.2f} of the tolerance"
     assert np.median(np.abs(want) / tol) > 4  # (what cancels is large beside it)
+
+
+@pytest.mark.parametrize("far", [8, 20, 60, 100])
+@pytest.mark.parametrize("kv,group", [(2, 4), (1, 12)])
+def test_queries_of_a_wide_range_over_8_bits(bn, kv, group, far):
+    """Small values of q count in full beside one 2^far times as large that meets codes of zero, and
+    beside one that meets others."""
+    cache = _fill(bn, [40, 700], kv, 64, 16, torch.int8)
+    q = (_q(2, kv * group, 64).float() * 2.0 ** -far).to(torch.bfloat16)
+    q[:, :, 5] = 1.0
+    q[1, 0, 9] = 0.0
+    for layer in cache.layers:
+        layer[0][..., 5] = 0
+    scale = 0.125 * 2.0 ** far
+    _check(cache, q, *bn.bitnet_paged_attention(q, cache, scale=scale, return_lse=True),
+           scale=scale)
+    q[:, :, 5] *= 2.0 ** (3 - far)
+    cache.layers[0][0][..., 5] = -3
+    _check(cache, q, *bn.bitnet_paged_attention(q, cache, scale=scale, return_lse=True),
+           scale=scale)
