@@ -547,9 +547,9 @@ def bitnet_linear_b3(x: torch.Tensor, packed_b3: torch.Tensor, s_w: torch.Tensor
 # ----------------------------------------------------------------------------- decode step
 # The operators of a decode step beside the ternary projections. They run on the device of their
 # tensors, whichever is current. With `stream` given, what a call allocates belongs to that stream (no
-# pending work of the current one can still be using it), and no tensor of a call is reused before
-# both streams are done with it. A call's host time is that of a decode step's, so the checks are
-# few and flat.
+# pending work of the current one can still be using it), and no tensor of a call, the cache's own
+# among them, is reused before both streams are done with it. A call's host time is that of a decode
+# step's, so the checks are few and flat.
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(
     torch._C, "_cuda_getCurrentRawStream") else (
     lambda i: torch.cuda.current_stream(i).cuda_stream)
@@ -707,6 +707,9 @@ class PagedCache:
                 c_layer.k_scale, c_layer.v_scale = (_on(t, torch.float32, dev, "scale")
                                                     for t in scales)
         self._layer_refs = [ctypes.byref(c_layer) for c_layer in self._layers]
+        self._tensors = [table, lens, refs, error] + [t for layer in self.layers for t in layer
+                                                      if t is not None]
+        self._streams = set()  # those that calls were given: see _keep
         self._c = bitnet_cache(_on(table, torch.int32, dev, "table"),
                                _on(lens, torch.int32, dev, "lens"),
                                _on(refs, torch.int32, dev, "refs"),
@@ -721,6 +724,15 @@ class PagedCache:
         if not 0 <= i < len(self.layers):
             raise IndexError(f"layer {i} of {len(self.layers)}")
         return self._layer_refs[i]
+
+    def _keep(self, stream: torch.cuda.Stream, *tensors):
+        """Neither the cache's tensors nor these are to be reused before `stream` is done with them.
+        The cache's are told once per stream: what the allocator notes of a tensor holds until it is
+        freed, and covers what the stream was given until then."""
+        if stream.cuda_stream not in self._streams:
+            _keep(stream, *self._tensors)
+            self._streams.add(stream.cuda_stream)
+        _keep(stream, *tensors)
 
     def workspace_size(self, n: int) -> int:
         """Bytes of scratch for upkeep calls on lists of n slots."""
@@ -811,7 +823,7 @@ def bitnet_cache_fork(cache: PagedCache, src: torch.Tensor, dst: torch.Tensor,
     if st:
         _check(st, "bitnet_cache_fork")
     if stream is not None:
-        _keep(stream, src, dst, ws)
+        cache._keep(stream, src, dst, ws)
 
 
 def bitnet_cache_extend(cache: PagedCache, seqs: torch.Tensor, add: torch.Tensor,
@@ -830,7 +842,7 @@ def bitnet_cache_extend(cache: PagedCache, seqs: torch.Tensor, add: torch.Tensor
     if st:
         _check(st, "bitnet_cache_extend")
     if stream is not None:
-        _keep(stream, seqs, add, copies, ws)
+        cache._keep(stream, seqs, add, copies, ws)
     return copies
 
 
@@ -846,7 +858,7 @@ def bitnet_cache_free(cache: PagedCache, seqs: torch.Tensor,
     if st:
         _check(st, "bitnet_cache_free")
     if stream is not None:
-        _keep(stream, seqs, ws)
+        cache._keep(stream, seqs, ws)
 
 
 def bitnet_cache_compact(cache: PagedCache, copies: Optional[torch.Tensor] = None,
@@ -863,7 +875,7 @@ def bitnet_cache_compact(cache: PagedCache, copies: Optional[torch.Tensor] = Non
     if st:
         _check(st, "bitnet_cache_compact")
     if stream is not None:
-        _keep(stream, copies, ws)
+        cache._keep(stream, copies, ws)
     return copies
 
 
@@ -881,7 +893,7 @@ def bitnet_cache_copy(cache: PagedCache, copies: torch.Tensor, stream=None) -> N
     if st:
         _check(st, "bitnet_cache_copy")
     if stream is not None:
-        _keep(stream, copies)
+        cache._keep(stream, copies)
 
 
 def bitnet_cache_append(cache: PagedCache, layer: int, k: torch.Tensor, v: torch.Tensor,
@@ -906,7 +918,7 @@ def bitnet_cache_append(cache: PagedCache, layer: int, k: torch.Tensor, v: torch
     if st:
         _check(st, "bitnet_cache_append")
     if stream is not None:
-        _keep(stream, k, v, seqs, pos)
+        cache._keep(stream, k, v, seqs, pos)
 
 
 def bitnet_paged_attention(q: torch.Tensor, cache: PagedCache, layer: int = 0,
@@ -957,7 +969,7 @@ def bitnet_paged_attention(q: torch.Tensor, cache: PagedCache, layer: int = 0,
     if st:
         _check(st, "bitnet_paged_attention")
     if stream is not None:
-        _keep(stream, q, seqs, out, lse, ws)
+        cache._keep(stream, q, seqs, out, lse, ws)
     return out if lse is None else (out, lse)
 
 

@@ -328,3 +328,55 @@ def test_long_rows(bn):
     assert ref.pairs(bn.bitnet_cache_compact(cache)) == m.compact()
     m.check(cache)
     assert cache.errors() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.int8])
+@pytest.mark.parametrize("what", ["append", "attention", "copy", "extend", "fork", "free", "compact"])
+def test_a_dropped_cache_lives_until_the_given_stream_is_done(bn, what, dtype):
+    """A cache that is dropped behind a call on a side stream that has yet to run it: none of its
+    memory is handed out before, neither its pools nor its tables, so the call neither reads nor writes
+    what others put there."""
+    side = torch.cuda.Stream()
+    kv, D = 2, 64
+    x = torch.ones(2, kv, D, dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros(2, kv, D, dtype=torch.bfloat16, device="cuda")
+    slots, one, more = _dev([0, 1]), _dev([1, 1]), _dev([2, 3])
+    copies = _dev([1, 0, 0, 9])
+    calls = {
+        "append": lambda c: bn.bitnet_cache_append(c, 1, x, x, slots, stream=side),
+        "attention": lambda c: bn.bitnet_paged_attention(q, c, 1, slots, stream=side),
+        "copy": lambda c: bn.bitnet_cache_copy(c, copies, stream=side),
+        "extend": lambda c: bn.bitnet_cache_extend(c, slots, one, stream=side),
+        "fork": lambda c: bn.bitnet_cache_fork(c, slots, more, stream=side),
+        "free": lambda c: bn.bitnet_cache_free(c, slots, stream=side),
+        "compact": lambda c: bn.bitnet_cache_compact(c, stream=side),
+    }
+
+    def new():
+        return bn.make_cache(20, 4, 3, kv, D, 16, 2, dtype)
+
+    for _ in range(2):
+        cache = new()
+        bn.bitnet_cache_extend(cache, slots, _dev([20, 5]))
+        bn.bitnet_cache_append(cache, 1, x, x, slots)
+        want = bn.bitnet_paged_attention(q, cache, 1, slots)
+        mine = cache.layers + [(cache.table, cache.lens, cache.refs, cache.error)]
+        mine = {t.data_ptr(): t.numel() * t.element_size() for ts in mine for t in ts}
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+        got = calls[what](cache)
+        del cache
+        others = [new() for _ in range(2)]
+        theirs = [t for c in others for ts in c.layers + [(c.table, c.lens, c.refs, c.error)]
+                  for t in ts]
+        assert not side.query()
+        for t in theirs:
+            at, size = t.data_ptr(), t.numel() * t.element_size()
+            assert all(at + size <= p or p + n <= at for p, n in mine.items())
+        before = [t.clone() for t in theirs]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(theirs, before))
+        if what == "attention":
+            assert torch.equal(got, want)
+        del others, theirs, before, got
