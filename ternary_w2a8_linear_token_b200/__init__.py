@@ -750,10 +750,14 @@ class PagedCache:
         return size
 
     def errors(self) -> int:
-        """Reads and clears the error word (synchronises)."""
+        """Reads and clears the error word, once the device has done all that it was given before, on
+        whichever stream. No other thread may make calls on the cache meanwhile: a bit that one sets
+        between the reading and the clearing would be lost."""
+        torch.cuda.synchronize(self.device)
         e = int(self.error.item())
         if e:
             self.error.zero_()
+            torch.cuda.current_stream(self.device).synchronize()  # cleared before other streams go on
         return e
 
 

@@ -380,3 +380,33 @@ def test_a_dropped_cache_lives_until_the_given_stream_is_done(bn, what, dtype):
         if what == "attention":
             assert torch.equal(got, want)
         del others, theirs, before, got
+
+
+def test_errors_waits_for_every_stream(bn):
+    """What a call on another stream reports is there as soon as the call has been made: one that named
+    the stream, one that ran under it, a replayed graph; and it is cleared before later calls set it."""
+    cache, _ = _make(bn, 8, 3, 2, 16)
+    side, bad = torch.cuda.Stream(), _dev([1, 1])
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        bn.bitnet_cache_free(cache, bad)
+
+    def under():
+        with torch.cuda.stream(side):
+            bn.bitnet_cache_free(cache, bad)
+
+    def replayed():
+        with torch.cuda.stream(side):
+            graph.replay()
+
+    bn.bitnet_cache_free(cache, bad, stream=side)
+    assert cache.errors() == bn.CACHE_ERR_SEQ
+    for call in (lambda: bn.bitnet_cache_free(cache, bad, stream=side), under, replayed):
+        for _ in range(3):
+            with torch.cuda.stream(side):
+                torch.cuda._sleep(20_000_000)
+            call()
+            assert cache.errors() == bn.CACHE_ERR_SEQ
+            call()  # at once behind the clearing
+            assert cache.errors() == bn.CACHE_ERR_SEQ and cache.errors() == 0
