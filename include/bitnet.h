@@ -509,7 +509,8 @@ bitnet_status bitnet_cache_copy(const bitnet_cache* cache, const bitnet_cache_la
  *         bitnet_cache_extend has counted it). A position outside [0, lens) is reported
  *         (BITNET_CACHE_ERR_LEN) and the token skipped.
  *   BITNET_CACHE_I8: per token and head scale = 127 / max(max |x|, 1e-5), q = rint(x * scale), the
- *   arithmetic of bitnet_quant_act. No two tokens may have one slot and position.
+ *   arithmetic of bitnet_quant_act; where a token's K or V of a head holds an Inf or NaN, its scale is
+ *   NaN and q says nothing, so that attention shows it. No two tokens may have one slot and position.
  */
 bitnet_status bitnet_cache_append(const bitnet_cache* cache, const bitnet_cache_layer* layer,
                                   const uint16_t* k, const uint16_t* v, int64_t T,

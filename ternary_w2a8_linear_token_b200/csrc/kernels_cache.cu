@@ -621,10 +621,13 @@ __global__ void __launch_bounds__(kApplyThreads) append_kernel(CacheView c, bitn
                 reinterpret_cast<uint4*>(is_v ? lay.v : lay.k)[to * kLanes + piece] = x[u];
                 continue;
             }
-            // bf16 magnitudes order as unsigned integers: an exact maximum over the row's lanes.
+            // bf16 magnitudes order as unsigned integers, Inf and NaN behind the others: an exact
+            // maximum over the row's lanes. A row with either gets NaN as its scale.
             const uint32_t lanes = ((1u << kLanes) - 1) << (threadIdx.x & 31 & ~(kLanes - 1));
-            const float amax = bf16_lo(__reduce_max_sync(lanes, absmax8_bits(x[u])));
-            const float scale = __fdiv_rn(127.0f, fmaxf(amax, kActEps));
+            const uint32_t top = __reduce_max_sync(lanes, absmax8_bits(x[u]));
+            const float amax = top < 0x7F80u ? fmaxf(bf16_lo(top), kActEps)
+                                             : __uint_as_float(0x7FC00000u);
+            const float scale = __fdiv_rn(127.0f, amax);
             reinterpret_cast<uint2*>(is_v ? lay.v : lay.k)[to * kLanes + piece] =
                 quant8(x[u], scale);
             if (piece == 0) (is_v ? lay.v_scale : lay.k_scale)[to] = scale;

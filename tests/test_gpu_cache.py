@@ -410,3 +410,33 @@ def test_errors_waits_for_every_stream(bn):
             assert cache.errors() == bn.CACHE_ERR_SEQ
             call()  # at once behind the clearing
             assert cache.errors() == bn.CACHE_ERR_SEQ and cache.errors() == 0
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("w", [0, 1])
+@pytest.mark.parametrize("D", [64, 128])
+def test_inf_and_nan_show_in_8_bits(bn, D, w, value):
+    """One Inf or NaN in K or V of one token and head: that row's scale is NaN, every other row is as
+    without it, and attention gives NaN for the query heads that see it, and what it gave for the
+    others."""
+    g = np.random.default_rng([D, w])
+    x = [ref.bf16(g.standard_normal((30, 3, D))).cuda() for _ in range(2)]
+    seqs, pos = _dev([0] * 17 + [1] * 13), _dev(list(range(17)) + list(range(13)))
+    q = ref.bf16(g.standard_normal((2, 6, D))).cuda()
+    got = []
+    for bad in (False, True):
+        cache, _ = _make(bn, 8, 2, 4, 16, dtype=torch.int8, kv=3, D=D)
+        bn.bitnet_cache_extend(cache, _dev([0, 1]), _dev([17, 13]))
+        if bad:
+            x[w][20, 1, D - 9] = value  # position 3 of slot 1
+        bn.bitnet_cache_append(cache, 0, *x, seqs, pos)
+        got.append((cache.layers[0], bn.bitnet_paged_attention(q, cache, return_lse=True)))
+        page = int(cache.table[1, 0])
+        assert cache.errors() == 0
+    (clean, (o, l)), (layer, (ob, lb)) = got
+    assert torch.isnan(layer[2 + w][page, 1, 3])
+    layer[2 + w][page, 1, 3], layer[w][page, 1, 3] = clean[2 + w][page, 1, 3], clean[w][page, 1, 3]
+    assert all(torch.equal(a, b) for a, b in zip(layer, clean))
+    assert ob[1, 2:4].isnan().all() and bool(lb[1, 2:4].isnan().all()) == (w == 0)
+    ob[1, 2:4], lb[1, 2:4] = o[1, 2:4], l[1, 2:4]
+    assert torch.equal(ob, o) and torch.equal(lb, l)
