@@ -43,6 +43,8 @@ constexpr int kMinUnits = 2;      // fewest units that are worth a CTA of their 
 constexpr int kJoinThreads = 128;
 constexpr int kTerms = 3;     // bf16 terms of a weight: 24 bits, all that binary32 has
 constexpr float kLag = 8.0f;  // powers of two that weights may exceed 1 by
+// The maximum of scores that were all -inf or NaN: -inf itself stands for no visible token.
+constexpr float kLowest = -3.402823466e38f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // A unit is kTile tokens for each warp: 16 of 256 bytes (a row of K or V), 32 of 128 or 64, so
@@ -554,6 +556,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8, NH>::kCtas)
 #pragma unroll
             for (int h = 0; h < NH; ++h)
 #pragma unroll
+                for (int e = 0; e < 2; ++e) m[h][e] = fmaxf(m[h][e], kLowest);
+#pragma unroll
+            for (int h = 0; h < NH; ++h)
+#pragma unroll
                 for (int t = 0; t < MT; ++t)
 #pragma unroll
                     for (int x = 0; x < 4; ++x) grown |= w[h][t][x] > m[h][x & 1] + kLag;
@@ -571,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8, NH>::kCtas)
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1)
                             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-                        const float keep = exp2_fast(m[h][e] - (top == -INFINITY ? 0.0f : top));
+                        const float keep = exp2_fast(m[h][e] - top);
                         m[h][e] = top;
                         l[h][e] *= keep;
 #pragma unroll
@@ -585,13 +591,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8, NH>::kCtas)
             for (int h = 0; h < NH; ++h)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float base = m[h][e] == -INFINITY ? 0.0f : m[h][e];
 #pragma unroll
                     for (int t = 0; t < MT; ++t)
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
                             const int x = 2 * half + e;
-                            w[h][t][x] = exp2_fast(w[h][t][x] - base);
+                            w[h][t][x] = exp2_fast(w[h][t][x] - m[h][e]);
                             l[h][e] += w[h][t][x];
                         }
                 }
@@ -700,14 +705,15 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8, NH>::kCtas)
 #pragma unroll
                     for (int w = 0; w < kWarps; ++w) v += buf[(w * rows + r) * piece + d];
                     if (whole) {
-                        float t = 0.0f, b = fmaxf(fmaxf(sh.m[0][r], sh.m[1][r]),
-                                                  fmaxf(sh.m[2][r], sh.m[3][r]));
-                        b = b == -INFINITY ? 0.0f : b;
+                        float t = 0.0f;
+                        const float b = fmaxf(fmaxf(sh.m[0][r], sh.m[1][r]),
+                                              fmaxf(sh.m[2][r], sh.m[3][r]));
 #pragma unroll
                         for (int w = 0; w < kWarps; ++w)
                             t += sh.l[w][r] * exp2_fast(sh.m[w][r] - b);
                         p.out[(int64_t(cur.b) * p.heads + head0 + r) * D + d0 + d] =
-                            __bfloat16_as_ushort(__float2bfloat16_rn(t == 0.0f ? 0.0f : v / t));
+                            __bfloat16_as_ushort(
+                                __float2bfloat16_rn(b == -INFINITY ? 0.0f : v / t));
                     } else {
                         part[r * D + d0 + d] = v;
                     }
@@ -728,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8, NH>::kCtas)
                     part[kRows * D + kRows + r] = t;
                 } else if (p.lse) {
                     p.lse[int64_t(cur.b) * p.heads + head0 + r] =
-                        t == 0.0f ? -INFINITY : (b + log2f(t)) * kLn2;
+                        b == -INFINITY ? -INFINITY : (b + log2f(t)) * kLn2;
                 }
             }
             __syncthreads();
@@ -814,13 +820,13 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
         o.z += v.z * f;
         o.w += v.w * f;
     }
-    const float scale = total == 0.0f ? 0.0f : 1.0f / total;  // (a NaN stays one)
+    const float scale = top == -INFINITY ? 0.0f : 1.0f / total;  // (of no visible token: o is 0)
     const int64_t row = int64_t(note.b) * p.heads + note.head0 + r;
     const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * scale, o.y * scale);
     const __nv_bfloat162 hi = __floats2bfloat162_rn(o.z * scale, o.w * scale);
     *reinterpret_cast<uint2*>(p.out + row * D + 4 * d) =
         make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-    if (p.lse && d == 0) p.lse[row] = total == 0.0f ? -INFINITY : (top + log2f(total)) * kLn2;
+    if (p.lse && d == 0) p.lse[row] = top == -INFINITY ? -INFINITY : (top + log2f(total)) * kLn2;
 }
 
 template <int D, bool I8, int NH>

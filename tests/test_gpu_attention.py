@@ -557,3 +557,51 @@ def test_queries_of_a_wide_range_over_8_bits(bn, kv, group, far):
     cache.layers[0][0][..., 5] = -3
     _check(cache, q, *bn.bitnet_paged_attention(q, cache, scale=scale, return_lse=True),
            scale=scale)
+
+
+@pytest.mark.parametrize("D,kv,group", [(64, 2, 4), (128, 1, 12)])
+def test_scores_of_minus_infinity(bn, D, kv, group):
+    """Inf in K against a q of the other sign. All visible scores -inf: out is the formula's 0 / 0 and
+    lse its log 0, in an item of one CTA, one that several share, and a window of one token; with a
+    q of the same sign NaN in both. Where some scores are finite, attention over their tokens alone.
+    Without a visible token (no tokens, or only pages outside the pool) out stays 0."""
+    lens = [1, 40, 5000, 5000, 17, 0, 33]
+    cache = _fill(bn, lens, kv, D, 16, torch.bfloat16)
+    k = cache.layers[0][0]
+    q = _q(len(lens), kv * group, D)
+    q[..., 3] = torch.where(torch.arange(kv * group, device="cuda") % 2 == 1, 0.5, -0.5)
+
+    def pages(s, n):
+        return cache.table[s, :n].long()
+
+    for s in (0, 1, 2):
+        k[pages(s, -(-lens[s] // 16)), :, :, 3] = float("inf")
+    k[pages(3, 200), :, :, 3] = float("inf")  # 3200 of 5000 tokens
+    k[pages(4, 1), :, :, 3] = float("-inf")  # 16 of 17
+    cache.table[6, :3] = -1
+    down = torch.arange(kv * group, device="cuda") % 2 == 0
+    out, lse = bn.bitnet_paged_attention(q, cache, return_lse=True)
+    assert cache.errors() == bn.CACHE_ERR_PAGE
+    assert out[:3].isnan().all()
+    assert torch.all(lse[:3, down] == -np.inf) and lse[:3, ~down].isnan().all()
+    assert not out[5:].any() and torch.all(lse[5:] == -np.inf)
+    for s, first, heads in ((3, 3200, down), (4, 16, ~down)):
+        assert out[s, ~heads].isnan().all() and lse[s, ~heads].isnan().all()
+        kk, vv = _tokens(cache, 0, s, lens[s])
+        o, l, to, tl = ref.attention(q[s].double().cpu().numpy(), kk[first:], vv[first:], D ** -0.5)
+        h = heads.cpu().numpy()
+        tol = to + ref.BF16_HALF * (np.abs(o) + to)
+        assert np.all(np.abs(out[s].double().cpu().numpy() - o)[h] <= tol[h])
+        assert np.all(np.abs(lse[s].double().cpu().numpy() - l)[h] <= tl[h])
+    one, lse1 = bn.bitnet_paged_attention(q[1:3], cache, seqs=_dev([1, 2]), window=1,
+                                          return_lse=True)
+    assert one.isnan().all() and torch.all(lse1[:, down] == -np.inf)
+
+
+def test_scores_that_overflow(bn):
+    """Finite values whose scores pass binary32's range downwards are not taken for no token at all."""
+    cache = _fill(bn, [3, 900], 1, 64, 16, torch.bfloat16)
+    cache.layers[0][0].fill_(1e30)
+    q = torch.full((2, 2, 64), -1e30, dtype=torch.bfloat16, device="cuda")
+    out, lse = bn.bitnet_paged_attention(q, cache, return_lse=True)
+    assert out.isnan().all() and torch.all(lse == -np.inf)
