@@ -381,8 +381,10 @@ bitnet_status bitnet_linear_b3(const uint16_t* x, int64_t M, int64_t K, const ui
  *   exact.
  *   A row of x that holds an Inf or NaN gives unspecified values in that row of y only.
  *   Rows of up to BITNET_W4_MAX_GROUPS groups (BITNET_ERR_UNSUPPORTED beyond). Under programmatic
- *   dependent launch the weights are read before the previous kernel of the stream has ended: a
- *   kernel that writes them must not let its successors start early.
+ *   dependent launch the weights and scales are read before the previous kernels of the stream have
+ *   ended. bitnet_pack_w4 may come directly before this call; behind any other kernel that writes
+ *   them a kernel launched without that attribute, a copy or a memset has to come first (most calls
+ *   of this library are launched with it).
  * x, packed, W and y 16-byte aligned, scales 2-byte aligned. No workspace. Asynchronous on
  * `stream`; argument errors as for the other calls.
  */

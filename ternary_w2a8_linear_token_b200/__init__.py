@@ -622,7 +622,9 @@ def bitnet_pack_w4(W: torch.Tensor, group: int = 128, stream=None):
 def bitnet_linear_w4(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, group: int,
                      out_dtype: torch.dtype = torch.bfloat16, y: Optional[torch.Tensor] = None,
                      stream=None) -> torch.Tensor:
-    """y (M, N) = x (M, K) bf16 times 4-bit weights with group scales (bitnet_pack_w4)."""
+    """y (M, N) = x (M, K) bf16 times 4-bit weights with group scales (bitnet_pack_w4). Behind a kernel
+    other than bitnet_pack_w4 that changes weights or scales (not a copy), another torch kernel has to
+    come first: the call reads them before its predecessor has ended."""
     M, K = x.shape
     if group not in (32, 64, 128):
         raise ValueError(f"group must be 32, 64 or 128, got {group}")

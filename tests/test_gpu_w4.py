@@ -231,3 +231,27 @@ def test_large_layers_nan_stays_in_its_row(bn):
             assert z[1].isnan().all()
             keep = [m for m in range(M) if m != 1]
             assert torch.equal(z[keep], y[keep])
+
+
+@pytest.mark.parametrize("M,N,K,group", [(1, 640, 2560, 128), (2, 2560, 6912, 64),
+                                         (8, 10000, 1024, 32), (3, 96, 32768, 32)])
+def test_packed_anew_and_used_at_once(bn, M, N, K, group):
+    """Weights packed into the buffers that the calls before have read, and multiplied by the next call
+    of the stream: the results are those of weights that were there long before."""
+    g = torch.Generator(device="cuda").manual_seed(N)
+    Ws = [torch.randn(N, K, generator=g, device="cuda") * 2.0 ** i for i in range(3)]
+    x = torch.randn(M, K, generator=g, device="cuda").to(torch.bfloat16)
+    want = []
+    for W in Ws:
+        packed, scales = bn.bitnet_pack_w4(W, group)
+        torch.cuda.synchronize()
+        want.append(bn.bitnet_linear_w4(x, packed, scales, group, out_dtype=torch.float32))
+    stream = torch.cuda.current_stream().cuda_stream
+    got = []
+    for i in range(30):
+        assert bn.lib.bitnet_pack_w4(Ws[i % 3].data_ptr(), N, K, group, packed.data_ptr(),
+                                     scales.data_ptr(), stream) == bn.OK
+        got.append([bn.bitnet_linear_w4(x, packed, scales, group, out_dtype=torch.float32)
+                    for _ in range(2)])
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want[i % 3]) for i, ys in enumerate(got) for y in ys)
