@@ -72,10 +72,12 @@ __global__ void w4_packed_kernel() {}
 //
 // In bf16 a word's eight weights cost eleven instructions to unpack, and instructions, not HBM, bound
 // large layers (131071 x 4096 at 68 % of the copy rate). Few tokens therefore go in bytes: x as
-// integers in units of 2^-28 of the largest value of a block (what smaller values lose is less than
-// binary32 sums of the block would), cut into four signed bytes, which take four of a product's
-// columns; eight weights are then three instructions, the sums of a group are exact in 32-bit
-// integers, and one subtraction makes a float of each (96 % there at one token).
+// 30-bit integers in units of 2^-28 of the largest value of a block, cut into four signed bytes, which
+// take four of a product's columns; eight weights are then three instructions, the sums of a group
+// are exact in 32-bit integers, and one subtraction makes a float of each (96 % there at one token).
+// Values below 2^-20 of the largest lose bits, each at most 2^-29 of the largest. Binary32 sums lose
+// as much where the largest value's product is among them, but nothing of the kind where its weight
+// is 0 or its group's scale far below the others': there this form is the less exact one.
 constexpr int kW4Most = 16;  // warps of a CTA, and of an SM
 constexpr int kW4Stages = 4;
 constexpr uint32_t kW4Room = 227 * 1024;  // shared memory of a CTA

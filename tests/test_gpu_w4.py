@@ -255,3 +255,43 @@ def test_packed_anew_and_used_at_once(bn, M, N, K, group):
                     for _ in range(2)])
     torch.cuda.synchronize()
     assert all(torch.equal(y, want[i % 3]) for i, ys in enumerate(got) for y in ys)
+
+
+@pytest.mark.parametrize("far", [4, 8, 14, 20, 26])
+@pytest.mark.parametrize("M,N,K,group", [(1, 28672, 2560, 128), (1, 6912, 2560, 32),
+                                         (2, 14336, 4096, 64), (3, 28672, 2560, 128),
+                                         (4, 131071, 576, 128)])
+def test_large_layers_low_digits(bn, M, N, K, group, far):
+    """The small values of a block are the whole result: its largest, 2^far times as large, meets codes
+    of t = 0. Up to 2^20 no bit of x is cut off, beyond it is off by 2^-29 of the largest of its block.
+    Sums within a group are exact, so beside that there is a binary32 step for each group, of sums
+    whose digits are up to four times the terms, and some for joining digits and warps."""
+    packed, t, scales = _large(N, K, group, 11)
+    at = torch.arange(0, K, 128, device="cuda") + 37  # one value of each block
+    words = packed.view(torch.int32).view(N, -1, 16)
+    # weight 37 = 32 * 1 + 8 * 0 + 5: word 1, bits 24 to 27
+    words[:, :, 1] = (words[:, :, 1] & ~(15 << 24)) | 8 << 24
+    t = t.clone()
+    t[:, at] = 0
+    g = torch.Generator(device="cuda").manual_seed(M)
+    small = torch.rand(M, K, generator=g, device="cuda") + 1
+    small *= torch.randint(0, 2, (M, K), generator=g, device="cuda") * 2 - 1
+    x = small * 2.0 ** -far
+    x[:, at] = 1.9921875 * (torch.randint(0, 2, (M, len(at)), generator=g, device="cuda") * 2 - 1)
+    x = x.to(torch.bfloat16)
+    w = t.double() * scales.double().repeat_interleave(group, 1)[:, :K]
+    xd = x.double()
+    want, size = xd @ w.T, xd.abs() @ w.abs().T
+    tol = 4 * (scales.shape[1] + 20) * ref.F32_STEP * size
+    if far > 20:
+        tol = tol + 2.0 ** -29 * 1.9921875 * w.abs().sum(1)
+    y = bn.bitnet_linear_w4(x, packed, scales, group, out_dtype=torch.float32)
+    err = (y.double() - want).abs()
+    assert torch.all(err <= tol), f"{(err / tol).max().item():.2f} of the tolerance"
+    # to the bit where nothing of x is cut off: one block, one group, one value
+    if group == 128:
+        x.zero_()
+        x[:, 37] = -1.9921875
+        x[:, 100] = 1.9921875 * 2.0 ** -21
+        y = bn.bitnet_linear_w4(x, packed, scales, group, out_dtype=torch.float32)
+        assert torch.equal(y, (x[:, 100:101].double() @ w[:, 100:101].T).float())
