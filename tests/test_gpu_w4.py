@@ -295,3 +295,37 @@ def test_large_layers_low_digits(bn, M, N, K, group, far):
         x[:, 100] = 1.9921875 * 2.0 ** -21
         y = bn.bitnet_linear_w4(x, packed, scales, group, out_dtype=torch.float32)
         assert torch.equal(y, (x[:, 100:101].double() @ w[:, 100:101].T).float())
+
+
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,N,K,group", [(17, 14336, 4096, 128), (35, 14336, 4096, 32),
+                                         (17, 2560, 16384, 64), (35, 2560, 16384, 128),
+                                         (100, 4736, 8192, 32), (33, 600, 60032, 64)])
+def test_large_layers_several_token_tiles(bn, M, N, K, group, out):
+    """More than 16 tokens of layers of more than 2^25 weights: passes of 16, the last cut; teams of four
+    and of eight; x through shared memory and L1."""
+    packed, t, scales = _large(N, K, group, N)
+    g = torch.Generator(device="cuda").manual_seed(M)
+    x = torch.randn(M, K, generator=g, device="cuda").to(torch.bfloat16)
+    y = bn.bitnet_linear_w4(x, packed, scales, group, out_dtype=out)
+    w = t.double() * scales.double().repeat_interleave(group, 1)[:, :K]
+    want, size = x.double() @ w.T, x.double().abs() @ w.abs().T
+    tol = (K + 2) * ref.F32_STEP * size
+    if out == torch.bfloat16:
+        tol = tol + ref.BF16_HALF * (want.abs() + tol)
+    err = (y.double() - want).abs()
+    assert torch.all(err <= tol), f"{(err / tol).max().item():.2f} of the tolerance"
+
+
+def test_more_tokens_than_one_launch(bn):
+    """65535 * 16 + 3 tokens: rows on both sides of the split, and nothing behind the last."""
+    M, N, K = 65535 * 16 + 3, 5, 64
+    packed, t, scales = _large(N, K, 64, 1)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn(M, K, generator=g, device="cuda").to(torch.bfloat16)
+    buf = torch.full((M * N + 64,), 7.0, device="cuda")
+    y = bn.bitnet_linear_w4(x, packed, scales, 64, y=buf[:M * N].view(M, N))
+    w = t.double() * scales.double().repeat_interleave(64, 1)[:, :K]
+    want, size = x.double() @ w.T, x.double().abs() @ w.abs().T
+    assert torch.all((y.double() - want).abs() <= (K + 2) * ref.F32_STEP * size)
+    assert torch.all(buf[M * N:] == 7.0)
