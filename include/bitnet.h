@@ -410,6 +410,9 @@ bitnet_status bitnet_linear_w4(const uint16_t* x, int64_t M, int64_t K, const ui
  * j % page_size; entries past its ceil(lens[s] / page_size) pages are not read. refs[p] counts
  * the slots that hold page p; the page is free while it is 0. A new cache has lens and refs 0.
  *
+ * Calls on one cache read and write the same memory, so the caller orders them: on one stream, or by
+ * events. Nothing may change the tables under a running call.
+ *
  * Device lists of slots (`seqs`, `src`, `dst`, int32) may be padded: an entry with a negative
  * slot is skipped. Every list must name a slot at most once where the call changes that slot.
  *

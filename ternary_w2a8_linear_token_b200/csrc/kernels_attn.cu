@@ -167,7 +167,8 @@ __device__ __forceinline__ void walk_enter(const AttnParams& p, const Shared& sh
     w.units = units_of<UNIT>(w.s);
 }
 
-// To the next unit; there must be one.
+// To the next unit; there must be one. (Where lengths change under the call there may be none: then
+// the last query's come again, so that nothing is reached out of range.)
 template <int UNIT>
 __device__ __forceinline__ void walk_next(const AttnParams& p, const Shared& sh, int blocks,
                                           Walk& w) {
@@ -178,9 +179,10 @@ __device__ __forceinline__ void walk_next(const AttnParams& p, const Shared& sh,
     if (++w.head < p.c.kv_heads) return;
     w.head = 0;
     do {
+        if (w.b >= p.B - 1) break;
         ++w.b;
         walk_enter<UNIT>(p, sh, w);
-    } while (w.units == 0 && w.b < p.B - 1);
+    } while (w.units == 0);
 }
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t a) {
@@ -322,7 +324,11 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8, NH>::kCtas)
             break;
         }
         before += all;
-        b0 += kThreads;  // (there is a sequence that holds u0)
+        b0 += kThreads;
+        if (b0 >= p.B) {  // no sequence holds u0: lengths have changed since the sum
+            if (threadIdx.x == 0) ws.note[blockIdx.x].b = -1;
+            return;
+        }
         const int64_t next = b0 + threadIdx.x;
         const Seen s = next < p.B ? seen_by(p, next, false) : Seen{-1, 0, 0};
         mine = units_of<UNIT>(s);
@@ -761,7 +767,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     const int64_t ctas = ws.head[0], units = ws.head[1];
     const Note note = ws.note[c0];  // (of a CTA without a share it says nothing)
     if (c0 >= ctas || note.b < 0 || r >= note.rows) return;
-    const int last = static_cast<int>(share_owner(units, ctas, note.end));
+    // (beyond the CTAs only where lengths have changed under the call)
+    const int last = static_cast<int>(min(share_owner(units, ctas, note.end), ctas - 1));
     const int grp = threadIdx.x / kLanes, d = threadIdx.x % kLanes;
     float top = -INFINITY, sum = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
