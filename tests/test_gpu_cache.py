@@ -355,7 +355,8 @@ def test_a_dropped_cache_lives_until_the_given_stream_is_done(bn, what, dtype):
     def new():
         return bn.make_cache(20, 4, 3, kv, D, 16, 2, dtype)
 
-    for _ in range(2):
+    seen = 0
+    for cycles in (20_000_000, 40_000_000, 400_000_000, 800_000_000):
         cache = new()
         bn.bitnet_cache_extend(cache, slots, _dev([20, 5]))
         bn.bitnet_cache_append(cache, 1, x, x, slots)
@@ -364,13 +365,16 @@ def test_a_dropped_cache_lives_until_the_given_stream_is_done(bn, what, dtype):
         mine = {t.data_ptr(): t.numel() * t.element_size() for ts in mine for t in ts}
         torch.cuda.synchronize()
         with torch.cuda.stream(side):
-            torch.cuda._sleep(20_000_000)
+            torch.cuda._sleep(cycles)
         got = calls[what](cache)
         del cache
         others = [new() for _ in range(2)]
         theirs = [t for c in others for ts in c.layers + [(c.table, c.lens, c.refs, c.error)]
                   for t in ts]
-        assert not side.query()
+        if side.query():  # the host was slower than that: longer
+            del others, theirs
+            continue
+        seen += 1
         for t in theirs:
             at, size = t.data_ptr(), t.numel() * t.element_size()
             assert all(at + size <= p or p + n <= at for p, n in mine.items())
@@ -380,6 +384,9 @@ def test_a_dropped_cache_lives_until_the_given_stream_is_done(bn, what, dtype):
         if what == "attention":
             assert torch.equal(got, want)
         del others, theirs, before, got
+        if seen == 2:
+            break
+    assert seen
 
 
 def test_errors_waits_for_every_stream(bn):
