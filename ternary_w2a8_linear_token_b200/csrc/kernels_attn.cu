@@ -59,7 +59,7 @@ struct Shape {
     static constexpr int kStageBytes = 2 * kPool + (I8 ? 2 * kTile * 4 : 0);
     // CTAs per SM and stages of the ring: a third CTA where registers allow, with two stages for
     // rows of 128 bytes (D = 64 in bf16, 64 sequences in a window of 4100 tokens: 3.5 µs less than
-    // with two CTAs of three stages; D = 128 in 8 bits, 8 sequences of up to 65536: 8 µs less).
+    // with two CTAs of three stages; D = 128 in 8 bits, 8 sequences of up to 65536: 6 µs less).
     static constexpr int kCtas = D == 64 || (I8 && NH == 1) ? 3 : 2;
     static constexpr int kStages = kCtas == 3 && kRowBytes == 128 ? 2 : 3;
     // Shared memory in which the warps' states are joined.

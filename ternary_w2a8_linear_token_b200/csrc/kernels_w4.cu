@@ -609,8 +609,9 @@ cudaError_t launch_w4_as(const W4Params& p, int teams, uint32_t smem, cudaStream
 }
 
 // x goes through shared memory where it fits (*fits): for eight warps on half an SM while a copy of
-// x for each half is small (one token of 14336 values, 4096 rows: 9.4 against 10.6 µs; 8 tokens of
-// 4096 values, 14336 rows: 12.3 against 11.7), for sixteen on all of it otherwise.
+// x for each half is small (one token: 2560 x 2560 2.9 µs, on whole SMs 3.7; 28672 x 4096 13.2 and 13.7),
+// for sixteen on all of it otherwise (14336 x 4096 at 8 tokens 10.7 µs, on halves 11.3; 4096 x 14336 at
+// one 8.6 and 9.4).
 template <int NT, int NG, int RT, W4X XM, int W>
 cudaError_t launch_w4(const W4Params& p, bool* fits, cudaStream_t stream) {
     constexpr int kTok = NT * w4_tokens(XM), kTeams = kW4Most / W;
